@@ -63,7 +63,8 @@ typedef enum {
   DS_ERR_CUDA = 4,        /* a CUDA runtime call failed (launch or query) */
   DS_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up */
   DS_ERR_BOUNDS = 6,      /* a token id read from device memory is outside [0, V) */
-  DS_ERR_NONFINITE = 7    /* a NaN or +inf logit, or a row with no finite logit */
+  DS_ERR_NONFINITE = 7,   /* a NaN or +inf logit, or a row with no finite logit */
+  DS_ERR_PAGES = 8        /* the cache has too few free pages (ds_cache.h) */
 } ds_status;
 
 typedef enum { DS_F32 = 0, DS_BF16 = 1 } ds_dtype;

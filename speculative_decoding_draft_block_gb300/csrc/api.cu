@@ -12,13 +12,7 @@
 
 using namespace ds;
 
-namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) == 0; }
+namespace ds {
 
 // The kernels are built for sm_103a only; refuse other devices up front.
 ds_status device_supported() {
@@ -42,6 +36,16 @@ ds_status device_supported() {
   }
   return cached[dev] ? DS_OK : DS_ERR_UNSUPPORTED;
 }
+
+}  // namespace ds
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) == 0; }
 
 bool shape_ok(int32_t B, int32_t K, int32_t V, int32_t r) {
   if (B < 1 || K < 1 || K > 64 || V < 8 || (V % 8) != 0) return false;
@@ -649,6 +653,7 @@ const char* ds_status_string(ds_status s) {
     case DS_ERR_TIMEOUT: return "device wait timed out";
     case DS_ERR_BOUNDS: return "token id out of range";
     case DS_ERR_NONFINITE: return "non-finite logit or empty distribution";
+    case DS_ERR_PAGES: return "too few free cache pages";
   }
   return "unknown status";
 }

@@ -33,7 +33,8 @@ enum DsStatusCode {
   kErrCuda = 4,
   kErrTimeout = 5,
   kErrBounds = 6,
-  kErrNonfinite = 7
+  kErrNonfinite = 7,
+  kErrPages = 8
 };
 
 __device__ __forceinline__ void report(int32_t* status, int code) {

@@ -186,6 +186,9 @@ cudaError_t launch_rnn_pack(const void* W_ih, const void* W_hh, int32_t r, int32
 bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
                       const cuuint64_t* strides, const cuuint32_t* box);
 
+// DS_OK on a device the kernels are built for (api.cu).
+ds_status device_supported();
+
 constexpr int kTileRows = 32;   // rows per sampling CTA
 constexpr int kTileCols = 256;  // tokens per sampling CTA (8 chunks of 32)
 

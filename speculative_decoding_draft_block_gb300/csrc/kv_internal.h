@@ -1,0 +1,106 @@
+// Internal types of the paged cache's kernels (kv_cache.cu, kv_pages.cu,
+// attn_*.cu); the contract of the entry points is in include/ds_cache.h.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ds_cache.h"
+
+namespace ds {
+
+// A pool as the kernels see it: byte strides, one layer's base or all layers'.
+struct PoolView {
+  char* k;
+  char* v;
+  int64_t layer_stride, page_stride, token_stride, head_stride;  // bytes
+  int32_t n_layers, n_pages, page_shift, n_kv_heads, row_bytes;  // row: head_dim elements
+};
+
+struct AppendParams {
+  PoolView pool;  // k, v of the layer
+  int32_t B, T, max_pages;
+  const char* k_new;
+  const char* v_new;
+  int64_t k_token, k_head, v_token, v_head;  // byte strides
+  const int32_t* q_start;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  int32_t* status;
+};
+
+struct AttnParams {
+  PoolView pool;  // k, v of the layer
+  int32_t dtype, D;
+  int32_t B, T, max_pages, max_q, n_heads, group;
+  int32_t causal, window;
+  float scale;
+  const char* q;
+  char* out;
+  int64_t q_token, q_head, o_token, o_head;  // byte strides
+  const int32_t* q_start;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  float* lse;
+  char* workspace;
+  int32_t* status;
+};
+
+struct UpdateParams {
+  PoolView pool;
+  int32_t B, max_pages;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* ref;
+  const int32_t* parent;
+  const int32_t* new_len;
+  int32_t* table_out;
+  int32_t* len_out;
+  int32_t* ref_out;
+  int32_t* ws;
+  int32_t* status;
+};
+
+struct CompactParams {
+  PoolView pool;
+  int32_t B, max_pages;
+  const int32_t* table;
+  const int32_t* ref;
+  int32_t* table_out;
+  int32_t* ref_out;
+  int32_t* page_map;
+  int32_t* n_used;
+  int32_t* ws;
+  int32_t* status;
+};
+
+// A request's new rows as every kernel reads them: rows q0 .. q0 + n - 1 of T,
+// row i at position kv - n + i. A malformed request has n = 0 and ok = false.
+struct Request {
+  int32_t q0, n, kv;
+  bool ok;
+};
+
+__device__ __forceinline__ Request load_request(const int32_t* q_start, const int32_t* kv_len, int32_t b,
+                                                int32_t T, int32_t max_q, int64_t cap) {
+  Request r;
+  r.q0 = __ldg(q_start + b);
+  const int32_t q1 = __ldg(q_start + b + 1);
+  r.kv = __ldg(kv_len + b);
+  r.n = q1 - r.q0;
+  r.ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= T && r.n <= max_q && r.kv >= 0 && (int64_t)r.kv <= cap;
+  if (!r.ok) r.n = 0;
+  return r;
+}
+
+constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are built for
+
+size_t update_ws_bytes(int32_t B, int32_t n_pages);
+size_t compact_ws_bytes(int32_t n_pages);
+size_t attention_ws_bytes(int32_t dtype, int32_t D);
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_update(const UpdateParams& p, cudaStream_t s);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t s);
+cudaError_t launch_attention_simt(const AttnParams& p, cudaStream_t s);
+
+}  // namespace ds

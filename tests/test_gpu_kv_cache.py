@@ -1,0 +1,485 @@
+"""The paged cache on the GPU against its plain 64-bit forms (_kv_ref.py)."""
+import os
+
+import numpy as np
+import pytest
+
+import _kv_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def kv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_draft_block_gb300 import _lib, build, kv_cache
+    if not os.path.exists(_lib.LIB_PATH):
+        build.build()
+    return kv_cache
+
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _i32(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def _host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+class Batch:
+    """Ragged rows over a pool whose unseen places hold NaN; pages scattered; the table -1 where nothing is needed."""
+
+    def __init__(self, dtype, D, S, Hk, G, lens, layout="nhd", window=0, causal=True, seed=0, spread=1.0, extra=5,
+                 strided=False):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.RandomState(seed)
+        self.dtype, self.D, self.S, self.causal, self.window = dtype, D, S, causal, window
+        n_q, n_kv = [a for a, _ in lens], [b for _, b in lens]
+        M = max(1, max(ref.ceil_div(n, S) for n in n_kv))
+        N = sum(ref.ceil_div(n, S) for n in n_kv) + extra
+        shape = (1, N, S, Hk, D) if layout == "nhd" else (1, N, Hk, S, D)
+        self.k, self.v = (torch.full(shape, float("nan"), dtype=DT[dtype], device="cuda") for _ in range(2))
+        if layout != "nhd":
+            self.k, self.v = self.k.transpose(2, 3), self.v.transpose(2, 3)
+        order = rng.permutation(N)
+        table, at = np.full((len(lens), M), -1, dtype=np.int32), 0
+        for b, (nq, n) in enumerate(lens):
+            lo = max(0, n - nq - window + 1) if window else 0   # nothing before this is seen
+            for p in range(ref.ceil_div(n, S)):
+                if (p + 1) * S <= lo:
+                    continue
+                table[b, p] = order[at]
+                at += 1
+                a, z = max(lo, p * S) - p * S, min(n, (p + 1) * S) - p * S
+                for x in (self.k, self.v):
+                    x[0, int(table[b, p]), a:z] = (torch.randn((z - a, Hk, D), device="cuda", generator=g) * spread).to(DT[dtype])
+        T = sum(n_q)
+        H = G * Hk
+        if strided:   # a slice of a wider projection, heads 2 * D apart
+            wide = torch.randn((T, H + 2, 2 * D), device="cuda", generator=g).to(DT[dtype])
+            self.q = wide[:, 1:H + 1, :D]
+            self.out = torch.zeros((T, H + 1, 2 * D), dtype=DT[dtype], device="cuda")[:, :H, D:]
+        else:
+            self.q = torch.randn((T, H, D), device="cuda", generator=g).to(DT[dtype]) * spread
+            self.out = torch.full((T, H, D), 7.0, dtype=DT[dtype], device="cuda")
+        self.lse = torch.full((T, H), 7.0, device="cuda")
+        self.table, self.kv_len = _i32(table), _i32(n_kv)
+        self.q_start = _i32(np.concatenate([[0], np.cumsum(n_q)]))
+        self.max_q = max(1, max(n_q))
+        self.status = torch.zeros(4, dtype=torch.int32, device="cuda")
+
+    def call(self, kv, stream=None, scale=None, lse=True):
+        pool = kv.KvPool(self.k, self.v)
+        ws = torch.full((kv.ds_paged_attention_workspace_bytes(pool, self.q.shape[1]),), 0xA5, dtype=torch.uint8,
+                        device="cuda")
+        self.ws = ws
+        return kv.ds_paged_attention(pool, 0, self.q, self.q_start, self.max_q, self.table, self.kv_len, self.out, ws,
+                                     self.status, lse=self.lse if lse else None, causal=self.causal, window=self.window,
+                                     scale=scale, stream=stream)
+
+    def verify(self, kv, **kw):
+        assert self.call(kv, **kw) == 0
+        assert int(self.status[0]) == 0
+        scale = kw.get("scale") or ref.default_scale(self.D)
+        k, v = _host(self.k[0]), _host(self.v[0])
+        want, lse, tol, lse_tol = ref.attend(_host(self.q), k, v, self.table.cpu().numpy(), self.kv_len.cpu().numpy(),
+                                             self.q_start.cpu().numpy(), self.causal, self.window, scale,
+                                             self.dtype == "bf16")
+        got = _host(self.out)
+        assert np.isfinite(got).all()
+        off = np.abs(got - want) - tol
+        assert off.max() <= 0, (off.max(), np.unravel_index(off.argmax(), off.shape), np.abs(got - want).max())
+        if kw.get("lse", True):
+            got = _host(self.lse)
+            empty = np.isneginf(lse)
+            assert np.array_equal(np.isneginf(got), empty)
+            off = np.abs(got[~empty] - lse[~empty]) - lse_tol[~empty]
+            assert off.size == 0 or off.max() <= 0, off.max()
+
+
+MIXED = [(1, 1), (1, 0), (0, 37), (3, 3), (5, 2), (17, 200), (1, 129), (2, 128), (4, 127), (9, 33), (33, 40)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,S,Hk,G,layout", [(128, 16, 2, 4, "nhd"), (64, 32, 1, 1, "hnd"), (128, 64, 2, 5, "hnd"),
+                                             (64, 128, 3, 8, "nhd"), (128, 256, 1, 16, "nhd"), (64, 16, 1, 7, "nhd"),
+                                             (128, 32, 1, 128, "hnd"), (64, 64, 2, 33, "nhd")])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 20), (False, 1)])
+def test_attention_of_mixed_requests(kv, dtype, D, S, Hk, G, layout, causal, window):
+    """Empty requests, empty contexts, more rows than tokens, lengths about the pages' and tiles' ends."""
+    Batch(dtype, D, S, Hk, G, MIXED, layout, window, causal, seed=D + S + G).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(1, 5000)], [(1, 4097), (17, 3000), (5, 1)], [(300, 700)], [(130, 1500), (1, 900)],
+                                  [(257, 257), (64, 64)]])
+def test_attention_of_long_contexts(kv, dtype, lens):
+    """Work split over the context and joined; prompts of several tiles."""
+    Batch(dtype, 128, 32, 2, 4, lens, seed=len(lens)).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 128, 129, 500])
+def test_attention_windows_on_long_contexts(kv, dtype, window):
+    """Pages before the window hold NaN or have no entry."""
+    Batch(dtype, 64, 16, 2, 3, [(40, 2000), (1, 1025), (7, 600), (200, 450)], window=window, seed=window).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_many_small_requests(kv, dtype):
+    rng = np.random.RandomState(3)
+    lens = [(int(a), int(a + c)) for a, c in zip(rng.randint(0, 4, 700), rng.randint(0, 90, 700))]
+    Batch(dtype, 64, 16, 1, 2, lens, seed=9).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_peaked_scores(kv, dtype):
+    """Scores that span hundreds: the running maximum rises many times."""
+    Batch(dtype, 128, 64, 2, 4, [(9, 1100), (1, 777), (140, 300)], seed=4, spread=4.0).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_rising_scores(kv, dtype):
+    """Keys that grow along the context: the maximum rises in every tile."""
+    x = Batch(dtype, 64, 32, 1, 4, [(1, 3000), (30, 1000)], seed=5)
+    scale = torch.linspace(0.0, 6.0, 3000, device="cuda")
+    table = x.table.cpu().numpy()
+    for b, n in ((0, 3000), (1, 1000)):
+        for p in range(ref.ceil_div(n, 32)):
+            z = min(32, n - 32 * p)
+            x.k[0, int(table[b, p]), :z] = (x.k[0, int(table[b, p]), :z].float()
+                                            * scale[32 * p:32 * p + z, None, None]).to(DT[dtype])
+    x.verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_strided_rows_and_scale(kv, dtype):
+    x = Batch(dtype, 128, 16, 2, 4, [(5, 90), (1, 300), (40, 41)], strided=True, seed=6)
+    base = x.out._base if x.out._base is not None else x.out
+    x.verify(kv, scale=0.03)
+    assert (base[:, -1] == 0).all() and (base[:, :, :128] == 0).all()      # nothing beside the rows is written
+    x.verify(kv, lse=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_same_bits_twice_and_on_another_stream(kv, dtype):
+    x = Batch(dtype, 128, 16, 2, 4, [(1, 2500), (17, 1300), (60, 61)], seed=7)
+    x.verify(kv)
+    first = x.out.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            x.out.fill_(3.0)
+            assert x.call(kv) == 0
+    s.synchronize()
+    assert torch.equal(first.view(torch.int16 if dtype == "bf16" else torch.int32),
+                       x.out.view(torch.int16 if dtype == "bf16" else torch.int32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_in_a_graph(kv, dtype):
+    x = Batch(dtype, 64, 64, 2, 4, [(1, 600), (9, 300)], seed=8)
+    pool = kv.KvPool(x.k, x.v)
+    ws = torch.empty(kv.ds_paged_attention_workspace_bytes(pool, 8), dtype=torch.uint8, device="cuda")
+
+    def step():
+        kv.check(kv.ds_paged_attention(pool, 0, x.q, x.q_start, x.max_q, x.table, x.kv_len, x.out, ws, x.status, lse=x.lse))
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    x.kv_len.copy_(_i32([433, 300]))                # a shorter context at replay: lengths are read on the device
+    # the request's row stands at its last token now
+    x.out.fill_(1.0)
+    g.replay()
+    torch.cuda.synchronize()
+    got = x.out.clone()
+    x.verify(kv)
+    assert torch.equal(got, x.out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_reports_what_is_out_of_bounds(kv, dtype):
+    """Malformed device data: the status says so, nothing faults, the other requests' rows stand."""
+    def fresh():
+        return Batch(dtype, 64, 16, 1, 2, [(2, 100), (3, 50), (1, 70)], seed=11)
+
+    good = fresh()
+    good.verify(kv)
+    for what in ("page", "negative page", "kv_len", "negative kv_len", "q_start", "max_q", "q_end"):
+        x = fresh()
+        if what == "page":
+            x.table[1, 0] = x.k.shape[1]
+        elif what == "negative page":
+            x.table[1, 2] = -1
+        elif what == "kv_len":
+            x.kv_len[1] = x.table.shape[1] * 16 + 1
+        elif what == "negative kv_len":
+            x.kv_len[1] = -5
+        elif what == "q_start":
+            x.q_start[2] = 1
+        elif what == "max_q":
+            x.max_q = 2
+        else:
+            x.q_start[3] = 1000
+        assert x.call(kv) == 0
+        assert int(x.status[0]) == 6, what
+        assert torch.equal(x.out[:2], good.out[:2]), what
+
+
+def test_append_places_rows(kv):
+    for dtype, D, S, Hk, layout in (("bf16", 128, 16, 2, "nhd"), ("f32", 64, 32, 3, "hnd"), ("bf16", 8, 256, 1, "nhd"),
+                                    ("f32", 200, 64, 5, "hnd"), ("bf16", 72, 128, 4, "nhd")):
+        lens = [(1, 1), (0, 20), (3, 3), (5, 2), (40, 300), (1, S + 1), (S, S), (2, 0)] + [(1, 7)] * 300
+        rng = np.random.RandomState(S)
+        M = max(ref.ceil_div(n, S) for _, n in lens)
+        N = sum(ref.ceil_div(n, S) for _, n in lens) + 2
+        shape = (3, N, S, Hk, D) if layout == "nhd" else (3, N, Hk, S, D)
+        k, v = (torch.zeros(shape, dtype=DT[dtype], device="cuda") for _ in range(2))
+        if layout == "hnd":
+            k, v = k.transpose(2, 3), v.transpose(2, 3)
+        table, at, order = np.full((len(lens), M), -1, np.int32), 0, rng.permutation(N)
+        for b, (_, n) in enumerate(lens):
+            p = ref.ceil_div(n, S)
+            table[b, :p] = order[at:at + p]
+            at += p
+        q_start = np.concatenate([[0], np.cumsum([a for a, _ in lens])])
+        T = int(q_start[-1])
+        g = torch.Generator(device="cuda").manual_seed(1)
+        wide = torch.randn((T, 2 * Hk, D), device="cuda", generator=g).to(DT[dtype])    # K and V of one projection
+        kn, vn = wide[:, :Hk], torch.randn((T, Hk, D), device="cuda", generator=g).to(DT[dtype])
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        want_k, want_v = k.clone(), v.clone()
+        for b, (a, n) in enumerate(lens):
+            for i in range(a):
+                p = n - a + i
+                if p >= 0:
+                    want_k[1, int(table[b, p // S]), p % S] = kn[q_start[b] + i]
+                    want_v[1, int(table[b, p // S]), p % S] = vn[q_start[b] + i]
+        pool = kv.KvPool(k, v)
+        kv.check(kv.ds_cache_append(pool, 1, kn, vn, _i32(q_start), _i32(table), _i32([n for _, n in lens]), status))
+        assert int(status[0]) == 0
+        assert torch.equal(k, want_k) and torch.equal(v, want_v)
+        # a page out of range: reported, the rest written, nothing else touched
+        k.zero_(), v.zero_()
+        bad = table.copy()
+        bad[4, 18 if S == 16 else 0] = N
+        kv.check(kv.ds_cache_append(pool, 1, kn, vn, _i32(q_start), _i32(bad), _i32([n for _, n in lens]), status))
+        lost = 300 - 40 < (19 * 16 if S == 16 else S)
+        assert int(status[0]) == (6 if lost else 0)
+
+
+def _state(rng, B, S, N, width, M, pins):
+    """Requests in groups that share their first pages; some empty; some pages pinned from outside."""
+    pages = list(rng.permutation(N))
+    table, lens = [[-1] * M for _ in range(B)], [0] * B
+    for b0 in range(0, B, width):
+        common = int(rng.randint(0, max(1, M * S - 2 * S)))
+        row = [pages.pop() for _ in range(min(ref.ceil_div(common, S), len(pages)))]
+        common = min(common, len(row) * S)
+        for b in range(b0, min(B, b0 + width)):
+            if rng.rand() < 0.1:
+                continue
+            if rng.rand() < 0.5 or not pages:
+                table[b][:len(row)], lens[b] = row, common
+            else:
+                n = common // S
+                extra = min(int(rng.randint(1, 3)), len(pages), M - n)
+                mine = row[:n] + [pages.pop() for _ in range(extra)]
+                table[b][:len(mine)] = mine
+                lens[b] = n * S + (int(rng.randint(1, extra * S + 1)) if extra else 0)
+    table = [[int(p) for p in r] for r in table]
+    lens = [int(n) for n in lens]
+    held = [0] * N
+    for b in range(B):
+        for p in table[b][:ref.ceil_div(lens[b], S)]:
+            held[p] += 1
+    for _ in range(pins):
+        held[int(rng.randint(N))] += 1
+    return table, lens, held
+
+
+@pytest.mark.parametrize("B,S,N,width,M,pins", [(1, 16, 9, 1, 6, 0), (7, 16, 64, 3, 6, 0), (64, 32, 900, 8, 9, 20),
+                                                (300, 16, 5000, 4, 11, 100), (33, 64, 70, 33, 5, 1), (5, 256, 11, 2, 3, 0),
+                                                (2000, 16, 30000, 2, 7, 50)])
+@pytest.mark.parametrize("kind", ["grow", "mixed", "beams"])
+def test_update_against_the_plain_form(kv, B, S, N, width, M, pins, kind):
+    for seed in range(4):
+        rng = np.random.RandomState(100 * seed + B)
+        table, lens, held = _state(rng, B, S, N, width, M, pins)
+        parent = None
+        if kind == "grow":
+            new = [min(M * S, n + int(rng.randint(0, S))) for n in lens]
+        elif kind == "mixed":
+            new = [int(rng.choice([0, n, max(0, n - int(rng.randint(0, 2 * S))), min(M * S, n + 1)])) for n in lens]
+        else:
+            parent = [int(rng.randint(-1, B)) if rng.rand() < 0.2 else min(B - 1, b // width * width + int(rng.randint(width)))
+                      for b in range(B)]
+            new = [min(M * S, (lens[p] if p >= 0 else 0) + int(rng.randint(0, 3))) for p in parent]
+        want = ref.update(table, lens, held, new, parent, S, N)
+        k = torch.arange(2 * N * S * 1 * 8, device="cuda").reshape(2, N, S, 1, 8).to(torch.float32)
+        v = -k
+        want_k, want_v = k.clone(), v.clone()
+        pool = kv.KvPool(k, v)
+        state = _i32(table), _i32(lens), _i32(held)
+        out = tuple(torch.full_like(x, -77) for x in state)
+        ws = torch.full((kv.ds_cache_update_workspace_bytes(B, N),), 0xA5, dtype=torch.uint8, device="cuda")
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        kv.check(kv.ds_cache_update(pool, *state, _i32(new), *out, ws, status, parent=None if parent is None else _i32(parent)))
+        if want is None:
+            assert int(status[0]) == 8
+            want = [[table[b][j] for j in range(M)] for b in range(B)], lens, held, {}
+        else:
+            assert int(status[0]) == 0
+        assert out[0].tolist() == want[0] and out[1].tolist() == want[1] and out[2].tolist() == want[2]
+        for a, z, n in want[3].values():
+            for x in (want_k, want_v):
+                x[:, z, :n] = x[:, a, :n]
+        assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def test_update_copies_every_layout(kv):
+    for dtype, layout, Hk, D, S in (("bf16", "nhd", 4, 128, 16), ("bf16", "hnd", 3, 72, 32), ("f32", "hnd", 2, 64, 64)):
+        N, L = 12, 3
+        shape = (L, N, S, Hk, D) if layout == "nhd" else (L, N, Hk, S, D)
+        k, v = (torch.randn(shape, device="cuda").to(DT[dtype]) for _ in range(2))
+        if layout == "hnd":
+            k, v = k.transpose(2, 3), v.transpose(2, 3)
+        want_k, want_v = k.clone(), v.clone()
+        table, lens = [[3, 5, -1], [3, 5, -1], [3, 5, -1]], [S + 7] * 3
+        held = [0] * N
+        held[3] = held[5] = 3
+        new = [S + 8, S + 7, 2 * S + 1]
+        want = ref.update(table, lens, held, new, None, S, N)
+        assert sorted(want[3]) == [0, 2]
+        state = _i32(table), _i32(lens), _i32(held)
+        out = tuple(torch.empty_like(x) for x in state)
+        ws = torch.empty(kv.ds_cache_update_workspace_bytes(3, N), dtype=torch.uint8, device="cuda")
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        kv.check(kv.ds_cache_update(kv.KvPool(k, v), *state, _i32(new), *out, ws, status))
+        for a, z, n in want[3].values():
+            for x in (want_k, want_v):
+                x[:, z, :n] = x[:, a, :n]
+        assert int(status[0]) == 0 and out[0].tolist() == want[0] and out[2].tolist() == want[2]
+        assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def test_update_refuses_bad_state_and_changes_nothing(kv):
+    S, N, M, B = 16, 8, 3, 3
+    k = torch.zeros((1, N, S, 1, 8), device="cuda")
+    pool = kv.KvPool(k, k.clone())
+    table, lens, held = [[0, 1, -1], [2, -1, -1], [-1, -1, -1]], [20, 5, 0], [1, 1, 1, 0, 0, 0, 0, 0]
+    ok = [30, 6, 48]
+    cases = [(dict(new=[49, 6, 1]), 6), (dict(new=[-1, 6, 1]), 6), (dict(parent=[0, 3, 2]), 6), (dict(parent=[0, -2, 2]), 6),
+             (dict(lens=[20, 5, 49]), 6), (dict(lens=[-1, 5, 0]), 6), (dict(held=[1, 0, 1, 0, 0, 0, 0, 0], new=[0, 6, 1]), 6),
+             (dict(table=[[0, 9, -1], [2, -1, -1], [-1, -1, -1]], new=[30, 6, 1]), 6),
+             (dict(held=[1, 1, 1, 1, 1, 1, 0, 0]), 8), (dict(), 0)]
+    for change, code in cases:
+        t, n, h = change.get("table", table), change.get("lens", lens), change.get("held", held)
+        parent = change.get("parent")
+        state = _i32(t), _i32(n), _i32(h)
+        out = tuple(torch.full_like(x, -77) for x in state)
+        ws = torch.empty(kv.ds_cache_update_workspace_bytes(B, N), dtype=torch.uint8, device="cuda")
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        kv.check(kv.ds_cache_update(pool, *state, _i32(change.get("new", ok)), *out, ws, status,
+                                    parent=None if parent is None else _i32(parent)))
+        assert int(status[0]) == code, (change, int(status[0]))
+        if code:
+            assert all(torch.equal(a, b) for a, b in zip(state, out)), change
+
+
+@pytest.mark.parametrize("N,B,held", [(1, 1, 1.0), (5, 2, 0.0), (64, 3, 0.5), (1000, 9, 0.9), (20000, 40, 0.3), (4099, 7, 1.0)])
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+def test_compact_against_the_plain_form(kv, N, B, held, layout):
+    rng = np.random.RandomState(N)
+    S, Hk, D, L = 16, 2, 8, 2
+    pages = rng.permutation(N)[:int(round(held * N))]
+    M = max(1, ref.ceil_div(len(pages), B) + 1)
+    table = [[int(p) for p in pages[b::B]] for b in range(B)]
+    table = [r + [-1] * (M - len(r)) for r in table]
+    cnt = [0] * N
+    for p in pages:
+        cnt[int(p)] = int(rng.randint(1, 4))
+    shape = (L, N, S, Hk, D) if layout == "nhd" else (L, N, Hk, S, D)
+    k = torch.randn(shape, device="cuda")
+    v = torch.randn(shape, device="cuda")
+    if layout == "hnd":
+        k, v = k.transpose(2, 3), v.transpose(2, 3)
+    want_k, want_v = k.clone(), v.clone()
+    want = ref.compact(table, cnt)
+    out_t, out_r, out_m = (torch.full((B, M), -77, dtype=torch.int32, device="cuda"),
+                           torch.full((N,), -77, dtype=torch.int32, device="cuda"),
+                           torch.full((N,), -77, dtype=torch.int32, device="cuda"))
+    used, status = _i32([-1]), torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.full((kv.ds_cache_compact_workspace_bytes(N),), 0xA5, dtype=torch.uint8, device="cuda")
+    kv.check(kv.ds_cache_compact(kv.KvPool(k, v), _i32(table), _i32(cnt), out_t, out_r, out_m, used, ws, status))
+    assert int(status[0]) == 0
+    assert out_t.tolist() == want[0] and out_r.tolist() == want[1] and out_m.tolist() == want[2]
+    assert used.tolist() == [want[3]]
+    for a, z in want[4]:
+        for x in (want_k, want_v):
+            x[:, z] = x[:, a]
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def test_compact_refuses_negative_counts(kv):
+    N, B, M = 8, 1, 4
+    k = torch.randn((1, N, 16, 1, 8), device="cuda")
+    before = k.clone()
+    table, cnt = _i32([[6, 7, 2, -1]]), _i32([0, -1, 1, 0, 0, 0, 1, 1])
+    t, r, m = torch.empty_like(table), torch.empty_like(cnt), torch.empty_like(cnt)
+    used, status = _i32([0]), torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.ds_cache_compact_workspace_bytes(N), dtype=torch.uint8, device="cuda")
+    kv.check(kv.ds_cache_compact(kv.KvPool(k, k.clone()), table, cnt, t, r, m, used, ws, status))
+    assert int(status[0]) == 6
+    assert torch.equal(t, table) and torch.equal(r, cnt) and torch.equal(k, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cycles_of_a_paged_cache(kv, dtype):
+    """Verify cycles through PagedCache (grow, append, attend, fall back, fork, compact) against a contiguous copy."""
+    rng = np.random.RandomState(5)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    B, Hk, G, D, S, n = 6, 2, 2, 64, 16, 5
+    c = kv.PagedCache(2, 90, S, Hk, D, B, 160, dtype=DT[dtype], heads_outside=True)
+    past = [[(np.zeros((0, Hk, D)), np.zeros((0, Hk, D))) for _ in range(2)] for _ in range(B)]
+    q_start = _i32([n * b for b in range(B + 1)])
+    for cycle in range(8):
+        lens = [past[b][0][0].shape[0] for b in range(B)]
+        c.update(_i32([x + n for x in lens]))
+        for layer in range(2):
+            kn, vn = (torch.randn((B * n, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+            q = torch.randn((B * n, Hk * G, D), device="cuda", generator=g).to(DT[dtype])
+            c.append(layer, kn, vn, q_start)
+            out = c.attend(layer, q, q_start, n)
+            for b in range(B):
+                k0, v0 = past[b][layer]
+                past[b][layer] = (np.concatenate([k0, _host(kn[b * n:(b + 1) * n])]),
+                                  np.concatenate([v0, _host(vn[b * n:(b + 1) * n])]))
+            kk = [past[b][layer][0] for b in range(B)]
+            longest = max(x.shape[0] for x in kk)
+            kp, vp = np.zeros((B, longest, Hk, D)), np.zeros((B, longest, Hk, D))
+            for b in range(B):
+                kp[b, :kk[b].shape[0]], vp[b, :kk[b].shape[0]] = past[b][layer]
+            want, _, tol, _ = ref.attend(_host(q), kp, vp, np.arange(B)[:, None], [x.shape[0] for x in kk],
+                                         list(range(0, B * n + 1, n)), True, 0, ref.default_scale(D), dtype == "bf16")
+            assert (np.abs(_host(out) - want) <= tol).all()
+        c.check_status()
+        parent = list(range(B)) if cycle % 3 else [int(rng.randint(B)) for _ in range(B)]
+        keep = [len(past[p][0][0]) - int(rng.randint(0, n)) for p in parent]
+        c.update(_i32(keep), parent=_i32(parent))
+        past = [[(past[p][layer][0][:m], past[p][layer][1][:m]) for layer in range(2)] for p, m in zip(parent, keep)]
+        if cycle % 2:
+            c.compact()
+            assert int(c.n_used[0]) == int((c.ref > 0).sum())
+            assert (c.ref[:int(c.n_used[0])] > 0).all()
+    c.check_status()
