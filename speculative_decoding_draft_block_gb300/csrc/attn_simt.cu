@@ -84,12 +84,6 @@ __global__ void __launch_bounds__(128) attn_rows_kernel(const AttnParams p) {
 
 }  // namespace
 
-size_t attention_ws_bytes(int32_t dtype, int32_t D) {
-  (void)dtype;
-  // per CTA two partial results of 256 rows: D sums, maximum and sum
-  return (size_t)kMaxAttnCtas * 2 * 256 * (D + 2) * sizeof(float) + 65536;
-}
-
 cudaError_t launch_attention_simt(const AttnParams& p, cudaStream_t s) {
   const dim3 grid((p.max_q + 3) / 4, p.n_heads, p.B);
   const bool bf = p.dtype == DS_BF16;

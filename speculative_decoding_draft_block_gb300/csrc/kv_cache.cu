@@ -237,7 +237,9 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   p.lse = a->lse;
   p.workspace = static_cast<char*>(a->workspace);
   p.status = a->status;
-  return launch_attention_simt(p, (cudaStream_t)stream) == cudaSuccess ? DS_OK : DS_ERR_CUDA;
+  const cudaError_t err = p.dtype == DS_BF16 ? launch_attention_tc(p, (cudaStream_t)stream)
+                                             : launch_attention_simt(p, (cudaStream_t)stream);
+  return err == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 
 size_t ds_cache_update_workspace_bytes(int32_t B, int32_t n_pages) {

@@ -7,7 +7,7 @@ import math
 import numpy as np
 
 U32 = 2.0 ** -24          # unit roundoff of float32
-UBF = 2.0 ** -9           # of bfloat16
+UBF = 2.0 ** -8           # of bfloat16: 8 significand bits, so half a unit in the last place is 2^-8 of the value
 
 
 def ceil_div(a, b):
