@@ -71,7 +71,8 @@ struct Layout {
 struct Header {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[10], empty[10];
-  uint64_t cleared[10];          // the slot's V tile has had its unseen rows cleared
+  uint64_t to_clear[10];         // the slot is being filled with a V tile some rows of which no row sees
+  uint64_t cleared[10];          // and those have been cleared
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t x_ready, x_free;      // exchange of the streams' statistics
   uint64_t drain;
@@ -204,6 +205,10 @@ struct Walk {
   __device__ __forceinline__ bool empty() const { return u.tiles == 0; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
   __device__ __forceinline__ int64_t unit_end() const { return base + (int64_t)(h + 1) * n; }
+  // whether no row of the unit sees some of a tile's keys
+  __device__ __forceinline__ bool partly_seen(int tile) const {
+    return tile * kTile < u.lo || (tile + 1) * kTile > u.hi;
+  }
   // place of a key tile's K or V in the order of the ring, counted from the piece's first
   __device__ __forceinline__ uint32_t k_place(int j) const { return u.two ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
   __device__ __forceinline__ uint32_t v_place(int j) const {
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.to_clear[i], 1);
       mbar_init(&sh.cleared[i], 1);
     }
     mbar_init(&sh.x_ready, 8);
@@ -378,13 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         report(p.status, kErrBounds);
         return 0;
       };
-      auto load = [&](const CUtensorMap* map, int tile, int page) {
+      auto load = [&](const CUtensorMap* map, int tile, int page, bool is_v) {
         const uint32_t s = rc % kSlots;
         if (lane == 0) ok = wait_bar(&sh.empty[s], ((rc / kSlots) & 1) ^ 1, abort_flag, p.status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) return;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) mbar_expect_tx(&sh.full[s], n * kHalves * box_bytes);
+        if (lane == 0) {
+          mbar_expect_tx(&sh.full[s], n * kHalves * box_bytes);
+          if (is_v && wk.partly_seen(tile)) mbar_arrive(&sh.to_clear[s]);
+        }
         __syncwarp();
         if (page >= 0) {
           uint8_t* dst = sRing + s * L::kTileBytes + lane * box_bytes;
@@ -416,18 +425,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < n && ok; ++j) {
             const int now = page;
             if (j + 1 < n) page = page_of(first + j + 1);
-            load(&tmK, first + j, now);
-            if (ok) load(&tmV, first + j, now);
+            load(&tmK, first + j, now, false);
+            if (ok) load(&tmV, first + j, now, true);
           }
         } else {
-          load(&tmK, first, page);
+          load(&tmK, first, page, false);
           for (int j = 0; j < n && ok; ++j) {
             const int now = page;
             if (j + 1 < n) {
               page = page_of(first + j + 1);
-              load(&tmK, first + j + 1, page);
+              load(&tmK, first + j + 1, page, false);
             }
-            if (ok) load(&tmV, first + j, now);
+            if (ok) load(&tmV, first + j, now, true);
           }
         }
       }
@@ -483,9 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_parity ^= 1u << s;
             const uint32_t at = rc + wk.v_place(j), slot = at % kSlots;
             if (!two || s == 0) {
-              const int key = (wk.u.tile0 + wk.t0 + j) * kTile;
               ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
-              if (ok && (key < wk.u.lo || key + kTile > wk.u.hi)) {
+              if (ok && wk.partly_seen(wk.u.tile0 + wk.t0 + j)) {
                 ok = wait_bar(&sh.cleared[slot], (c_parity >> slot) & 1, abort_flag, p.status);
                 c_parity ^= 1u << slot;
               }
@@ -510,7 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       // ---------------------------------------------------------------- unseen V rows
-      uint32_t rc = 0;
+      // The producer says when it begins to fill a slot with such a tile: only
+      // from then on does the parity of the slot's barrier mean this filling (a
+      // barrier tells a phase from the next one, not from the one after), and the
+      // slot is not filled again before the MMA issuer has seen `cleared`.
+      uint32_t rc = 0, parity = 0;
       bool ok = true;
       while (ok && wk.next(p, per_tile)) {
         if (wk.empty()) continue;
@@ -519,10 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j = x == 0 ? 0 : n - 1;
           if (x == 1 && n == 1) break;
           const int key = (wk.u.tile0 + wk.t0 + j) * kTile;
-          if (key >= wk.u.lo && key + kTile <= wk.u.hi) continue;
+          if (!wk.partly_seen(wk.u.tile0 + wk.t0 + j)) continue;
           const uint32_t at = rc + wk.v_place(j), slot = at % kSlots;
-          ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
+          ok = wait_bar(&sh.to_clear[slot], (parity >> slot) & 1, abort_flag, p.status) &&
+               wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
           if (!ok) break;
+          parity ^= 1u << slot;
           uint8_t* tile = sRing + slot * L::kTileBytes;
           const int head = max(0, wk.u.lo - key), tail = min(kTile, wk.u.hi - key);
           for (int half = 0; half < kHalves; ++half) {

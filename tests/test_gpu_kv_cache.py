@@ -124,6 +124,15 @@ def test_attention_of_long_contexts(kv, dtype, lens):
     Batch(dtype, 128, 32, 2, 4, lens, seed=len(lens)).verify(kv)
 
 
+@pytest.mark.parametrize("D,S,Hk,G,lens", [(128, 64, 8, 1, [(1, 1700 + 61 * i) for i in range(24)]),
+                                           (64, 128, 8, 2, [(5, 900 + 77 * i) for i in range(20)]),
+                                           (128, 32, 6, 8, [(17, 400 + 83 * i) for i in range(20)]),
+                                           (64, 16, 8, 4, [(40 + 13 * i, 700 + 50 * i) for i in range(10)])])
+def test_attention_of_many_long_contexts(kv, D, S, Hk, G, lens):
+    """Many key tiles and several units for every SM, of one row tile and of two."""
+    Batch("bf16", D, S, Hk, G, lens, seed=D + G).verify(kv)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [1, 128, 129, 500])
 def test_attention_windows_on_long_contexts(kv, dtype, window):
