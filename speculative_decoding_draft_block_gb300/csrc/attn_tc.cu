@@ -448,73 +448,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t iqk = idesc_bf16(kTile, kTile, false, false);
-        constexpr uint32_t ipv = idesc_bf16(kTile, D, false, true);
-        constexpr uint64_t kbits = smem_desc_bits(16, 1024, 2);
-        constexpr uint64_t vbits = smem_desc_bits(kTile * 128, 1024, 2);
-        uint32_t rc = 0, qc = 0;
-        uint32_t p_parity = 0, c_parity = 0;  // of the next phase of p_full[s] and cleared[slot], a bit each
-        bool ok = true;
-        while (ok && wk.next(p, per_tile)) {
-          if (wk.empty()) continue;
-          const int n = wk.t1 - wk.t0, two = wk.u.two;
-          const int steps = two ? 2 * n : n;
-          for (int s = 0; s <= two && ok; ++s)
-            ok = wait_bar(&sh.q_full[(qc + s) & 1], ((qc + s) >> 1) & 1, abort_flag, p.status);
-          tc_fence_after();
-          auto qk = [&](int t) {
-            const int s = t & 1, j = two ? t >> 1 : t;
-            const uint32_t at = rc + wk.k_place(j), slot = at % kSlots;
-            if (!two || s == 0) {
-              ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
-              if (!ok) return;
-              tc_fence_after();
-            }
-            const uint8_t* a = sQ + ((qc + (two ? s : 0)) & 1) * L::kTileBytes;
-            const uint8_t* b = sRing + slot * L::kTileBytes;
+      // (all lanes run the loop, one issues)
+      constexpr uint32_t iqk = idesc_bf16(kTile, kTile, false, false);
+      constexpr uint32_t ipv = idesc_bf16(kTile, D, false, true);
+      constexpr uint64_t kbits = smem_desc_bits(16, 1024, 2);
+      constexpr uint64_t vbits = smem_desc_bits(kTile * 128, 1024, 2);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = smem_desc(sQ, kbits), k_desc = smem_desc(sRing, kbits), v_desc = smem_desc(sRing, vbits);
+      uint32_t rc = 0, qc = 0;
+      uint32_t p_parity = 0, c_parity = 0;  // of the next phase of p_full[s] and cleared[slot], a bit each
+      bool ok = true;
+      while (ok && wk.next(p, per_tile)) {
+        if (wk.empty()) continue;
+        const int n = wk.t1 - wk.t0, two = wk.u.two;
+        const int steps = two ? 2 * n : n;
+        for (int s = 0; s <= two && ok; ++s)
+          ok = wait_bar(&sh.q_full[(qc + s) & 1], ((qc + s) >> 1) & 1, abort_flag, p.status);
+        tc_fence_after();
+        auto qk = [&](int t) {
+          const int s = t & 1, j = two ? t >> 1 : t;
+          const uint32_t at = rc + wk.k_place(j), slot = __shfl_sync(0xffffffffu, at % kSlots, 0);
+          if (!two || s == 0) {
+            ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
+            if (!ok) return;
+            tc_fence_after();
+          }
+          const uint32_t qs = __shfl_sync(0xffffffffu, (qc + (two ? s : 0)) & 1, 0);
+          const uint64_t a = q_desc + qs * (L::kTileBytes >> 4), b = k_desc + slot * (L::kTileBytes >> 4);
+          const uint32_t d = tm + s * kTile;
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-              mma_bf16(tmem + s * kTile, smem_desc(a + off, kbits), smem_desc(b + off, kbits), iqk, k != 0);
+              constexpr uint32_t kHalf = (kTile * 128) >> 4;
+              const uint32_t off = (k >> 2) * kHalf + (k & 3) * 2;
+              mma_bf16(d, a + off, b + off, iqk, k != 0);
             }
             mma_commit(&sh.s_full[s]);
             if (!two || s == 1) mma_commit(&sh.empty[slot]);
             // Q is free after the last product that reads it
-            if (t + 1 == steps || (two && t + 2 == steps)) mma_commit(&sh.q_empty[(qc + (two ? s : 0)) & 1]);
-          };
-          if (ok) qk(0);
-          if (ok && steps > 1) qk(1);
-          for (int t = 0; t < steps && ok; ++t) {
-            const int s = t & 1, j = two ? t >> 1 : t;
-            ok = wait_bar(&sh.p_full[s], (p_parity >> s) & 1, abort_flag, p.status);
-            if (!ok) break;
-            p_parity ^= 1u << s;
-            const uint32_t at = rc + wk.v_place(j), slot = at % kSlots;
-            if (!two || s == 0) {
-              ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
-              if (ok && wk.partly_seen(wk.u.tile0 + wk.t0 + j)) {
-                ok = wait_bar(&sh.cleared[slot], (c_parity >> slot) & 1, abort_flag, p.status);
-                c_parity ^= 1u << slot;
-              }
-              if (!ok) break;
+            if (t + 1 == steps || (two && t + 2 == steps)) mma_commit(&sh.q_empty[qs]);
+          }
+          __syncwarp();
+        };
+        if (ok) qk(0);
+        if (ok && steps > 1) qk(1);
+        for (int t = 0; t < steps && ok; ++t) {
+          const int s = t & 1, j = two ? t >> 1 : t;
+          const uint32_t at = rc + wk.v_place(j), slot = __shfl_sync(0xffffffffu, at % kSlots, 0);
+          if (!two || s == 0) {
+            ok = wait_bar(&sh.full[slot], (at / kSlots) & 1, abort_flag, p.status);
+            if (ok && wk.partly_seen(wk.u.tile0 + wk.t0 + j)) {
+              ok = wait_bar(&sh.cleared[slot], (c_parity >> slot) & 1, abort_flag, p.status);
+              c_parity ^= 1u << slot;
             }
-            tc_fence_after();
-            const uint8_t* b = sRing + slot * L::kTileBytes;
+            if (!ok) break;
+          }
+          ok = wait_bar(&sh.p_full[s], (p_parity >> s) & 1, abort_flag, p.status);
+          if (!ok) break;
+          p_parity ^= 1u << s;
+          tc_fence_after();
+          const uint64_t b = v_desc + slot * (L::kTileBytes >> 4);
+          const uint32_t d = tm + 256 + s * D, a = tm + s * kTile;
+          const uint32_t more = t >= 2;
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_bf16_ta(tmem + 256 + s * D, tmem + s * kTile + k * 8, smem_desc(b + k * 2048, vbits), ipv,
-                          (t >= 2 || k != 0) ? 1u : 0u);
+            for (int k = 0; k < kTile / 16; ++k) mma_bf16_ta(d, a + k * 8, b + k * (2048 >> 4), ipv, k != 0 ? 1u : more);
             mma_commit(&sh.pv_done[s]);
             if (!two || s == 1) mma_commit(&sh.empty[slot]);
-            if (t + 2 < steps) qk(t + 2);
           }
-          rc += 2 * n;
-          qc += two + 1;
+          __syncwarp();
+          if (t + 2 < steps) qk(t + 2);
         }
-        mma_commit(&sh.drain);
-        drain_bar(&sh.drain, 0);  // no product in flight when TMEM is freed
+        rc += 2 * n;
+        qc += two + 1;
       }
+      if (elect_one()) mma_commit(&sh.drain);
+      __syncwarp();
+      drain_bar(&sh.drain, 0);  // no product in flight when TMEM is freed
       __syncwarp();
     } else if (warp == 2) {
       // ---------------------------------------------------------------- unseen V rows

@@ -203,6 +203,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// One lane of a fully active warp (the same one at every call). A warp that runs
+// its MMA loop with all lanes and issues under this keeps descriptors and
+// addresses in uniform registers; issued by a lane of a divergent branch, each
+// MMA has to move them there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] x B[smem]: A's rows are lanes, its bf16 elements two a column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
