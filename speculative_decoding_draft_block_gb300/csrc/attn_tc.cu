@@ -26,15 +26,22 @@
 //        stream, and both read each key tile from shared memory. Bound by the
 //        tensor core and the softmax. Units with one row tile run on stream 0.
 //
-//   warp 0      producer: TMA loads of Q tiles and of K and V tiles (one box per
-//               page and 64 elements, 128B-swizzled) into a ring of kSlots, in
-//               the order in which the MMA issuer uses them
-//   warp 1      MMA issuer: S = Q K^T (both in shared memory), O += P V (P in
-//               TMEM over its scores, V in shared memory, MN-major)
-//   warp 2      clears the V rows that no row sees in a unit's first and last
-//               tile: a weight of zero does not cancel a NaN in a matrix product
-//   warp 3      walks over the shares and hands the pieces of units to the others
+//   warps 0, 1  producers: walk over the share (solo: one a stream, with its K and
+//               V; pair: one for Q and K, one for V), hand its pieces to the softmax
+//               and load tiles by TMA (one box per page and 64 elements,
+//               128B-swizzled) into a ring of kSlots
+//   warps 2, 3  MMA issuers (solo: one a stream; pair: one for both): S = Q K^T (both in shared memory),
+//               O += P V (P in TMEM over its scores, V in shared memory, MN-major).
+//               What to do with a tile stands in the slot's info word. They also
+//               clear the V rows that no row sees in a unit's first and last tile:
+//               a weight of zero does not cancel a NaN in a matrix product
 //   warps 4-7, 8-11   softmax of streams 0 and 1: a thread a row
+//
+// With one producer and one issuer warp for both streams their waits, commits and
+// bookkeeping bound the solo form (4.6 TB/s, now 6.1).
+// The ring's entries stand in a fixed order, in which every role counts by itself:
+//   solo  K0 K1 | V0 K0' V1 K1' | V0' ...   (the streams' next tiles in turn)
+//   pair  K V K V ...
 //
 // TMEM (512 columns): scores 2 x 128, accumulators 2 x D. Every wait is bounded.
 #include <cuda.h>
@@ -56,7 +63,7 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kTile = 128;         // keys a tile, rows a tile
 constexpr float kSlack = 8.f;      // growth of the exponents that is left in the sums
-constexpr uint32_t kCtrlRegs = 72, kSoftRegs = 216, kLaunchRegs = 168;
+constexpr uint32_t kCtrlRegs = 88, kSoftRegs = 208, kLaunchRegs = 168;
 static_assert(128 * kCtrlRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr uint32_t kWaitPolls = 1u << 16;
 constexpr uint32_t kHeader = 2048;  // barriers and small records, before the tiles
@@ -85,20 +92,26 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 64, "four 16-byte words");
 
-struct Clear {
-  int slot, parity, head, tail;  // keep rows [head, tail) of the V tile
+// A ring slot's info word: what the entry is, and for a value tile the rows to keep.
+enum : uint32_t {
+  kNull = 1u,   // nothing: the stream has ended, the other one has not
+  kEnd = 2u,    // no more entries of this stream
+  kFirst = 4u,  // first tile of a piece
+  kLast = 8u,   // last tile of a piece
+  kTwo = 16u,   // the unit has two row tiles
+  kPart = 32u   // value tile: only rows [bits 8..15, bits 16..23) are seen
 };
 
 struct Header {
   Piece piece[2][kAhead];
-  Clear clear[kAhead];
   uint64_t piece_full[2][kAhead], piece_empty[2][kAhead];
-  uint64_t clear_full[kAhead], clear_empty[kAhead];
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t cleared[kMaxSlots];   // the slot's V tile has had its unseen rows cleared
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t drain;
+  uint64_t drain[2];
+  uint32_t info[kMaxSlots];
+  uint32_t entry[kMaxSlots];  // 1 + the number of the entry that the slot was last given to
+  int ended[2];         // tiles of a stream's share, -1 while not known
   uint32_t tmem;
   int abort_flag;
   int64_t scan[kThreads / 32];
@@ -106,6 +119,32 @@ struct Header {
   int start_b[2];
 };
 static_assert(sizeof(Header) <= kHeader, "header");
+
+// A role's place in the ring.
+//
+// A barrier's parity tells the phase that is awaited from the one before it and
+// no more, so a role may wait for an entry's filling (its release) only once it
+// knows that the slot's filling (release) before that one is over.
+//   - A pair's issuer passes every entry in order: it has waited for it.
+//   - The solo issuers pass their own stream's entries only, and with five slots
+//     the slot's last entry is the other stream's. So they wait for the entry's
+//     number in `entry` first: the producer writes it once the slot is released.
+//   - Producers wait for the release of the entry kSlots before theirs. The slot's
+//     entry before that, 2 * kSlots back, was released earlier: it is an earlier
+//     entry of the producer's own list or precedes, in its issuer's order, one
+//     whose release this producer has waited for (releases are commits, in order).
+template <int kSlots>
+struct RingPos {
+  uint32_t slot = 0, parity = 0, number = 0;
+  __device__ __forceinline__ void add(uint32_t n) {  // n < kSlots
+    number += n;
+    slot += n;
+    if (slot >= kSlots) {
+      slot -= kSlots;
+      parity ^= 1u;
+    }
+  }
+};
 
 // What the join needs to know of a cut unit: written by the share that begins it.
 struct CutUnit {
@@ -264,7 +303,7 @@ struct Walk {
       x.two = u.n_tok > per_tile;
       x.whole = x.n == u.n;
       x.slot = t0 > 0 ? 0 : 1;
-      if (!x.whole && x.slot == 1) {
+      if (cut != nullptr && !x.whole && x.slot == 1) {
         const CutUnit c = {u0, total, u.n, 1, x.token, x.n_tok, h, 0};
         *cut = c;
       }
@@ -278,23 +317,6 @@ struct Walk {
 __device__ __forceinline__ bool partly_seen(int tile, int lo, int hi) {
   return tile * kTile < lo || (tile + 1) * kTile > hi;
 }
-
-// A role's way through the pieces of one stream (all lanes).
-struct Pieces {
-  uint32_t k = 0;
-  __device__ __forceinline__ bool next(Header& sh, int stream, int lane, int32_t* status, Piece& x) {
-    const uint32_t i = k % kAhead;
-    if (!wait_bar(&sh.piece_full[stream][i], (k / kAhead) & 1, &sh.abort_flag, status, kIdlePolls)) return false;
-    const uint4* from = reinterpret_cast<const uint4*>(&sh.piece[stream][i]);
-    uint4* to = reinterpret_cast<uint4*>(&x);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) to[w] = from[w];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.piece_empty[stream][i]);
-    ++k;
-    return true;
-  }
-};
 
 // ---- packed float32 pairs ------------------------------------------------------------
 
@@ -372,21 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.drain[i], 1);
+      sh.ended[i] = -1;
       for (int k = 0; k < kAhead; ++k) {
         mbar_init(&sh.piece_full[i][k], 1);
-        mbar_init(&sh.piece_empty[i][k], kPair ? 10 : 6);  // producer, MMA issuer, softmax warps
+        mbar_init(&sh.piece_empty[i][k], kPair ? 8 : 4);  // softmax warps
       }
-    }
-    for (int i = 0; i < kAhead; ++i) {
-      mbar_init(&sh.clear_full[i], 1);
-      mbar_init(&sh.clear_empty[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
-      mbar_init(&sh.cleared[i], 1);
+      sh.entry[i] = 0;
     }
-    mbar_init(&sh.drain, 1);
     sh.abort_flag = 0;
     fence_barrier_init();
   }
@@ -442,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (F::begin(total, v0 + kLists - 1) < base) break;
   }
-  if (warp == 1) tmem_alloc(&sh.tmem, 512);
+  if (warp == 2) tmem_alloc(&sh.tmem, 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -451,188 +470,205 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kCtrlRegs>();
-    if (warp == 0) {
-      // ---------------------------------------------------------------- producer
+    if (warp < 2) {
+      // ---------------------------------------------------------------- producers
+      const int l = kPair ? 0 : warp;                      // share
+      const bool does_k = !kPair || warp == 0, does_v = !kPair || warp == 1;
       const int shift = p.pool.page_shift, page_size = 1 << shift;
-      const int rows = min(page_size, kTile);     // keys of a box
-      const int boxes = kTile / rows;             // pages a tile
+      const int rows = min(page_size, kTile);              // keys of a box
+      const int boxes = kTile / rows;                      // pages a tile
       const uint32_t box_bytes = (uint32_t)rows * 128u;
       if (lane == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
-      uint32_t rc = 0, qc[2] = {0, 0}, cc = 0;
+      Walk wk;
+      wk.start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.start_b[l], sh.start_base[l]);
+      if (does_k && lane == 0) part.cut[v0 + l].valid = 0;
+      RingPos<kSlots> kp, vp;                              // places of the next K and V entry
+      if (!kPair) kp.add(l);
+      vp.add(kPair ? 1 : l == 0 ? 2 : 4);
+      uint32_t q_par[2] = {1, 1}, np = 0;
+      int n_tiles = 0;                                     // of the share so far
       bool ok = true;
-      struct {
-        Pieces list;
-        const int32_t* table;
-        int h, lo, hi, tile, left;  // next key tile, tiles left with it
-        int page, v_page;           // this lane's page of the next key tile, of the value tile that is due
-        bool end;
-      } st[kLists];
+      Piece x = {};
+      const int32_t* table = nullptr;
       // page of this lane's box of a key tile, -1: no row of the unit sees it
-      auto page_of = [&](int l, int tile) {
+      auto page_of = [&](int tile) {
         const int key = tile * kTile + lane * rows;
-        if (lane >= boxes || key >= st[l].hi || key + rows <= st[l].lo) return -1;
-        const int page = __ldg(st[l].table + (key >> shift));
+        if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return -1;
+        const int page = __ldg(table + (key >> shift));
         if (page >= 0 && page < p.pool.n_pages) return page;
         report(p.status, kErrBounds);
         return 0;
       };
-      auto load = [&](const CUtensorMap* map, int l, int tile, int page, bool is_v) {
-        const uint32_t s = rc % kSlots;
-        ok = wait_bar(&sh.empty[s], ((rc / kSlots) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) return;
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (lane == 0) mbar_expect_tx(&sh.full[s], n * kHalves * box_bytes);
-        __syncwarp();
-        if (page >= 0) {
-          uint8_t* dst = sRing + s * L::kTileBytes + lane * box_bytes;
-          const int token = (tile * kTile + lane * rows) & (page_size - 1);
-#pragma unroll
-          for (int x = 0; x < kHalves; ++x)
-            tma_load_4d_plain(dst + x * (kTile * 128), map, &sh.full[s], x * 64, token, st[l].h, page);
-        }
-        if (is_v && partly_seen(tile, st[l].lo, st[l].hi)) {
-          ok = wait_bar(&sh.clear_empty[cc % kAhead], ((cc / kAhead) & 1) ^ 1, abort_flag, p.status);
-          if (!ok) return;
-          if (lane == 0) {
-            const Clear c = {(int)s, (int)((rc / kSlots) & 1), max(0, st[l].lo - tile * kTile),
-                             min(kTile, st[l].hi - tile * kTile)};
-            sh.clear[cc % kAhead] = c;
-            mbar_arrive(&sh.clear_full[cc % kAhead]);
-          }
-          ++cc;
-        }
-        ++rc;
+      auto wait_empty = [&](const RingPos<kSlots>& at) {
+        ok = wait_bar(&sh.empty[at.slot], at.parity ^ 1, abort_flag, p.status);
+        return ok;
       };
-      auto load_q = [&](int s, const Piece& x) {
-        const int token = x.token + (kPair ? s * per_tile : 0);
-        ok = wait_bar(&sh.q_empty[s], (qc[s] & 1) ^ 1, abort_flag, p.status);
-        if (!ok) return;
+      auto load = [&](const CUtensorMap* map, const RingPos<kSlots>& at, int tile, int page, uint32_t info) {
+        if (!wait_empty(at)) return;
+        const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) {
-          mbar_expect_tx(&sh.q_full[s], (uint32_t)per_tile * p.group * D * 2);
-          for (int y = 0; y < kHalves; ++y)
-            tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128), &tmQ, &sh.q_full[s], y * 64, x.h * p.group,
-                              token);
+          sh.info[at.slot] = info;
+          *(volatile uint32_t*)&sh.entry[at.slot] = at.number + 1;
+          mbar_expect_tx(&sh.full[at.slot], __popc(some) * kHalves * box_bytes);
         }
-        ++qc[s];
-      };
-      // the next key tile of list l, with Q where a piece begins
-      auto load_k = [&](int l) {
-        if (st[l].left == 0) {
-          Piece x;
-          do {
-            ok = st[l].list.next(sh, l, lane, p.status, x);
-          } while (ok && x.n == 0);
-          if (!ok) return;
-          st[l].end = x.n < 0;
-          if (st[l].end) return;
-          st[l].table = p.block_table + (int64_t)x.b * p.max_pages;
-          st[l].h = x.h;
-          st[l].lo = x.lo;
-          st[l].hi = x.hi;
-          st[l].tile = x.tile0;
-          st[l].left = x.n;
-          st[l].page = page_of(l, x.tile0);
-          load_q(l, x);
-          if (kPair && ok && x.two) load_q(1, x);
-          if (!ok) return;
-        }
-        const int page = st[l].page, tile = st[l].tile++;
-        st[l].v_page = page;
-        if (--st[l].left > 0) st[l].page = page_of(l, tile + 1);
-        load(&tmK, l, tile, page, false);
-      };
-      for (int l = 0; l < kLists; ++l) {
-        st[l].left = 0;
-        st[l].end = false;
-      }
-      bool more = true;
+        __syncwarp();
+        uint8_t* dst = sRing + at.slot * L::kTileBytes;
+        const int token = (tile * kTile) & (page_size - 1);
+        for (int i = 0; i < boxes; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, i);
+          if (pg >= 0 && elect_one()) {
 #pragma unroll
-      for (int l = 0; l < kLists; ++l)
-        if (ok) load_k(l);
-      while (ok && more) {
-        more = false;
-#pragma unroll
-        for (int l = 0; l < kLists; ++l) {
-          if (!ok || st[l].end) continue;
-          load(&tmV, l, st[l].tile - 1, st[l].v_page, true);
-          if (ok) load_k(l);
-          more |= !st[l].end;
+            for (int y = 0; y < kHalves; ++y)
+              tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[at.slot], y * 64, token, x.h, pg);
+          }
+          __syncwarp();
+        }
+      };
+      // an entry without a tile
+      auto mark = [&](const RingPos<kSlots>& at, uint32_t info) {
+        if (lane == 0) {
+          sh.info[at.slot] = info;
+          *(volatile uint32_t*)&sh.entry[at.slot] = at.number + 1;
+          mbar_arrive(&sh.full[at.slot]);
+        }
+        __syncwarp();
+      };
+      auto next_k = [&] {
+        // (solo: K0 is followed by three other entries' places, then by four)
+        kp.add(kPair ? 2 : l == 0 && n_tiles == 1 ? 3 : 4);
+      };
+      while (ok) {
+        x = wk.next(p, unit_tokens, per_tile, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
+        if (does_k) {  // to the softmax
+          const uint32_t i = np % kAhead;
+          ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, p.status, kIdlePolls);
+          if (!ok) break;
+          if (lane == 0) {
+            sh.piece[l][i] = x;
+            mbar_arrive(&sh.piece_full[l][i]);
+          }
+          ++np;
+        }
+        if (x.n < 0) break;
+        if (x.n == 0) continue;
+        table = p.block_table + (int64_t)x.b * p.max_pages;
+        int page = page_of(x.tile0);
+        if (does_k) {
+          for (int s = kPair ? 0 : l; s <= (kPair ? x.two : l); ++s) {
+            ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], abort_flag, p.status);
+            if (!ok) break;
+            if (s == 0) q_par[0] ^= 1;
+            if (s == 1) q_par[1] ^= 1;
+            if (elect_one()) {
+              mbar_expect_tx(&sh.q_full[s], (uint32_t)per_tile * p.group * D * 2);
+              for (int y = 0; y < kHalves; ++y)
+                tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128), &tmQ, &sh.q_full[s], y * 64, x.h * p.group,
+                                  x.token + (kPair ? s * per_tile : 0));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        const uint32_t base_info = x.two ? kTwo : 0u;
+        for (int j = 0; j < x.n && ok; ++j) {
+          const int tile = x.tile0 + j, now = page;
+          const uint32_t info = base_info | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
+          if (j + 1 < x.n) page = page_of(tile + 1);
+          if (does_k) {
+            load(&tmK, kp, tile, now, info);
+            if (!ok) break;
+          }
+          ++n_tiles;
+          next_k();
+          if (does_v) {
+            uint32_t vi = info;
+            if (partly_seen(tile, x.lo, x.hi))
+              vi |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
+            load(&tmV, vp, tile, now, vi);
+            vp.add(kPair ? 2 : 4);
+          }
         }
       }
-      if (ok) ok = wait_bar(&sh.clear_empty[cc % kAhead], ((cc / kAhead) & 1) ^ 1, abort_flag, p.status);
-      if (ok && lane == 0) {
-        sh.clear[cc % kAhead].slot = -1;  // no more
-        mbar_arrive(&sh.clear_full[cc % kAhead]);
-      }
-      // nothing of this CTA may be in flight when it exits (also after an abort)
-      if (lane == 0) {
-        for (uint32_t j = rc > kSlots ? rc - kSlots : 0; j < rc; ++j) drain_bar(&sh.full[j % kSlots], (j / kSlots) & 1);
-        for (int s = 0; s < 2; ++s)
-          if (qc[s] > 0) drain_bar(&sh.q_full[s], (qc[s] - 1) & 1);
+      if (kPair) {
+        if (ok && does_k && wait_empty(kp)) mark(kp, kEnd);
+      } else if (ok) {
+        // The other stream may have more tiles: fill this one's places until both have
+        // ended. Whether the other has is read after the wait for a slot: what is
+        // waited for may be the other's last entry, and no entry follows that one.
+        volatile int* ended = sh.ended;
+        if (lane == 0) ended[l] = n_tiles;
+        while (wait_empty(kp)) {
+          const int other = __shfl_sync(0xffffffffu, ended[l ^ 1], 0);
+          const bool end = other >= 0 && n_tiles >= other;
+          mark(kp, end ? kEnd : kNull);
+          if (end) break;
+          ++n_tiles;
+          next_k();
+          if (!wait_empty(vp)) break;
+          mark(vp, kNull);
+          vp.add(4);
+        }
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ---------------------------------------------------------------- MMA issuer
+    } else {
+      // ---------------------------------------------------------------- MMA issuers
       // (all lanes run the loop, one issues)
       constexpr uint32_t iqk = idesc_bf16(kTile, kTile, false, false);
       constexpr uint32_t ipv = idesc_bf16(kTile, D, false, true);
       constexpr uint64_t kbits = smem_desc_bits(16, 1024, 2);
       constexpr uint64_t vbits = smem_desc_bits(kTile * 128, 1024, 2);
+      const int s0 = kPair ? 0 : warp - 2;  // the issuer's stream (a pair's has both)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t q_desc = smem_desc(sQ, kbits), k_desc = smem_desc(sRing, kbits), v_desc = smem_desc(sRing, vbits);
-      uint32_t slot = 0, phase = 0;                       // the ring's next slot, its phase
-      uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0}, c_parity = 0;
-      bool ok = true;
-      Pieces list[kLists];
-      // the list's next key tile; `first` of its piece; `part`: some of its keys unseen
-      int lo[kLists], hi[kLists], tile[kLists], left[kLists];
-      bool two = false, end[kLists];
-      auto advance = [&](int l, bool& first, bool& part) {
-        first = left[l] == 0;
-        if (first) {
-          Piece x;
-          do {
-            ok = list[l].next(sh, l, lane, p.status, x);
-          } while (ok && x.n == 0);
-          end[l] = !ok || x.n < 0;
-          if (end[l]) return;
-          lo[l] = x.lo;
-          hi[l] = x.hi;
-          tile[l] = x.tile0;
-          left[l] = x.n;
-          two = kPair && x.two;
+      RingPos<kSlots> kp, vp;
+      if (!kPair) kp.add(s0);
+      vp.add(kPair ? 1 : s0 == 0 ? 2 : 4);
+      uint32_t q_par = 0, p_par = 0;  // a bit a stream
+      bool ok = true, begun = false;
+      // waits for the entry at `at`; its info word
+      auto take = [&](const RingPos<kSlots>& at) {
+        if (!kPair) {
+          volatile uint32_t* entry = &sh.entry[at.slot];
+          for (uint32_t i = 0; !__all_sync(0xffffffffu, *entry == at.number + 1); ++i) {
+            __nanosleep(40);
+            if ((i & 255) == 255) {
+              if (i > (kWaitPolls << 8)) {
+                *abort_flag = 1;
+                report(p.status, kErrTimeout);
+              }
+              if (__any_sync(0xffffffffu, *abort_flag)) {
+                ok = false;
+                return (uint32_t)kEnd;
+              }
+            }
+          }
         }
-        part = partly_seen(tile[l], lo[l], hi[l]);
-        ++tile[l];
-        --left[l];
+        ok = wait_bar(&sh.full[at.slot], at.parity, abort_flag, p.status);
+        return ok ? __shfl_sync(0xffffffffu, *(volatile uint32_t*)&sh.info[at.slot], 0) : (uint32_t)kEnd;
+      };
+      auto next_k = [&] {
+        kp.add(kPair ? 2 : s0 == 0 && !begun ? 3 : 4);
+        begun = true;
+      };
+      auto next_v = [&] { vp.add(kPair ? 2 : 4); };
+      // releases an entry that was not used, after those before it
+      auto release = [&](const RingPos<kSlots>& at) {
+        if (elect_one()) mma_commit(&sh.empty[at.slot]);
+        __syncwarp();
       };
       auto wait_q = [&](int s) {
-        ok = ok && wait_bar(&sh.q_full[s], q_par[s], abort_flag, p.status);
-        q_par[s] ^= 1;
+        ok = ok && wait_bar(&sh.q_full[s], (q_par >> s) & 1, abort_flag, p.status);
+        q_par ^= 1u << s;
       };
-      // the ring's next tile; its slot
-      auto take = [&](bool part) {
-        const uint32_t at = __shfl_sync(0xffffffffu, slot, 0);
-        ok = ok && wait_bar(&sh.full[at], phase, abort_flag, p.status);
-        if (part) {
-          ok = ok && wait_bar(&sh.cleared[at], (c_parity >> at) & 1, abort_flag, p.status);
-          c_parity ^= 1u << at;
-        }
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1;
-        }
-        return at;
-      };
-      // S = Q K^T of stream s; `free_k`, `free_q`: the last products that read them
-      auto qk = [&](int s, uint32_t at, bool free_k, bool free_q) {
+      // S = Q K^T of stream s with the keys in `slot`; `free_k`: no other stream reads them
+      auto qk = [&](int s, uint32_t slot, bool last, bool free_k) {
         if (!ok) return;
         tc_fence_after();
-        const uint64_t a = q_desc + s * (L::kTileBytes >> 4), b = k_desc + at * (L::kTileBytes >> 4);
+        const uint64_t a = q_desc + s * (L::kTileBytes >> 4), b = k_desc + slot * (L::kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -640,170 +676,121 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_bf16(tm + s * kTile, a + off, b + off, iqk, k != 0);
           }
           mma_commit(&sh.s_full[s]);
-          if (free_k) mma_commit(&sh.empty[at]);
-          if (free_q) mma_commit(&sh.q_empty[s]);
+          if (free_k) mma_commit(&sh.empty[slot]);
+          if (last) mma_commit(&sh.q_empty[s]);
         }
         __syncwarp();
       };
-      // O (+)= P V of stream s, `last` of its piece
-      auto pv = [&](int s, uint32_t at, bool first, bool last, bool free_v) {
-        ok = ok && wait_bar(&sh.p_full[s], p_par[s], abort_flag, p.status);
+      // O (+)= P V of stream s with the values in `slot`
+      auto pv = [&](int s, uint32_t slot, bool first, bool last, bool free_v) {
+        ok = ok && wait_bar(&sh.p_full[s], (p_par >> s) & 1, abort_flag, p.status);
         if (!ok) return;
-        p_par[s] ^= 1;
+        p_par ^= 1u << s;
         tc_fence_after();
-        const uint64_t b = v_desc + at * (L::kTileBytes >> 4);
+        const uint64_t b = v_desc + slot * (L::kTileBytes >> 4);
         const uint32_t more = first ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             mma_bf16_ta(tm + 256 + s * D, tm + s * kTile + k * 8, b + k * (2048 >> 4), ipv, k != 0 ? 1u : more);
-          if (free_v) mma_commit(&sh.empty[at]);
+          if (free_v) mma_commit(&sh.empty[slot]);
           if (last) mma_commit(&sh.pv_done[s]);
         }
         __syncwarp();
       };
-#pragma unroll
-      for (int l = 0; l < kLists; ++l) {
-        left[l] = 0;
-        end[l] = false;
-      }
-      // Order of the products: S0 S1 | O0 S0' O1 S1' | ...: a stream's scores are
-      // made while the other's go through the softmax. The ring's order follows.
-      if (!kPair) {
-        bool first[2], part[2];
-        auto step_k = [&](int l) {
-          advance(l, first[l], part[l]);
-          if (end[l]) return;
-          if (first[l]) wait_q(l);
-          const uint32_t at = take(false);
-          qk(l, at, true, left[l] == 0);
-        };
-#pragma unroll
-        for (int l = 0; l < kLists; ++l) step_k(l);
-        while (ok && !(end[0] && end[kLists - 1])) {
-#pragma unroll
-          for (int l = 0; l < kLists; ++l) {
-            if (!ok || end[l]) continue;
-            const uint32_t at = take(part[l]);
-            pv(l, at, first[l], left[l] == 0, true);
-            step_k(l);
-          }
-        }
-      } else {
-        bool first, part;
-        advance(0, first, part);
-        if (!end[0]) {
-          wait_q(0);
-          const uint32_t at = take(false);
-          qk(0, at, !two, left[0] == 0);
-          if (two) {
-            wait_q(1);
-            qk(1, at, true, left[0] == 0);
-          }
-        }
-        while (ok && !end[0]) {
-          const bool both = two, from = first, last = left[0] == 0;
-          const uint32_t v_at = take(part);
-          if (!last) {
-            // within a piece: the next keys are waited for first, so that the
-            // products follow each other without a wait but for the weights
-            advance(0, first, part);
-            const uint32_t k_at = take(false);
-            pv(0, v_at, from, false, !both);
-            qk(0, k_at, !both, left[0] == 0);
-            if (both) {
-              pv(1, v_at, from, false, true);
-              qk(1, k_at, true, left[0] == 0);
-            }
-          } else {
-            pv(0, v_at, from, true, !both);
-            if (both) pv(1, v_at, from, true, true);
-            if (!ok) break;
-            advance(0, first, part);
-            if (end[0]) break;
-            wait_q(0);
-            const uint32_t k_at = take(false);
-            qk(0, k_at, !two, left[0] == 0);
-            if (two) {
-              wait_q(1);
-              qk(1, k_at, true, left[0] == 0);
-            }
-          }
-        }
-      }
-      if (elect_one()) mma_commit(&sh.drain);
-      __syncwarp();
-      drain_bar(&sh.drain, 0);  // no product in flight when TMEM is freed
-      __syncwarp();
-    } else if (warp == 2) {
-      // ---------------------------------------------------------------- unseen V rows
-      // (a slot's barrier tells a filling from the next one, not from the one after:
-      // its parity is good here because the producer has begun this filling, and does
-      // not begin the next before the MMA issuer has seen `cleared`)
-      for (uint32_t k = 0;; ++k) {
-        const uint32_t i = k % kAhead;
-        if (!wait_bar(&sh.clear_full[i], (k / kAhead) & 1, abort_flag, p.status, kIdlePolls)) break;
-        const Clear c = sh.clear[i];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.clear_empty[i]);
-        if (c.slot < 0) break;
-        if (!wait_bar(&sh.full[c.slot], c.parity, abort_flag, p.status)) break;
-        uint8_t* tile = sRing + c.slot * L::kTileBytes;
+      // clears the rows of the value tile in `slot` that no row sees
+      auto clear = [&](uint32_t slot, uint32_t info) {
+        const int head = (info >> 8) & 255, tail = (info >> 16) & 255;
+        uint8_t* tile = sRing + slot * L::kTileBytes;
         for (int half = 0; half < kHalves; ++half) {
           uint4* v = reinterpret_cast<uint4*>(tile + half * (kTile * 128));
-          for (int j = lane; j < c.head * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
-          for (int j = c.tail * 8 + lane; j < kTile * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
+          for (int j = lane; j < head * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
+          for (int j = tail * 8 + lane; j < kTile * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.cleared[c.slot]);
-      }
-    } else {
-      // ---------------------------------------------------------------- the shares' pieces
-      // (one lane serves the lists in turn without blocking: a list that is full must
-      // not keep the other one empty)
-      if (lane == 0) {
-        Walk wk[kLists];
-        Piece x[kLists];
-        uint32_t k[kLists];
-        int done = 0;
-#pragma unroll
-        for (int l = 0; l < kLists; ++l) {
-          wk[l].start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.start_b[l], sh.start_base[l]);
-          part.cut[v0 + l].valid = 0;
-          x[l] = wk[l].next(p, unit_tokens, per_tile, part.cut + v0 + l, total);
-          k[l] = 0;
+      };
+      auto uniform = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      if (!kPair) {
+        uint32_t info = take(kp);
+        while (ok) {
+          if (info & kEnd) {
+            release(kp);
+            break;
+          }
+          if (info & kNull) {
+            release(kp);
+            next_k();
+            take(vp);
+            if (!ok) break;
+            release(vp);
+          } else {
+            if (info & kFirst) wait_q(s0);
+            qk(s0, uniform(kp.slot), info & kLast, true);
+            next_k();
+            const uint32_t vi = take(vp);
+            if (!ok) break;
+            if (vi & kPart) clear(vp.slot, vi);
+            pv(s0, uniform(vp.slot), vi & kFirst, vi & kLast, true);
+          }
+          next_v();
+          if (ok) info = take(kp);
         }
-        for (uint32_t idle = 0; done < kLists && idle < (kIdlePolls << 3);) {
-          bool moved = false;
-#pragma unroll
-          for (int l = 0; l < kLists; ++l) {
-            const uint32_t i = k[l] % kAhead;
-            if (k[l] == 0xffffffffu || !mbar_test_wait(&sh.piece_empty[l][i], ((k[l] / kAhead) & 1) ^ 1)) continue;
-            moved = true;
-            sh.piece[l][i] = x[l];
-            mbar_arrive(&sh.piece_full[l][i]);
-            if (x[l].n < 0) {
-              k[l] = 0xffffffffu;
-              ++done;
-            } else {
-              ++k[l];
-              x[l] = wk[l].next(p, unit_tokens, per_tile, part.cut + v0 + l, total);
+      } else if (warp == 2) {
+        // S0 S1 | O0 S0' O1 S1' | ...: a stream's scores are made while the other's go
+        // through the softmax. One warp for both streams: products of two warps
+        // interleave on the tensor core and take longer (1.01 against 1.31 PFLOP/s).
+        uint32_t info = take(kp);
+        while (ok) {
+          if (info & kEnd) {
+            release(kp);
+            break;
+          }
+          // a new piece
+          const bool two = info & kTwo;
+          bool last = info & kLast;
+          {
+            const uint32_t slot = uniform(kp.slot);
+            wait_q(0);
+            qk(0, slot, last, !two);
+            if (two) {
+              wait_q(1);
+              qk(1, slot, last, true);
             }
           }
-          if (moved) {
-            idle = 0;
-          } else {
-            ++idle;
-            if ((idle & 63) == 0 && *abort_flag) break;
-            __nanosleep(100);
+          next_k();
+          bool first = true;
+          while (ok) {
+            const uint32_t vi = take(vp);
+            if (!ok) break;
+            const uint32_t v_at = uniform(vp.slot);
+            if (vi & kPart) clear(v_at, vi);
+            next_v();
+            if (last) {
+              pv(0, v_at, first, true, !two);
+              if (two) pv(1, v_at, first, true, true);
+              break;
+            }
+            // the next keys are there as a rule: wait for them before the weights, so
+            // that the products follow each other with waits for weights only
+            info = take(kp);
+            last = info & kLast;
+            const uint32_t k_at = uniform(kp.slot);
+            pv(0, v_at, first, false, !two);
+            qk(0, k_at, last, !two);
+            if (two) {
+              pv(1, v_at, first, false, true);
+              qk(1, k_at, last, true);
+            }
+            next_k();
+            first = false;
           }
-        }
-        if (done < kLists && !*abort_flag) {
-          *abort_flag = 1;
-          report(p.status, kErrTimeout);
+          if (ok) info = take(kp);
         }
       }
+      if (elect_one()) mma_commit(&sh.drain[warp - 2]);
+      __syncwarp();
+      drain_bar(&sh.drain[warp - 2], 0);  // no product in flight when TMEM is freed
       __syncwarp();
     }
   } else {
@@ -817,9 +804,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_tok = row / p.group, g = row - tile_tok * p.group;
     const int v = v0 + (kPair ? 0 : s);            // share
     uint32_t ns = 0, np = 0;                       // score tiles and pieces so far
-    Pieces list;
-    Piece x;
-    while (list.next(sh, kPair ? 0 : s, lane, p.status, x) && x.n >= 0) {
+    const int list = kPair ? 0 : s;
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t at = k % kAhead;
+      if (!wait_bar(&sh.piece_full[list][at], (k / kAhead) & 1, abort_flag, p.status, kIdlePolls)) break;
+      const Piece x = sh.piece[list][at];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.piece_empty[list][at]);
+      if (x.n < 0) break;
       if (kPair && s == 1 && !x.two) continue;
       const int i = (kPair ? s * per_tile : 0) + tile_tok;  // token of the unit
       const bool valid = tile_tok < per_tile && i < x.n_tok;
@@ -953,7 +945,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  // Each load has been waited for by an issuer, except after an abort: then wait
+  // (with a limit) until nothing can be in flight when the CTA exits.
+  if (*abort_flag)
+    for (int i = 0; i < 64; ++i) __nanosleep(20000);
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
