@@ -92,14 +92,15 @@ struct Piece {
 };
 static_assert(sizeof(Piece) == 64, "four 16-byte words");
 
-// A ring slot's info word: what the entry is, and for a value tile the rows to keep.
+// A ring slot's info word, for key entries: what this entry and the value entry
+// of the same tile are.
 enum : uint32_t {
   kNull = 1u,   // nothing: the stream has ended, the other one has not
   kEnd = 2u,    // no more entries of this stream
   kFirst = 4u,  // first tile of a piece
   kLast = 8u,   // last tile of a piece
   kTwo = 16u,   // the unit has two row tiles
-  kPart = 32u   // value tile: only rows [bits 8..15, bits 16..23) are seen
+  kPart = 32u   // only keys [bits 8..15, bits 16..23) of the tile are seen
 };
 
 struct Header {
@@ -187,14 +188,16 @@ struct Form {
 constexpr uint32_t kIdlePolls = 1u << 22;
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
                                          uint32_t polls) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t i = 0; i < polls; ++i) {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    if ((i & 15) == 15 && *abort_flag) return false;
+#pragma unroll 1
+  for (uint32_t i = 0; !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {
+    if ((i & 15) != 15) continue;
+    if (i >= polls) {
+      *abort_flag = 1;
+      report(status, kErrTimeout);
+    }
+    if (*abort_flag) return false;
   }
-  *abort_flag = 1;
-  report(status, kErrTimeout);
-  return false;
+  return true;
 }
 
 // The same by a whole warp, with one answer for all lanes: warp-wide instructions follow.
@@ -518,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         uint8_t* dst = sRing + at.slot * L::kTileBytes;
         const int token = (tile * kTile) & (page_size - 1);
+#pragma unroll 1
         for (int i = 0; i < boxes; ++i) {
           const int pg = __shfl_sync(0xffffffffu, page, i);
           if (pg >= 0 && elect_one()) {
@@ -573,22 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        const uint32_t base_info = x.two ? kTwo : 0u;
         for (int j = 0; j < x.n && ok; ++j) {
           const int tile = x.tile0 + j, now = page;
-          const uint32_t info = base_info | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
           if (j + 1 < x.n) page = page_of(tile + 1);
           if (does_k) {
+            uint32_t info = (x.two ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
+            if (partly_seen(tile, x.lo, x.hi))
+              info |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
             load(&tmK, kp, tile, now, info);
             if (!ok) break;
           }
           ++n_tiles;
           next_k();
           if (does_v) {
-            uint32_t vi = info;
-            if (partly_seen(tile, x.lo, x.hi))
-              vi |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
-            load(&tmV, vp, tile, now, vi);
+            load(&tmV, vp, tile, now, 0);
             vp.add(kPair ? 2 : 4);
           }
         }
@@ -628,164 +630,188 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kPair) kp.add(s0);
       vp.add(kPair ? 1 : s0 == 0 ? 2 : 4);
       uint32_t q_par = 0, p_par = 0;  // a bit a stream
-      bool ok = true, begun = false;
-      // waits for the entry at `at`; its info word
-      auto take = [&](const RingPos<kSlots>& at) {
+      bool begun = false;
+      auto uniform = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      // The waits stand with the products in one region of the elected lane: a
+      // warp-wide wait with its vote costs the issuer 200 cycles and more, as much
+      // as three products. `good`: no wait has given up (that lane's flag).
+      bool good = true;
+      auto wait1 = [&](uint64_t* bar, uint32_t parity) {
+        good = good && wait_one(bar, parity, abort_flag, p.status, kWaitPolls);
+      };
+      auto wait_entry = [&](const RingPos<kSlots>& at) {
         if (!kPair) {
           volatile uint32_t* entry = &sh.entry[at.slot];
-          for (uint32_t i = 0; !__all_sync(0xffffffffu, *entry == at.number + 1); ++i) {
+          for (uint32_t i = 0; good && *entry != at.number + 1; ++i) {
             __nanosleep(40);
-            if ((i & 255) == 255) {
-              if (i > (kWaitPolls << 8)) {
-                *abort_flag = 1;
-                report(p.status, kErrTimeout);
-              }
-              if (__any_sync(0xffffffffu, *abort_flag)) {
-                ok = false;
-                return (uint32_t)kEnd;
-              }
+            if ((i & 255) == 255 && *abort_flag) good = false;
+            if (i > (kWaitPolls << 8)) {
+              *abort_flag = 1;
+              report(p.status, kErrTimeout);
+              good = false;
             }
           }
         }
-        ok = wait_bar(&sh.full[at.slot], at.parity, abort_flag, p.status);
-        return ok ? __shfl_sync(0xffffffffu, *(volatile uint32_t*)&sh.info[at.slot], 0) : (uint32_t)kEnd;
+        wait1(&sh.full[at.slot], at.parity);
       };
+      // S = Q K^T of stream s with the keys in `slot`; `free_k`: no other stream reads them
+      auto qk = [&](int s, uint32_t slot, bool last, bool free_k) {
+        if (!good) return;
+        tc_fence_after();
+        const uint64_t a = q_desc + s * (L::kTileBytes >> 4), b = k_desc + slot * (L::kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
+          mma_bf16(tm + s * kTile, a + off, b + off, iqk, k != 0);
+        }
+        mma_commit(&sh.s_full[s]);
+        if (free_k) mma_commit(&sh.empty[slot]);
+        if (last) mma_commit(&sh.q_empty[s]);
+      };
+      // O (+)= P V of stream s with the values in `slot`
+      auto pv = [&](int s, uint32_t slot, bool first, bool last, bool free_v) {
+        wait1(&sh.p_full[s], (p_par >> s) & 1);
+        if (!good) return;
+        tc_fence_after();
+        const uint64_t b = v_desc + slot * (L::kTileBytes >> 4);
+        const uint32_t more = first ? 0u : 1u;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_bf16_ta(tm + 256 + s * D, tm + s * kTile + k * 8, b + k * (2048 >> 4), ipv, k != 0 ? 1u : more);
+        if (free_v) mma_commit(&sh.empty[slot]);
+        if (last) mma_commit(&sh.pv_done[s]);
+      };
+      // within a region: the info word of the entry at `at`, or, after a wait that has
+      // given up, an end without an entry; after it, that word for all lanes
+      auto info_of = [&](const RingPos<kSlots>& at) {
+        return good ? *(volatile uint32_t*)&sh.info[at.slot] : (uint32_t)(kEnd | kNull);
+      };
+      auto share_info = [&](uint32_t word) { return __reduce_or_sync(0xffffffffu, word); };
       auto next_k = [&] {
         kp.add(kPair ? 2 : s0 == 0 && !begun ? 3 : 4);
         begun = true;
       };
       auto next_v = [&] { vp.add(kPair ? 2 : 4); };
-      // releases an entry that was not used, after those before it
-      auto release = [&](const RingPos<kSlots>& at) {
-        if (elect_one()) mma_commit(&sh.empty[at.slot]);
+      // clears the rows of the value tile at vp that no row sees
+      auto clear = [&](uint32_t info) {
+        if (elect_one()) wait_entry(vp);
         __syncwarp();
-      };
-      auto wait_q = [&](int s) {
-        ok = ok && wait_bar(&sh.q_full[s], (q_par >> s) & 1, abort_flag, p.status);
-        q_par ^= 1u << s;
-      };
-      // S = Q K^T of stream s with the keys in `slot`; `free_k`: no other stream reads them
-      auto qk = [&](int s, uint32_t slot, bool last, bool free_k) {
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t a = q_desc + s * (L::kTileBytes >> 4), b = k_desc + slot * (L::kTileBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
-            mma_bf16(tm + s * kTile, a + off, b + off, iqk, k != 0);
-          }
-          mma_commit(&sh.s_full[s]);
-          if (free_k) mma_commit(&sh.empty[slot]);
-          if (last) mma_commit(&sh.q_empty[s]);
-        }
-        __syncwarp();
-      };
-      // O (+)= P V of stream s with the values in `slot`
-      auto pv = [&](int s, uint32_t slot, bool first, bool last, bool free_v) {
-        ok = ok && wait_bar(&sh.p_full[s], (p_par >> s) & 1, abort_flag, p.status);
-        if (!ok) return;
-        p_par ^= 1u << s;
-        tc_fence_after();
-        const uint64_t b = v_desc + slot * (L::kTileBytes >> 4);
-        const uint32_t more = first ? 0u : 1u;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ta(tm + 256 + s * D, tm + s * kTile + k * 8, b + k * (2048 >> 4), ipv, k != 0 ? 1u : more);
-          if (free_v) mma_commit(&sh.empty[slot]);
-          if (last) mma_commit(&sh.pv_done[s]);
-        }
-        __syncwarp();
-      };
-      // clears the rows of the value tile in `slot` that no row sees
-      auto clear = [&](uint32_t slot, uint32_t info) {
+        if (__any_sync(0xffffffffu, *abort_flag)) return;
         const int head = (info >> 8) & 255, tail = (info >> 16) & 255;
-        uint8_t* tile = sRing + slot * L::kTileBytes;
+        uint8_t* tile = sRing + vp.slot * L::kTileBytes;
+#pragma unroll 1
         for (int half = 0; half < kHalves; ++half) {
           uint4* v = reinterpret_cast<uint4*>(tile + half * (kTile * 128));
+#pragma unroll 1
           for (int j = lane; j < head * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
           for (int j = tail * 8 + lane; j < kTile * 8; j += 32) v[j] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
       };
-      auto uniform = [&](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
       if (!kPair) {
-        uint32_t info = take(kp);
-        while (ok) {
+        // S | O S' | O' S'' ...: a region does the product with the weights and the next scores
+        uint32_t next = 0;
+        if (elect_one()) {
+          wait_entry(kp);
+          next = info_of(kp);
+          if (!(next & (kNull | kEnd))) {
+            wait1(&sh.q_full[s0], q_par);
+            qk(s0, kp.slot, next & kLast, true);
+          }
+        }
+        uint32_t info = share_info(next);
+        while (true) {
           if (info & kEnd) {
-            release(kp);
+            if (!(info & kNull) && elect_one()) mma_commit(&sh.empty[kp.slot]);
+            __syncwarp();
             break;
           }
-          if (info & kNull) {
-            release(kp);
-            next_k();
-            take(vp);
-            if (!ok) break;
-            release(vp);
-          } else {
-            if (info & kFirst) wait_q(s0);
-            qk(s0, uniform(kp.slot), info & kLast, true);
-            next_k();
-            const uint32_t vi = take(vp);
-            if (!ok) break;
-            if (vi & kPart) clear(vp.slot, vi);
-            pv(s0, uniform(vp.slot), vi & kFirst, vi & kLast, true);
+          const uint32_t k_was = uniform(kp.slot);
+          next_k();
+          const uint32_t k_at = uniform(kp.slot), v_at = uniform(vp.slot);
+          if (info & kFirst) q_par ^= 1;
+          if ((info & (kPart | kNull)) == kPart) clear(info);
+          next = 0;
+          if (elect_one()) {
+            if (info & kNull) {  // releases of unused entries, after those before them
+              mma_commit(&sh.empty[k_was]);
+              wait_entry(vp);
+              if (good) mma_commit(&sh.empty[v_at]);
+            } else {
+              wait_entry(vp);
+              pv(s0, v_at, info & kFirst, info & kLast, true);
+            }
+            wait_entry(kp);
+            next = info_of(kp);
+            if (!(next & (kNull | kEnd))) {
+              if (next & kFirst) wait1(&sh.q_full[s0], q_par);
+              qk(s0, k_at, next & kLast, true);
+            }
           }
+          if (!(info & kNull)) p_par ^= 1u << s0;
           next_v();
-          if (ok) info = take(kp);
+          info = share_info(next);
         }
       } else if (warp == 2) {
         // S0 S1 | O0 S0' O1 S1' | ...: a stream's scores are made while the other's go
         // through the softmax. One warp for both streams: products of two warps
         // interleave on the tensor core and take longer (1.01 against 1.31 PFLOP/s).
-        uint32_t info = take(kp);
-        while (ok) {
+        auto scores = [&](int s, uint32_t at, uint32_t info) {
+          const bool two = info & kTwo;
+          if (s == 1 && !two) return;
+          if (info & kFirst) wait1(&sh.q_full[s], (q_par >> s) & 1);
+          qk(s, at, info & kLast, s == 1 || !two);
+        };
+        uint32_t next = 0;
+        if (elect_one()) {
+          wait_entry(kp);
+          next = info_of(kp);
+          if (!(next & kEnd)) {
+            scores(0, kp.slot, next);
+            scores(1, kp.slot, next);
+          }
+        }
+        uint32_t info = share_info(next);
+        while (true) {
           if (info & kEnd) {
-            release(kp);
+            if (!(info & kNull) && elect_one()) mma_commit(&sh.empty[kp.slot]);
+            __syncwarp();
             break;
           }
-          // a new piece
-          const bool two = info & kTwo;
-          bool last = info & kLast;
-          {
-            const uint32_t slot = uniform(kp.slot);
-            wait_q(0);
-            qk(0, slot, last, !two);
-            if (two) {
-              wait_q(1);
-              qk(1, slot, last, true);
-            }
-          }
+          const bool two = info & kTwo, first = info & kFirst, last = info & kLast;
+          if (first) q_par ^= two ? 3u : 1u;
           next_k();
-          bool first = true;
-          while (ok) {
-            const uint32_t vi = take(vp);
-            if (!ok) break;
-            const uint32_t v_at = uniform(vp.slot);
-            if (vi & kPart) clear(v_at, vi);
-            next_v();
-            if (last) {
+          const uint32_t k_at = uniform(kp.slot), v_at = uniform(vp.slot);
+          if (info & kPart) clear(info);
+          next = 0;
+          if (elect_one()) {
+            wait_entry(vp);
+            if (!last) {
+              // the next keys are there as a rule: wait for them before the weights
+              wait_entry(kp);
+              next = info_of(kp);
+              pv(0, v_at, first, false, !two);
+              scores(0, k_at, next);
+              if (two) {
+                pv(1, v_at, first, false, true);
+                scores(1, k_at, next);
+              }
+            } else {
               pv(0, v_at, first, true, !two);
               if (two) pv(1, v_at, first, true, true);
-              break;
+              wait_entry(kp);
+              next = info_of(kp);
+              if (!(next & kEnd)) {
+                scores(0, k_at, next);
+                scores(1, k_at, next);
+              }
             }
-            // the next keys are there as a rule: wait for them before the weights, so
-            // that the products follow each other with waits for weights only
-            info = take(kp);
-            last = info & kLast;
-            const uint32_t k_at = uniform(kp.slot);
-            pv(0, v_at, first, false, !two);
-            qk(0, k_at, last, !two);
-            if (two) {
-              pv(1, v_at, first, false, true);
-              qk(1, k_at, last, true);
-            }
-            next_k();
-            first = false;
           }
-          if (ok) info = take(kp);
+          p_par ^= two ? 3u : 1u;
+          next_v();
+          info = share_info(next);
         }
       }
       if (elect_one()) mma_commit(&sh.drain[warp - 2]);
@@ -822,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* lse = p.lse != nullptr ? p.lse + t_out * p.n_heads + head : nullptr;
       if (x.n == 0) {
         if (valid) {
+#pragma unroll 1
           for (int d = 0; d < D / 8; ++d) reinterpret_cast<uint4*>(out)[d] = make_uint4(0, 0, 0, 0);
           if (lse != nullptr) *lse = kNegInf;
         }
@@ -839,6 +866,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (work) {
+          if (__any_sync(0xffffffffu, key + kTile > hi || key < lo)) {
+            // scores that a row does not see become -inf, in place (the warps' loops
+            // share one instruction cache: what is rare is kept small)
+            const int a = lo - key, z = hi - key;
+#pragma unroll 1
+            for (int q = 0; q < kTile; q += 16) {
+              uint32_t y[16];
+              tmem_ld16_issue(tS + q, y);
+              tmem_ld16_wait(y);
+#pragma unroll
+              for (int w = 0; w < 16; ++w)
+                if (q + w < a || q + w >= z) y[w] = __float_as_uint(kNegInf);
+              tmem_st16(tS + q, y);
+            }
+            tmem_st_wait();
+          }
           uint32_t y[128];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32_issue(tS + 32 * q, y + 32 * q);
@@ -846,12 +889,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           reg_dep32(y + 32);
           reg_dep32(y + 64);
           reg_dep32(y + 96);
-          if (__any_sync(0xffffffffu, key + kTile > hi || key < lo)) {
-            const int a = lo - key, z = hi - key;
-#pragma unroll
-            for (int q = 0; q < 128; ++q)
-              if (q < a || q >= z) y[q] = __float_as_uint(kNegInf);
-          }
           float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
           for (int q = 0; q < 128; q += 8) {
@@ -870,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = raise ? ex2_approx((m - top) * c) : 1.f;
               if (raise) m = top;
               l *= f;
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
                 tmem_ld16_issue(tO + 16 * q, o);
@@ -918,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = !x.whole ? 1.f : some ? 1.f / l : 0.f;
       const size_t prow = (size_t)(v * 2 + x.slot) * F::kUnitRows + (kPair ? s * kTile : 0) + row;
       if (work) {
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld32_issue(tO + 32 * q, o);
