@@ -62,7 +62,8 @@ typedef struct {
  * p % page_size. Positions below zero (n_b > kv_len[b]) belong to no token.
  * Rows outside [0, T), a kv_len outside [0, max_pages * page_size] or a page
  * outside [0, n_pages) that a call needs: DS_ERR_BOUNDS in `status`; nothing
- * outside the buffers is read or written.
+ * outside the buffers is read or written. max_pages * page_size <= 2^30,
+ * T <= 2^23.
  */
 
 /* ---- new keys and values into their pages --------------------------------- */

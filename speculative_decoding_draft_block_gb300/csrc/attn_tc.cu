@@ -50,9 +50,8 @@
 #include <atomic>
 #include <mutex>
 
-#include "common.cuh"
+#include "attn_work.cuh"
 #include "internal.h"
-#include "kv_internal.h"
 #include "sm100.cuh"
 
 namespace ds {
@@ -67,7 +66,6 @@ constexpr uint32_t kCtrlRegs = 88, kSoftRegs = 208, kLaunchRegs = 168;
 static_assert(128 * kCtrlRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr uint32_t kWaitPolls = 1u << 16;
 constexpr uint32_t kHeader = 2048;  // barriers and small records, before the tiles
-constexpr int kUnitCost = 1;        // set-up of a unit, in key tiles
 constexpr int kAhead = 4;           // pieces handed out ahead, per stream
 constexpr int kMaxSlots = 12;
 
@@ -80,17 +78,6 @@ struct Layout {
   static constexpr uint32_t kBytes = kOffRing + kSlots * kTileBytes;
   static_assert(kSlots <= kMaxSlots && kBytes <= 227 * 1024, "shared memory");
 };
-
-// A piece of a unit: `n` key tiles from `tile0` (n = 0: the rows see nothing; n < 0: no more pieces).
-struct Piece {
-  int b, h, n, tile0;
-  int lo, hi;           // keys that some row of the unit sees
-  int token, n_tok;     // first row of q, tokens of the unit
-  int pos, kv;          // position of the first token, cached tokens
-  int two, whole, slot; // two row tiles; the piece is the unit; else its slot of partial results
-  int pad[3];
-};
-static_assert(sizeof(Piece) == 64, "four 16-byte words");
 
 // A ring slot's info word, for key entries: what this entry and the value entry
 // of the same tile are.
@@ -115,9 +102,7 @@ struct Header {
   int ended[2];         // tiles of a stream's share, -1 while not known
   uint32_t tmem;
   int abort_flag;
-  int64_t scan[kThreads / 32];
-  int64_t start_base[2];
-  int start_b[2];
+  ShareStart<kThreads, 2> work;
 };
 static_assert(sizeof(Header) <= kHeader, "header");
 
@@ -147,41 +132,9 @@ struct RingPos {
   }
 };
 
-// What the join needs to know of a cut unit: written by the share that begins it.
-struct CutUnit {
-  int64_t first, total;  // its first work tile, the work list's length
-  int32_t n, valid;      // key tiles
-  int32_t token, n_tok, h, pad;
-};
-static_assert(sizeof(CutUnit) <= 64, "record");
-
-constexpr int kRows = kMaxAttnCtas * 4 * kTile;  // rows of partial results: two slots a share
-
-struct Partials {
-  CutUnit* cut;  // [shares]
-  float2* stat;  // [kRows] reference and sum
-  float* out;    // [kRows][D]
-};
-
-template <int D>
-__host__ __device__ inline Partials partials(char* ws) {
-  Partials p;
-  p.cut = reinterpret_cast<CutUnit*>(ws);
-  p.stat = reinterpret_cast<float2*>(ws + kMaxAttnCtas * 2 * 64);
-  p.out = reinterpret_cast<float*>(p.stat + kRows);
-  return p;
-}
-
+// Key tiles, shares of the work list and rows of partial results of a form.
 template <bool kPair>
-struct Form {
-  static constexpr int kShares = kPair ? kMaxAttnCtas : 2 * kMaxAttnCtas;
-  static constexpr int kUnitRows = kPair ? 2 * kTile : kTile;
-  static constexpr int kUnitTiles = kPair ? 2 : 1;
-  // where share v begins
-  static __host__ __device__ __forceinline__ int64_t begin(int64_t total, int v) {
-    return (int64_t)((uint64_t)(total * v) / (uint64_t)kShares);
-  }
-};
+struct Form : WorkForm<kTile, kPair ? kMaxAttnCtas : 2 * kMaxAttnCtas, kPair ? 2 * kTile : kTile> {};
 
 // Bounded wait of one thread (about a second with kWaitPolls, a minute with
 // kIdlePolls, for roles that may have nothing to do for as long as a unit lasts).
@@ -211,116 +164,6 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
 }
 
-// ---- the work list -----------------------------------------------------------------
-
-// A unit's tokens and key tiles.
-struct Unit {
-  int i0, n_tok;         // first token, tokens
-  int pos;               // position of the first token
-  int lo, hi;            // keys that some row sees
-  int tile0, n;          // first key tile, number (0: nothing to see)
-};
-
-__device__ __forceinline__ Unit make_unit(const AttnParams& p, const Request& r, int qt, int unit_tokens) {
-  Unit u;
-  u.i0 = qt * unit_tokens;
-  u.n_tok = min(r.n - u.i0, unit_tokens);
-  u.pos = r.kv - r.n + u.i0;
-  u.hi = p.causal ? min(u.pos + u.n_tok, r.kv) : r.kv;
-  u.lo = p.window > 0 ? max(0, u.pos - p.window + 1) : 0;
-  u.n = 0;
-  u.tile0 = 0;
-  if (u.hi > u.lo) {
-    u.tile0 = u.lo / kTile;
-    u.n = (u.hi + kTile - 1) / kTile - u.tile0;
-  }
-  return u;
-}
-
-__device__ __forceinline__ Request request_of(const AttnParams& p, int b) {
-  return load_request(p.q_start, p.kv_len, b, p.T, p.max_q, (int64_t)p.max_pages << p.pool.page_shift);
-}
-
-__device__ __forceinline__ int64_t request_work(const AttnParams& p, const Request& r, int unit_tokens) {
-  int64_t w = 0;
-  for (int qt = 0; qt * unit_tokens < r.n; ++qt) w += make_unit(p, r, qt, unit_tokens).n + kUnitCost;
-  return w * p.pool.n_kv_heads;
-}
-
-// Tiles of a unit (first work tile `first`, n key tiles) that lie before work tile x.
-__host__ __device__ __forceinline__ int tiles_before(int64_t x, int64_t first, int n) {
-  const int64_t t = x - first - kUnitCost;
-  return t <= 0 ? 0 : t >= n ? n : (int)t;
-}
-
-// Walks over a share.
-struct Walk {
-  int64_t at, end, base;  // next work tile, end of the share, first work tile of (b, qt)
-  int b, qt;
-  Request r;
-
-  __device__ __forceinline__ void start(const AttnParams& p, int64_t first, int64_t last, int b0, int64_t base0) {
-    at = first;
-    end = last;
-    base = base0;
-    b = b0;
-    qt = 0;
-    if (at < end) r = request_of(p, b);
-  }
-  // The next piece, or one with n < 0; a unit that begins here and is cut goes to `cut`.
-  __device__ __forceinline__ Piece next(const AttnParams& p, int unit_tokens, int per_tile, CutUnit* cut,
-                                        int64_t total) {
-    Piece x;
-    x.n = -1;
-    while (at < end) {
-      if (qt * unit_tokens >= r.n) {
-        ++b;
-        qt = 0;
-        if (b >= p.B) break;
-        r = request_of(p, b);
-        continue;
-      }
-      const Unit u = make_unit(p, r, qt, unit_tokens);
-      const int64_t w = u.n + kUnitCost, all = w * p.pool.n_kv_heads;
-      if (at >= base + all) {
-        base += all;
-        ++qt;
-        continue;
-      }
-      const int h = (int)((at - base) / w);
-      const int64_t u0 = base + h * w;
-      const int t0 = tiles_before(at, u0, u.n), t1 = tiles_before(end, u0, u.n);
-      const bool here = u.n == 0 ? at == u0 : t1 > t0;
-      at = u0 + w;
-      if (!here) continue;
-      x.b = b;
-      x.h = h;
-      x.n = t1 - t0;
-      x.tile0 = u.tile0 + t0;
-      x.lo = u.lo;
-      x.hi = u.hi;
-      x.token = r.q0 + u.i0;
-      x.n_tok = u.n_tok;
-      x.pos = u.pos;
-      x.kv = r.kv;
-      x.two = u.n_tok > per_tile;
-      x.whole = x.n == u.n;
-      x.slot = t0 > 0 ? 0 : 1;
-      if (cut != nullptr && !x.whole && x.slot == 1) {
-        const CutUnit c = {u0, total, u.n, 1, x.token, x.n_tok, h, 0};
-        *cut = c;
-      }
-      return x;
-    }
-    return x;
-  }
-};
-
-// whether no row of the unit sees some of a tile's keys
-__device__ __forceinline__ bool partly_seen(int tile, int lo, int hi) {
-  return tile * kTile < lo || (tile + 1) * kTile > hi;
-}
-
 // ---- packed float32 pairs ------------------------------------------------------------
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -341,11 +184,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -384,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sRing = smem + L::kOffRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_tile = kTile / p.group;  // tokens of a row tile
-  const int unit_tokens = F::kUnitTiles * per_tile;
+  const int tile_rows = per_tile * p.group;      // rows in use of a row tile
+  const int unit_rows = (kPair ? 2 : 1) * tile_rows;
 
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle is taken from address bits
     if (tid == 0) report(p.status, kErrCuda);
@@ -413,56 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
 
-  // the CTA's shares: total work, then the requests that hold the shares' first tiles
-  int64_t mine = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
-    const Request r = request_of(p, b);
-    if (!r.ok && blockIdx.x == 0) report(p.status, kErrBounds);
-    mine += request_work(p, r, unit_tokens);
-  }
-  int64_t sum = mine;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane == 0) sh.scan[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) total += sh.scan[i];
   const Partials part = partials<D>(p.workspace);
   const int v0 = blockIdx.x * kLists;
-  const int64_t begin = F::begin(total, v0), end = F::begin(total, v0 + kLists);
-  if (begin >= end) {
+  const int64_t total = locate_shares<F, kThreads, kLists>(p, unit_rows, v0, sh.work);
+  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) {
     if (tid < kLists) part.cut[v0 + tid].valid = 0;
     return;
-  }
-  __syncthreads();
-  int64_t base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int64_t w = p.B <= kThreads ? mine : b < p.B ? request_work(p, request_of(p, b), unit_tokens) : 0;
-    int64_t inc = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) sh.scan[warp] = inc;
-    __syncthreads();
-    int64_t before = base, all = base;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += sh.scan[i];
-      all += sh.scan[i];
-    }
-    const int64_t a = before + inc - w;
-    for (int l = 0; l < kLists; ++l) {
-      const int64_t x = F::begin(total, v0 + l);
-      if (w > 0 && a <= x && x < a + w) {
-        sh.start_b[l] = b;
-        sh.start_base[l] = a;
-      }
-    }
-    base = all;
-    __syncthreads();
-    if (F::begin(total, v0 + kLists - 1) < base) break;
   }
   if (warp == 2) tmem_alloc(&sh.tmem, 512);
   __syncthreads();
@@ -486,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
-      Walk wk;
-      wk.start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.start_b[l], sh.start_base[l]);
+      Walk<F> wk;
+      wk.start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.work.b[l], sh.work.base[l]);
       if (does_k && lane == 0) part.cut[v0 + l].valid = 0;
       RingPos<kSlots> kp, vp;                              // places of the next K and V entry
       if (!kPair) kp.add(l);
@@ -546,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         kp.add(kPair ? 2 : l == 0 && n_tiles == 1 ? 3 : 4);
       };
       while (ok) {
-        x = wk.next(p, unit_tokens, per_tile, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
+        x = wk.next(p, unit_rows, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
         if (does_k) {  // to the softmax
           const uint32_t i = np % kAhead;
           ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, p.status, kIdlePolls);
@@ -562,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         table = p.block_table + (int64_t)x.b * p.max_pages;
         int page = page_of(x.tile0);
         if (does_k) {
-          for (int s = kPair ? 0 : l; s <= (kPair ? x.two : l); ++s) {
+          const bool two = x.rows > tile_rows;
+          for (int s = kPair ? 0 : l; s <= (kPair ? (int)two : l); ++s) {
             ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], abort_flag, p.status);
             if (!ok) break;
             if (s == 0) q_par[0] ^= 1;
@@ -581,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tile = x.tile0 + j, now = page;
           if (j + 1 < x.n) page = page_of(tile + 1);
           if (does_k) {
-            uint32_t info = (x.two ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
-            if (partly_seen(tile, x.lo, x.hi))
+            uint32_t info = (x.rows > tile_rows ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
+            if (F::partly_seen(tile, x.lo, x.hi))
               info |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
             load(&tmK, kp, tile, now, info);
             if (!ok) break;
@@ -838,9 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.piece_empty[list][at]);
       if (x.n < 0) break;
-      if (kPair && s == 1 && !x.two) continue;
+      if (kPair && s == 1 && x.rows <= tile_rows) continue;
       const int i = (kPair ? s * per_tile : 0) + tile_tok;  // token of the unit
-      const bool valid = tile_tok < per_tile && i < x.n_tok;
+      const bool valid = tile_tok < per_tile && i * p.group < x.rows;
       const int pos = x.pos + i;
       const int64_t t_out = x.token + i;
       const int head = x.h * p.group + g;
@@ -953,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ref = m == kNegInf ? kNegInf : m * c;
       const bool some = l > 0.f || l != l;
       const float f = !x.whole ? 1.f : some ? 1.f / l : 0.f;
-      const size_t prow = (size_t)(v * 2 + x.slot) * F::kUnitRows + (kPair ? s * kTile : 0) + row;
+      const size_t prow = (size_t)(v * 2 + x.slot) * F::kPartRows + (kPair ? s * kTile : 0) + row;
       if (work) {
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -974,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!x.whole)
             part.stat[prow] = make_float2(ref, l);
           else if (lse != nullptr)
-            *lse = some ? (ref + log2f(l)) * 0.693147180559945f : kNegInf;
+            *lse = some ? (ref + log2f(l)) * kLn2 : kNegInf;
         }
       }
       tc_fence_before();
@@ -990,73 +786,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// ---- join of the units that were cut -----------------------------------------------------
-//
-// Block (v, y): the unit that share v begins and does not finish, rows 8 y .. 8 y + 7,
-// a warp a row. Its parts are slot 1 of v and slot 0 of the shares after it, in
-// that order, so the sums do not depend on timing.
-template <int D, bool kPair>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
-  using F = Form<kPair>;
-  pdl_wait();
-  const Partials part = partials<D>(p.workspace);
-  const int share = blockIdx.x;
-  const CutUnit cu = part.cut[share];
-  if (!cu.valid) return;
-  const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int per_tile = kTile / p.group;
-  const int row = prow & (kTile - 1), tok = row / p.group;
-  const int i = prow / kTile * per_tile + tok;
-  if (tok >= per_tile || i >= cu.n_tok) return;
-  auto at = [&](int k) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kUnitRows + prow; };
-  constexpr int N = D / 32;
-  float m = kNegInf, l = 0.f, o[N];
-#pragma unroll
-  for (int d = 0; d < N; ++d) o[d] = 0.f;
-  // shares 32 at a time: a lane finds what its share has of the unit
-  int before = 0;
-  for (int k0 = share; before < cu.n; k0 += 32) {
-    const int k = k0 + lane;
-    const int a = k < F::kShares ? tiles_before(F::begin(cu.total, k), cu.first, cu.n) : cu.n;
-    const int z = k < F::kShares ? tiles_before(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
-    before = __shfl_sync(0xffffffffu, z, 31);
-    float2 st = make_float2(kNegInf, 0.f);
-    if (a < z) st = __ldcg(part.stat + at(k));  // (with little work some shares have nothing and have written nothing)
-    float top = st.x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float m1 = fmaxf(m, top);
-    if (m1 != m) {
-      const float f = m == kNegInf ? 0.f : ex2_approx(m - m1);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < N; ++d) o[d] *= f;
-      m = m1;
-    }
-    const float f = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
-    const float w = st.y * f;
-    unsigned todo = __ballot_sync(0xffffffffu, a < z);
-    while (todo) {
-      const int q = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const float fq = __shfl_sync(0xffffffffu, f, q);
-      l += __shfl_sync(0xffffffffu, w, q);
-      const float* y = part.out + at(k0 + q) * D + lane * N;
-#pragma unroll
-      for (int d = 0; d < N; ++d) o[d] = fmaf(__ldcg(y + d), fq, o[d]);
-    }
-  }
-  const bool some = l > 0.f || l != l;
-  const float inv = some ? 1.f / l : 0.f;
-  const int head = cu.h * p.group + row - tok * p.group;
-  const int64_t t = cu.token + i;
-  uint32_t* to = reinterpret_cast<uint32_t*>(p.out + t * p.o_token + head * p.o_head) + lane * (N / 2);
-#pragma unroll
-  for (int d = 0; d < N / 2; ++d) to[d] = to_bf16x2(o[2 * d] * inv, o[2 * d + 1] * inv);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[t * p.n_heads + head] = some ? (m + log2f(l)) * 0.693147180559945f : kNegInf;
 }
 
 template <int D, bool kPair>
@@ -1098,25 +827,20 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
   cfg.stream = s;
   cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, kPair>, p, mq, mk, mv);
   if (e != cudaSuccess) return e;
-  const int rows = p.max_q <= per_tile ? p.max_q * p.group : Form<kPair>::kUnitRows;
+  using F = Form<kPair>;
+  const int rows = p.max_q <= per_tile ? p.max_q * p.group : F::kPartRows;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(Form<kPair>::kShares, (rows + 7) / 8);
+  cfg.gridDim = dim3(F::kShares, (rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kPair>, p);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<F, D, __nv_bfloat16>, p, kTile, per_tile * p.group);
 }
 
 }  // namespace
-
-size_t attention_ws_bytes(int32_t dtype, int32_t D) {
-  (void)dtype;
-  // a record a share, and rows of partial results: D sums, reference and sum
-  return (size_t)kMaxAttnCtas * 2 * 64 + (size_t)kRows * (D + 2) * sizeof(float);
-}
 
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s) {
   const bool pair = p.max_q > kTile / p.group;

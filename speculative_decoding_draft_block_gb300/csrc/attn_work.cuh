@@ -1,0 +1,329 @@
+// The work of attention over the paged cache, cut into equal shares, and the join
+// of what was cut; shared by the tensor-core and the CUDA-core kernels.
+//
+// A unit is (request, KV head, block of query rows), where a request's rows are
+// its tokens times the G query heads of a KV head: row = token * G + head. All
+// units' key tiles, one unit after the other with kUnitCost tiles' worth of
+// set-up before each, are the work list; it is cut into kShares contiguous
+// shares of equal length. Lengths are read on the device only. A unit that is
+// cut leaves float32 partial results (sums, reference exponent, sum of weights),
+// which a second kernel joins in the order of the shares, so that no result
+// depends on timing.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kv_internal.h"
+#include "sm100.cuh"
+
+namespace ds {
+namespace {
+
+constexpr int kUnitCost = 1;  // set-up of a unit, in key tiles
+
+template <int kTileKeys, int kShareCount, int kPartialRows>
+struct WorkForm {
+  static constexpr int kKeys = kTileKeys;          // keys of a tile
+  static constexpr int kShares = kShareCount;
+  static constexpr int kPartRows = kPartialRows;   // rows of a slot of partial results
+  // where share v begins
+  static __host__ __device__ __forceinline__ int64_t begin(int64_t total, int v) {
+    return (int64_t)((uint64_t)(total * v) / (uint64_t)kShares);
+  }
+  // whether no row of a unit that sees keys [lo, hi) sees some of a tile's
+  static __device__ __forceinline__ bool partly_seen(int tile, int lo, int hi) {
+    return tile * kKeys < lo || (tile + 1) * kKeys > hi;
+  }
+};
+
+// A piece of a unit: `n` key tiles from `tile0` (n = 0: the rows see nothing; n < 0: no more pieces).
+struct Piece {
+  int b, h, n, tile0;
+  int lo, hi;             // keys that some row of the unit sees
+  int token, off, rows;   // the unit's rows begin at head `off` of the KV head's, of row `token` of q
+  int pos, kv;            // position of that token, cached tokens
+  int whole, slot;        // the piece is the unit; else its slot of partial results
+  int pad[3];
+};
+static_assert(sizeof(Piece) == 64, "four 16-byte words");
+
+// What the join needs to know of a cut unit: written by the share that begins it.
+struct CutUnit {
+  int64_t first, total;  // its first work tile, the work list's length
+  int32_t n, valid;      // key tiles
+  int32_t token, off, rows, h;
+};
+static_assert(sizeof(CutUnit) <= 64, "record");
+
+constexpr int kMaxShares = 2 * kMaxAttnCtas;
+constexpr int kRows = kMaxShares * 2 * 128;  // rows of partial results: two slots a share
+
+struct Partials {
+  CutUnit* cut;  // [shares]
+  float2* stat;  // [kRows] reference and sum
+  float* out;    // [kRows][D]
+};
+
+template <int D>
+__host__ __device__ inline Partials partials(char* ws) {
+  Partials p;
+  p.cut = reinterpret_cast<CutUnit*>(ws);
+  p.stat = reinterpret_cast<float2*>(ws + kMaxShares * 64);
+  p.out = reinterpret_cast<float*>(p.stat + kRows);
+  return p;
+}
+
+// A unit's rows and key tiles.
+struct Unit {
+  int token, off, rows;  // first token (of the request), row within it, rows
+  int pos;               // position of the first token
+  int lo, hi;            // keys that some row sees
+  int tile0, n;          // first key tile, number (0: nothing to see)
+};
+
+template <class F>
+__device__ __forceinline__ Unit make_unit(const AttnParams& p, const Request& r, int u, int unit_rows) {
+  Unit x;
+  const int row0 = u * unit_rows;
+  x.rows = min(r.n * p.group - row0, unit_rows);
+  x.token = row0 / p.group;
+  x.off = row0 - x.token * p.group;
+  const int last = (row0 + x.rows - 1) / p.group;
+  x.pos = r.kv - r.n + x.token;
+  x.hi = p.causal ? min(r.kv - r.n + last + 1, r.kv) : r.kv;
+  x.lo = p.window > 0 ? max(0, x.pos - p.window + 1) : 0;
+  x.n = 0;
+  x.tile0 = 0;
+  if (x.hi > x.lo) {
+    x.tile0 = x.lo / F::kKeys;
+    x.n = (x.hi + F::kKeys - 1) / F::kKeys - x.tile0;
+  }
+  return x;
+}
+
+__device__ __forceinline__ Request request_of(const AttnParams& p, int b) {
+  return load_request(p.q_start, p.kv_len, b, p.T, p.max_q, (int64_t)p.max_pages << p.pool.page_shift);
+}
+
+template <class F>
+__device__ __forceinline__ int64_t request_work(const AttnParams& p, const Request& r, int unit_rows) {
+  int64_t w = 0;
+#pragma unroll 1
+  for (int u = 0; u * unit_rows < r.n * p.group; ++u) w += make_unit<F>(p, r, u, unit_rows).n + kUnitCost;
+  return w * p.pool.n_kv_heads;
+}
+
+// Tiles of a unit (first work tile `first`, n key tiles) that lie before work tile x.
+__host__ __device__ __forceinline__ int tiles_before(int64_t x, int64_t first, int n) {
+  const int64_t t = x - first - kUnitCost;
+  return t <= 0 ? 0 : t >= n ? n : (int)t;
+}
+
+// Walks over a share.
+template <class F>
+struct Walk {
+  int64_t at, end, base;  // next work tile, end of the share, first work tile of (b, u)
+  int b, u;
+  Request r;
+
+  __device__ __forceinline__ void start(const AttnParams& p, int64_t first, int64_t last, int b0, int64_t base0) {
+    at = first;
+    end = last;
+    base = base0;
+    b = b0;
+    u = 0;
+    if (at < end) r = request_of(p, b);
+  }
+  // The next piece, or one with n < 0; a unit that begins here and is cut goes to `cut` (if given).
+  __device__ __forceinline__ Piece next(const AttnParams& p, int unit_rows, CutUnit* cut, int64_t total) {
+    Piece x;
+    x.n = -1;
+#pragma unroll 1
+    while (at < end) {
+      if (u * unit_rows >= r.n * p.group) {
+        ++b;
+        u = 0;
+        if (b >= p.B) break;
+        r = request_of(p, b);
+        continue;
+      }
+      const Unit y = make_unit<F>(p, r, u, unit_rows);
+      const int64_t w = y.n + kUnitCost, all = w * p.pool.n_kv_heads;
+      if (at >= base + all) {
+        base += all;
+        ++u;
+        continue;
+      }
+      const int h = (int)((at - base) / w);
+      const int64_t first = base + h * w;
+      const int t0 = tiles_before(at, first, y.n), t1 = tiles_before(end, first, y.n);
+      const bool here = y.n == 0 ? at == first : t1 > t0;
+      at = first + w;
+      if (!here) continue;
+      x.b = b;
+      x.h = h;
+      x.n = t1 - t0;
+      x.tile0 = y.tile0 + t0;
+      x.lo = y.lo;
+      x.hi = y.hi;
+      x.token = r.q0 + y.token;
+      x.off = y.off;
+      x.rows = y.rows;
+      x.pos = y.pos;
+      x.kv = r.kv;
+      x.whole = x.n == y.n;
+      x.slot = t0 > 0 ? 0 : 1;
+      if (cut != nullptr && !x.whole && x.slot == 1) {
+        const CutUnit c = {first, total, y.n, 1, x.token, x.off, x.rows, h};
+        *cut = c;
+      }
+      return x;
+    }
+    return x;
+  }
+};
+
+// Where the walks of shares v0 .. v0 + kLists - 1 begin: a request and its first work tile.
+template <int kThreads, int kLists>
+struct ShareStart {
+  int64_t scan[kThreads / 32];
+  int64_t base[kLists];
+  int b[kLists];
+};
+
+// Fills it in (whole block, kThreads threads); the work list's length. Not
+// filled in for shares that are empty.
+template <class F, int kThreads, int kLists, int kMax>
+__device__ __forceinline__ int64_t locate_shares(const AttnParams& p, int unit_rows, int v0,
+                                                 ShareStart<kThreads, kMax>& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t mine = 0;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const Request r = request_of(p, b);
+    if (!r.ok && blockIdx.x == 0) report(p.status, kErrBounds);
+    mine += request_work<F>(p, r, unit_rows);
+  }
+  int64_t sum = mine;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) s.scan[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll 1
+  for (int i = 0; i < kThreads / 32; ++i) total += s.scan[i];
+  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) return total;
+  __syncthreads();
+  int64_t base = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    const int64_t w = p.B <= kThreads ? mine : b < p.B ? request_work<F>(p, request_of(p, b), unit_rows) : 0;
+    int64_t inc = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += v;
+    }
+    if (lane == 31) s.scan[warp] = inc;
+    __syncthreads();
+    int64_t before = base, all = base;
+#pragma unroll 1
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += s.scan[i];
+      all += s.scan[i];
+    }
+    const int64_t a = before + inc - w;
+    for (int l = 0; l < kLists; ++l) {
+      const int64_t x = F::begin(total, v0 + l);
+      if (w > 0 && a <= x && x < a + w) {
+        s.b[l] = b;
+        s.base[l] = a;
+      }
+    }
+    base = all;
+    __syncthreads();
+    if (F::begin(total, v0 + kLists - 1) < base) break;
+  }
+  return total;
+}
+
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr float kLn2 = 0.693147180559945f;
+
+// ---- join of the units that were cut -----------------------------------------------------
+//
+// Block (v, y): the unit that share v begins and does not finish, rows 8 y .. 8 y + 7
+// of its slot, a warp a row. Its parts are slot 1 of v and slot 0 of the shares after
+// it. A slot's rows come in tiles of `tile`, of which the first `used` stand for rows.
+template <class F, int D, typename T>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int tile, int used) {
+  sm100::pdl_wait();
+  const Partials part = partials<D>(p.workspace);
+  const int share = blockIdx.x;
+  const CutUnit cu = part.cut[share];
+  if (!cu.valid) return;
+  const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int in_tile = prow % tile, row = prow / tile * used + in_tile;
+  if (in_tile >= used || row >= cu.rows) return;
+  auto at = [&](int k) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + prow; };
+  constexpr int N = D / 32;
+  float m = kNegInf, l = 0.f, o[N];
+#pragma unroll
+  for (int d = 0; d < N; ++d) o[d] = 0.f;
+  // shares 32 at a time: a lane finds what its share has of the unit
+  int before = 0;
+  for (int k0 = share; before < cu.n; k0 += 32) {
+    const int k = k0 + lane;
+    const int a = k < F::kShares ? tiles_before(F::begin(cu.total, k), cu.first, cu.n) : cu.n;
+    const int z = k < F::kShares ? tiles_before(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
+    before = __shfl_sync(0xffffffffu, z, 31);
+    float2 st = make_float2(kNegInf, 0.f);
+    if (a < z) st = __ldcg(part.stat + at(k));  // (with little work some shares have nothing and have written nothing)
+    float top = st.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float m1 = fmaxf(m, top);
+    if (m1 != m) {
+      const float f = m == kNegInf ? 0.f : ex2_approx(m - m1);
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < N; ++d) o[d] *= f;
+      m = m1;
+    }
+    const float f = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
+    const float w = st.y * f;
+    unsigned todo = __ballot_sync(0xffffffffu, a < z);
+    while (todo) {
+      const int q = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const float fq = __shfl_sync(0xffffffffu, f, q);
+      l += __shfl_sync(0xffffffffu, w, q);
+      const float* y = part.out + at(k0 + q) * D + lane * N;
+#pragma unroll
+      for (int d = 0; d < N; ++d) o[d] = fmaf(__ldcg(y + d), fq, o[d]);
+    }
+  }
+  const bool some = l > 0.f || l != l;
+  const float inv = some ? 1.f / l : 0.f;
+  const int at_head = cu.off + row, tok = at_head / p.group;
+  const int head = cu.h * p.group + at_head - tok * p.group;
+  const int64_t t = cu.token + tok;
+  char* to = p.out + t * p.o_token + head * p.o_head;
+  if (sizeof(T) == 2) {
+#pragma unroll
+    for (int d = 0; d < N / 2; ++d)
+      reinterpret_cast<uint32_t*>(to)[lane * (N / 2) + d] = to_bf16x2(o[2 * d] * inv, o[2 * d + 1] * inv);
+  } else {
+#pragma unroll
+    for (int d = 0; d < N; ++d) reinterpret_cast<float*>(to)[lane * N + d] = o[d] * inv;
+  }
+  if (p.lse != nullptr && lane == 0) p.lse[t * p.n_heads + head] = some ? (m + log2f(l)) * kLn2 : kNegInf;
+}
+
+}  // namespace
+}  // namespace ds

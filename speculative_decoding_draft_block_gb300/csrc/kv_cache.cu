@@ -126,7 +126,7 @@ ds_status check_pool(const ds_kv_pool& a, int32_t layer, PoolView* v) {
 
 // Requests, rows and table of a call over ragged rows. Positions are 32-bit.
 bool rows_ok(int32_t B, int32_t T, int32_t max_pages, int32_t page_size) {
-  return B >= 1 && B <= 65535 && T >= 0 && max_pages >= 1 && (int64_t)max_pages * page_size <= INT32_MAX;
+  return B >= 1 && B <= 65535 && T >= 0 && T <= (1 << 23) && max_pages >= 1 && (int64_t)max_pages * page_size <= (1 << 30);
 }
 
 bool overlap(const void* a, const void* b, size_t na, size_t nb) {
@@ -223,7 +223,8 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   p.n_heads = a->n_heads;
   p.group = a->n_heads / a->pool.n_kv_heads;
   p.causal = a->causal;
-  p.window = a->window;
+  // a window as long as the table hides nothing
+  p.window = (int64_t)a->window >= (int64_t)a->max_pages * a->pool.page_size ? 0 : a->window;
   p.scale = a->scale;
   p.q = static_cast<const char*>(a->q);
   p.out = static_cast<char*>(a->out);
@@ -238,7 +239,7 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   p.workspace = static_cast<char*>(a->workspace);
   p.status = a->status;
   const cudaError_t err = p.dtype == DS_BF16 ? launch_attention_tc(p, (cudaStream_t)stream)
-                                             : launch_attention_simt(p, (cudaStream_t)stream);
+                                             : launch_attention_f32(p, (cudaStream_t)stream);
   return err == cudaSuccess ? DS_OK : DS_ERR_CUDA;
 }
 

@@ -101,7 +101,7 @@ size_t attention_ws_bytes(int32_t dtype, int32_t D);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s);
-cudaError_t launch_attention_simt(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_f32(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s);
 
 }  // namespace ds
