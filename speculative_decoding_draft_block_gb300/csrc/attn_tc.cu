@@ -252,17 +252,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
 
+  if (warp == 2) tmem_alloc(&sh.tmem, 512);
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  // what stands above runs while the kernel before this one finishes
+  pdl_wait();
   const Partials part = partials<D>(p.workspace);
   const int v0 = blockIdx.x * kLists;
   const int64_t total = locate_shares<F, kThreads, kLists>(p, unit_rows, v0, sh.work);
-  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) {
-    if (tid < kLists) part.cut[v0 + tid].valid = 0;
-    return;
-  }
-  if (warp == 2) tmem_alloc(&sh.tmem, 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) {
+    if (tid < kLists) part.cut[v0 + tid].valid = 0;
+    if (warp == 2) tmem_dealloc(tmem, 512);
+    return;
+  }
   volatile int* abort_flag = &sh.abort_flag;
   pdl_launch_dependents();
 
@@ -276,11 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = min(page_size, kTile);              // keys of a box
       const int boxes = kTile / rows;                      // pages a tile
       const uint32_t box_bytes = (uint32_t)rows * 128u;
-      if (lane == 0) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-      }
       Walk<F> wk;
       wk.start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.work.b[l], sh.work.base[l]);
       if (does_k && lane == 0) part.cut[v0 + l].valid = 0;
@@ -825,18 +828,18 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::kBytes;
   cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, kPair>, p, mq, mk, mv);
   if (e != cudaSuccess) return e;
   using F = Form<kPair>;
   const int rows = p.max_q <= per_tile ? p.max_q * p.group : F::kPartRows;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(F::kShares, (rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<F, D, __nv_bfloat16>, p, kTile, per_tile * p.group);
 }
 

@@ -262,6 +262,7 @@ constexpr float kLn2 = 0.693147180559945f;
 // it. A slot's rows come in tiles of `tile`, of which the first `used` stand for rows.
 template <class F, int D, typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int tile, int used) {
+  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;

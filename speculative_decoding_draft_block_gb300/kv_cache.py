@@ -119,6 +119,14 @@ def _bytes(t, name):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _stream(stream, pool):
+    """The stream's handle; the current one of the pool's device by default (asked for
+    without building a Stream object, which takes as long as the launches)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(pool.device_index)
+    return _lib._stream(stream)
+
+
 class KvPool:
     """A pool of pages: K and V as tensors [n_layers, n_pages, page_size,
     n_kv_heads, head_dim] of equal strides with the last index contiguous. Any
@@ -135,6 +143,7 @@ class KvPool:
             raise ValueError("the last index of k and v must be contiguous")
         self.k, self.v = k, v
         self.dtype = k.dtype
+        self.device_index = k.device.index
         self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
         st = list(k.stride())
         # a stride that is never taken may be anything in torch: give a valid one
@@ -156,7 +165,7 @@ def ds_cache_append(pool, layer, k_new, v_new, q_start, block_table, kv_len, sta
     a = AppendArgs(pool.desc, layer, B, k_new.shape[0], M, k, v, kt, kh, vt, vh,
                    _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
                    _words(kv_len, "kv_len", B), _words(status, "status"))
-    return load().ds_cache_append(a, _lib._stream(stream))
+    return load().ds_cache_append(a, _stream(stream, pool))
 
 
 def ds_paged_attention_workspace_bytes(pool, n_heads):
@@ -186,7 +195,7 @@ def ds_paged_attention(pool, layer, q, q_start, max_q, block_table, kv_len, out,
                       1.0 / math.sqrt(pool.head_dim) if scale is None else scale, qp, qt, qh,
                       _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
                       _words(kv_len, "kv_len", B), op, ot, oh, lp, wp, wn, _words(status, "status"))
-    return load().ds_paged_attention(a, _lib._stream(stream))
+    return load().ds_paged_attention(a, _stream(stream, pool))
 
 
 def ds_cache_update_workspace_bytes(B, n_pages):
@@ -204,7 +213,7 @@ def ds_cache_update(pool, block_table, kv_len, ref, new_len, table_out, len_out,
                    _words(new_len, "new_len", B), _words(table_out, "table_out", B * M),
                    _words(len_out, "len_out", B), _words(ref_out, "ref_out", N), wp, wn,
                    _words(status, "status"))
-    return load().ds_cache_update(a, _lib._stream(stream))
+    return load().ds_cache_update(a, _stream(stream, pool))
 
 
 def ds_cache_compact_workspace_bytes(n_pages):
@@ -219,7 +228,7 @@ def ds_cache_compact(pool, block_table, ref, table_out, ref_out, page_map, n_use
     a = CompactArgs(pool.desc, B, M, _words(block_table, "block_table"), _words(ref, "ref", N),
                     _words(table_out, "table_out", B * M), _words(ref_out, "ref_out", N),
                     _words(page_map, "page_map", N), _words(n_used, "n_used", 1), wp, wn, _words(status, "status"))
-    return load().ds_cache_compact(a, _lib._stream(stream))
+    return load().ds_cache_compact(a, _stream(stream, pool))
 
 
 class PagedCache:
