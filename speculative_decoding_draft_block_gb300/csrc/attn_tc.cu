@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto page_of = [&](int tile) {
         const int key = tile * kTile + lane * rows;
         if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return -1;
-        const int page = __ldg(table + (key >> shift));
+        const int page = __ldcg(table + (key >> shift));
         if (page >= 0 && page < p.pool.n_pages) return page;
         report(p.status, kErrBounds);
         return 0;

@@ -266,7 +266,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
   sm100::pdl_wait();
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;
-  const CutUnit cu = part.cut[share];
+  CutUnit cu;
+  static_assert(sizeof(CutUnit) == 40, "five 8-byte words");
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    reinterpret_cast<long long*>(&cu)[i] = __ldcg(reinterpret_cast<const long long*>(part.cut + share) + i);
   if (!cu.valid) return;
   const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int in_tile = prow % tile, row = prow / tile * used + in_tile;

@@ -82,10 +82,11 @@ struct Request {
 
 __device__ __forceinline__ Request load_request(const int32_t* q_start, const int32_t* kv_len, int32_t b,
                                                 int32_t T, int32_t max_q, int64_t cap) {
+  // (past the first-level cache: a kernel may have started before the one that wrote these ended)
   Request r;
-  r.q0 = __ldg(q_start + b);
-  const int32_t q1 = __ldg(q_start + b + 1);
-  r.kv = __ldg(kv_len + b);
+  r.q0 = __ldcg(q_start + b);
+  const int32_t q1 = __ldcg(q_start + b + 1);
+  r.kv = __ldcg(kv_len + b);
   r.n = q1 - r.q0;
   r.ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= T && r.n <= max_q && r.kv >= 0 && (int64_t)r.kv <= cap;
   if (!r.ok) r.n = 0;

@@ -53,18 +53,29 @@ __device__ __forceinline__ int block_sum(int v, int* warp_sums) {
   return total;
 }
 
-// One word of every CTA of the cluster, published and summed: the words of the
-// CTAs before this one in `before`, of all in the result. A cluster barrier.
-template <typename T>
-__device__ __forceinline__ T cluster_exchange(cg::cluster_group& cl, T* slot, T v, T& before) {
-  if (threadIdx.x == 0) *slot = v;
+// What the CTAs of the cluster count, published and summed with one barrier: the
+// sums over the CTAs before this one in `before`, over all in the result.
+struct Counts {
+  long long a;
+  int b, c;
+};
+
+__device__ __forceinline__ Counts cluster_exchange(cg::cluster_group& cl, Counts* slot, Counts mine, Counts& before) {
+  if (threadIdx.x == 0) *slot = mine;
   cl.sync();
-  before = 0;
-  T all = 0;
+  before = Counts{0, 0, 0};
+  Counts all = {0, 0, 0};
+#pragma unroll
   for (int r = 0; r < kCluster; ++r) {
-    const T u = *cl.map_shared_rank(slot, r);
-    if (r < (int)cl.block_rank()) before += u;
-    all += u;
+    const Counts u = *cl.map_shared_rank(slot, r);
+    if (r < (int)cl.block_rank()) {
+      before.a += u.a;
+      before.b += u.b;
+      before.c += u.c;
+    }
+    all.a += u.a;
+    all.b += u.b;
+    all.c += u.c;
   }
   return all;
 }
@@ -141,11 +152,11 @@ __device__ __forceinline__ int written_page(const UpdateParams& p, const Move& m
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     update_plan_kernel(const UpdateParams p) {
   cg::cluster_group cl = cg::this_cluster();
+  sm100::pdl_launch_dependents();
   __shared__ int sums[kPlanWarps];
-  __shared__ int slot[2];
+  __shared__ Counts slot;
   // what the requests ask for may pass 32 bits (a length's limit is the table's,
   // not the pool's), and has to be compared with the free pages all the same
-  __shared__ long long slot64;
   __shared__ unsigned long long need_sum;
   const int tid = threadIdx.x, lane = tid & 31;
   const int rank = (int)cl.block_rank();
@@ -224,18 +235,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     free += c == 0;
   }
   if (need > 0) atomicAdd(&need_sum, (unsigned long long)need);
-  __syncthreads();
-  long long need_before;
-  int free_before, any;
-  const long long need_all = cluster_exchange(cl, &slot64, (long long)need_sum, need_before);
-  const int free_all = cluster_exchange(cl, &slot[0], block_sum(free, sums), free_before);
-  const int bad_all = cluster_exchange(cl, &slot[1], __syncthreads_or(bad), any);
-  const bool fail = bad_all > 0 || need_all > free_all;
-  if (fail && rank == 0 && tid == 0) report(p.status, bad_all > 0 ? kErrBounds : kErrPages);
+  const int free_sum = block_sum(free, sums);
+  const int bad_any = __syncthreads_or(bad);
+  Counts before;
+  const Counts all = cluster_exchange(cl, &slot, Counts{(long long)need_sum, free_sum, bad_any}, before);
+  const long long need_all = all.a;
+  const bool bad_all = all.c > 0, fail = bad_all || need_all > all.b;
+  if (fail && rank == 0 && tid == 0) report(p.status, bad_all ? kErrBounds : kErrPages);
   if (rank == 0 && tid == 0) w.fail[0] = fail;
 
   // places of the requests' new pages, and the pages that are given out
-  int at = fail ? 0 : (int)need_before;
+  int at = fail ? 0 : (int)before.a;
   for (int base = b0; base < b1; base += kPlanThreads) {
     const int b = base + tid;
     int n = 0;
@@ -248,7 +258,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     if (b < b1) w.start[b] = at + ex;
     at += total;
   }
-  at = free_before;
+  at = before.b;
   for (int base = p0; base < p1; base += kPlanThreads) {
     const int i = base + tid;
     const int c = i < p1 ? __ldcg(w.count + i) : 1;
@@ -265,29 +275,53 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 
 // ---- update: tables and copies ------------------------------------------------------------
 
-// Copies the first `tokens` tokens of a page of one layer of K or V.
+// Copies the first `tokens` tokens of a page of one layer of K or V. The index
+// runs along memory (heads inside tokens, or tokens inside heads) over runs of
+// contiguous bytes, as long as the strides allow: a whole page as a rule. A thread
+// has kFlight loads in flight before it stores.
+constexpr int kFlight = 4;
 __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int src, int dst, int tokens, int tid,
                                             int threads) {
-  const int chunks = v.row_bytes >> 4;
   const char* from = base + (int64_t)src * v.page_stride;
   char* to = base + (int64_t)dst * v.page_stride;
-  // the index runs along memory: heads inside tokens, or tokens inside heads
   const bool heads_inside = v.head_stride <= v.token_stride;
-  const int inner = heads_inside ? v.n_kv_heads : tokens;
-  const int64_t si = heads_inside ? v.head_stride : v.token_stride, so = heads_inside ? v.token_stride : v.head_stride;
-  const int n = chunks * v.n_kv_heads * tokens;
-  for (int x = tid; x < n; x += threads) {
-    const int row = x / chunks, c = x - row * chunks;
-    const int o = row / inner, i = row - o * inner;
-    const int64_t off = o * so + i * si + c * 16;
-    *reinterpret_cast<uint4*>(to + off) = __ldcs(reinterpret_cast<const uint4*>(from + off));
+  const int64_t s1 = heads_inside ? v.head_stride : v.token_stride, s2 = heads_inside ? v.token_stride : v.head_stride;
+  int run = v.row_bytes, n1 = heads_inside ? v.n_kv_heads : tokens, n2 = heads_inside ? tokens : v.n_kv_heads;
+  if (s1 == run) {
+    run *= n1;
+    n1 = 1;
+    if (s2 == run) {
+      run *= n2;
+      n2 = 1;
+    }
+  }
+  run >>= 4;
+  const int n = run * n1 * n2;
+  for (int x0 = tid; x0 < n; x0 += kFlight * threads) {
+    uint4 y[kFlight];
+    int64_t off[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int x = x0 + f * threads;
+      int64_t o = (int64_t)x * 16;
+      if (n1 * n2 > 1) {
+        const int q = x / run, i2 = q / n1;
+        o = i2 * s2 + (q - i2 * n1) * s1 + (x - q * run) * 16;
+      }
+      off[f] = o;
+      if (x < n) y[f] = __ldcs(reinterpret_cast<const uint4*>(from + o));
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+      if (x0 + f * threads < n) *reinterpret_cast<uint4*>(to + off[f]) = y[f];
   }
 }
 
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
+  sm100::pdl_wait();
   const int b = blockIdx.x, part = blockIdx.y;  // part: 2 * layer + (0: K, 1: V)
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
-  if (__ldg(w.fail)) {
+  if (__ldcg(w.fail)) {
     if (part == 0) {
       for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
         p.table_out[(int64_t)b * p.max_pages + j] = __ldg(p.table + (int64_t)b * p.max_pages + j);
@@ -295,22 +329,22 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
     }
     return;
   }
-  const int copy = __ldg(w.copy_of + b);
+  const int copy = __ldcg(w.copy_of + b);
   if (part > 0 && copy < 0) return;
   const Move m = load_move(p, b);
-  const int start = __ldg(w.start + b), shared = m.kept - (copy >= 0);
+  const int start = __ldcg(w.start + b), shared = m.kept - (copy >= 0);
   if (part == 0) {
     const int32_t* past = p.table + (int64_t)max(m.parent, 0) * p.max_pages;
     for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
       p.table_out[(int64_t)b * p.max_pages + j] =
-          j < shared ? __ldg(past + j) : j < m.want ? __ldg(w.free_list + start + j - shared) : -1;
+          j < shared ? __ldg(past + j) : j < m.want ? __ldcg(w.free_list + start + j - shared) : -1;
     if (threadIdx.x == 0) {
       p.len_out[b] = __ldg(p.new_len + b);
       if (copy >= 0) atomicSub(p.ref_out + copy, 1);
     }
     if (copy < 0) return;
   }
-  const int dst = __ldg(w.free_list + start);
+  const int dst = __ldcg(w.free_list + start);
   char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
   copy_tokens(p.pool, base, copy, dst, m.keep & ((1 << p.pool.page_shift) - 1), threadIdx.x, blockDim.x);
 }
@@ -334,8 +368,9 @@ __host__ __device__ inline CompactWs compact_ws(int32_t* ws, int32_t N) {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const CompactParams p) {
   cg::cluster_group cl = cg::this_cluster();
+  sm100::pdl_launch_dependents();
   __shared__ int sums[kPlanWarps];
-  __shared__ int slot[4];
+  __shared__ Counts slot[2];
   const int tid = threadIdx.x, rank = (int)cl.block_rank();
   const int N = p.pool.n_pages;
   const CompactWs w = compact_ws(p.ws, N);
@@ -347,14 +382,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     bad |= r < 0;
     held += r > 0;
   }
-  int held_before, any, below_before;
-  const int used = cluster_exchange(cl, &slot[0], block_sum(held, sums), held_before);
-  const bool fail = cluster_exchange(cl, &slot[1], __syncthreads_or(bad), any) > 0;
+  const int held_sum = block_sum(held, sums), bad_any = __syncthreads_or(bad);
+  Counts before, none;
+  const Counts all = cluster_exchange(cl, &slot[0], Counts{0, held_sum, bad_any}, before);
+  const int used = all.b;
+  const bool fail = all.c > 0;
   int below = 0;  // held pages below `used`
   for (int i = p0 + tid; i < min(p1, used); i += kPlanThreads) below += __ldg(p.ref + i) > 0;
-  const int held_below = cluster_exchange(cl, &slot[2], block_sum(below, sums), below_before);
+  const int held_below = cluster_exchange(cl, &slot[1], Counts{0, block_sum(below, sums), 0}, none).b;
 
-  int at = held_before;
+  int at = before.b;
   for (int base = p0; base < p1; base += kPlanThreads) {
     const int i = base + tid;
     const int r = i < p1 ? __ldg(p.ref + i) : 0;
@@ -387,19 +424,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 // One block a table row or a (move, layer, K or V); the number of moves is
 // known on the device only, so a fixed grid walks over them.
 __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams p) {
+  sm100::pdl_wait();
   const CompactWs w = compact_ws(p.ws, p.pool.n_pages);
   const int64_t entries = (int64_t)p.B * p.max_pages;
-  const bool fail = __ldg(w.moves + 1) != 0;
+  const bool fail = __ldcg(w.moves + 1) != 0;
   for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < entries; x += (int64_t)gridDim.x * blockDim.x) {
     const int e = __ldg(p.table + x);
-    p.table_out[x] = fail ? e : e >= 0 && e < p.pool.n_pages ? __ldg(p.page_map + e) : -1;
+    p.table_out[x] = fail ? e : e >= 0 && e < p.pool.n_pages ? __ldcg(p.page_map + e) : -1;
   }
-  const int n = __ldg(w.moves), parts = 2 * p.pool.n_layers;
+  const int n = __ldcg(w.moves), parts = 2 * p.pool.n_layers;
   const int tokens = 1 << p.pool.page_shift;
   for (int64_t x = blockIdx.x; x < (int64_t)n * parts; x += gridDim.x) {
     const int i = (int)(x / parts), part = (int)(x - (int64_t)i * parts);
     char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
-    copy_tokens(p.pool, base, __ldg(w.src + i), __ldg(w.dst + i), tokens, threadIdx.x, blockDim.x);
+    copy_tokens(p.pool, base, __ldcg(w.src + i), __ldcg(w.dst + i), tokens, threadIdx.x, blockDim.x);
   }
 }
 
@@ -414,20 +452,34 @@ size_t compact_ws_bytes(int32_t n_pages) {
   return (4 + 2 * (((size_t)n_pages / 2 + 4) & ~(size_t)3)) * sizeof(int32_t);
 }
 
+// The second launch is set up while the plan runs and waits for it (what the plan
+// writes is read past the first-level cache, __ldcg).
+template <class P>
+cudaError_t launch_apply(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t s) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s) {
   update_plan_kernel<<<kCluster, kPlanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  update_apply_kernel<<<dim3(p.B, 2 * p.pool.n_layers), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_apply(update_apply_kernel, p, dim3(p.B, 2 * p.pool.n_layers), s);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
   compact_plan_kernel<<<kCluster, kPlanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<152 * 8, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_apply(compact_apply_kernel, p, dim3(152 * 8), s);
 }
 
 }  // namespace ds
