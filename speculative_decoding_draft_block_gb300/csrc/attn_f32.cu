@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   const float c = p.scale * kLog2eHi;
   const int shift = p.pool.page_shift, mask = (1 << shift) - 1;
   Walk<F> wk;
-  wk.start(p, begin, end, sh.work.b[0], sh.work.base[0]);
+  wk.start(begin, end, sh.work, 0);
   while (true) {
     const Piece x = wk.next(p, kBM, tid == 0 ? part.cut + share : nullptr, total);
     if (x.n < 0) break;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
     bool valid[kRM];
 #pragma unroll
     for (int i = 0; i < kRM; ++i) {
-      const int row = ty * kRM + i, at = x.off + row, tok = at / p.group;
+      const int row = ty * kRM + i, at = x.off + row, tok = p.by_group.quotient(at);
       const int head = x.h * p.group + at - tok * p.group, pos = x.pos + tok;
       valid[i] = row < x.rows;
       hi[i] = !valid[i] ? 0 : p.causal ? min(pos + 1, x.kv) : x.kv;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
     find(0);
     for (int i = tid; i < kBM * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = i - row * (D / 4);
-      const int at = x.off + row, tok = at / p.group;
+      const int at = x.off + row, tok = p.by_group.quotient(at);
       const char* from = p.q + (int64_t)(x.token + tok) * p.q_token + (int64_t)(x.h * p.group + at - tok * p.group) * p.q_head;
       copy16(&sh.q[row][d * 4], row < x.rows ? from + d * 16 : nullptr);
     }

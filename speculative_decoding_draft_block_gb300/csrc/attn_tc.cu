@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem + L::kOffQ;
   uint8_t* sRing = smem + L::kOffRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_tile = kTile / p.group;  // tokens of a row tile
+  const int per_tile = p.by_group.quotient(kTile);  // tokens of a row tile
   const int tile_rows = per_tile * p.group;      // rows in use of a row tile
   const int unit_rows = (kPair ? 2 : 1) * tile_rows;
 
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int boxes = kTile / rows;                      // pages a tile
       const uint32_t box_bytes = (uint32_t)rows * 128u;
       Walk<F> wk;
-      wk.start(p, F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.work.b[l], sh.work.base[l]);
+      wk.start(F::begin(total, v0 + l), F::begin(total, v0 + l + 1), sh.work, l);
       if (does_k && lane == 0) part.cut[v0 + l].valid = 0;
       RingPos<kSlots> kp, vp;                              // places of the next K and V entry
       if (!kPair) kp.add(l);
@@ -295,12 +295,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Piece x = {};
       const int32_t* table = nullptr;
-      // page of this lane's box of a key tile, -1: no row of the unit sees it
+      // Table entry of this lane's box of a key tile, kNoPage: no row of the unit sees
+      // it. (Looked at when the tile is loaded, a tile later as a rule.)
+      constexpr int kNoPage = INT32_MIN;
       auto page_of = [&](int tile) {
         const int key = tile * kTile + lane * rows;
-        if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return -1;
-        const int page = __ldcg(table + (key >> shift));
-        if (page >= 0 && page < p.pool.n_pages) return page;
+        if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return kNoPage;
+        return __ldcg(table + (key >> shift));
+      };
+      auto checked = [&](int page) {
+        if (page == kNoPage || (page >= 0 && page < p.pool.n_pages)) return page;
         report(p.status, kErrBounds);
         return 0;
       };
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto load = [&](const CUtensorMap* map, const RingPos<kSlots>& at, int tile, int page, uint32_t info) {
         if (!wait_empty(at)) return;
+        page = checked(page);
         const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) {
           sh.info[at.slot] = info;
@@ -345,7 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       while (ok) {
         x = wk.next(p, unit_rows, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
-        if (does_k) {  // to the softmax
+        // the first tile's page is on its way while the piece goes to the softmax
+        int page = kNoPage;
+        if (x.n > 0) {
+          table = p.block_table + (int64_t)x.b * p.max_pages;
+          page = page_of(x.tile0);
+        }
+        if (does_k) {
           const uint32_t i = np % kAhead;
           ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, p.status, kIdlePolls);
           if (!ok) break;
@@ -357,8 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (x.n < 0) break;
         if (x.n == 0) continue;
-        table = p.block_table + (int64_t)x.b * p.max_pages;
-        int page = page_of(x.tile0);
         if (does_k) {
           const bool two = x.rows > tile_rows;
           for (int s = kPair ? 0 : l; s <= (kPair ? (int)two : l); ++s) {
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + s * kTile, tO = tmem + lanes + 256 + s * D;
     const float c = p.scale * kLog2eHi;
-    const int tile_tok = row / p.group, g = row - tile_tok * p.group;
+    const int tile_tok = p.by_group.quotient(row), g = row - tile_tok * p.group;
     const int v = v0 + (kPair ? 0 : s);            // share
     uint32_t ns = 0, np = 0;                       // score tiles and pieces so far
     const int list = kPair ? 0 : s;
@@ -666,18 +675,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (work) {
           if (__any_sync(0xffffffffu, key + kTile > hi || key < lo)) {
-            // scores that a row does not see become -inf, in place (the warps' loops
-            // share one instruction cache: what is rare is kept small)
+            // Scores that a row does not see become -inf, in place, 32 keys at a time and
+            // only where there are any. (The warps' loops share one instruction cache:
+            // with the selects unrolled over the 128 scores below, 2 KB of instructions
+            // more, every tile is slower.)
             const int a = lo - key, z = hi - key;
+            const uint32_t seen = (uint32_t)max(0, z - a);
 #pragma unroll 1
-            for (int q = 0; q < kTile; q += 16) {
-              uint32_t y[16];
-              tmem_ld16_issue(tS + q, y);
-              tmem_ld16_wait(y);
+            for (int q = 0; q < kTile; q += 32) {
+              if (__all_sync(0xffffffffu, q >= a && q + 32 <= z)) continue;
+              uint32_t y[32];
+              tmem_ld32_issue(tS + q, y);
+              tmem_ld_wait(y);
 #pragma unroll
-              for (int w = 0; w < 16; ++w)
-                if (q + w < a || q + w >= z) y[w] = __float_as_uint(kNegInf);
+              for (int w = 0; w < 32; ++w)
+                if ((uint32_t)(q - a + w) >= seen) y[w] = __float_as_uint(kNegInf);
               tmem_st16(tS + q, y);
+              tmem_st16(tS + q + 16, y + 16);
             }
             tmem_st_wait();
           }

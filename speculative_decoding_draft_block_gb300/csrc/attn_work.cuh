@@ -86,17 +86,17 @@ __device__ __forceinline__ Unit make_unit(const AttnParams& p, const Request& r,
   Unit x;
   const int row0 = u * unit_rows;
   x.rows = min(r.n * p.group - row0, unit_rows);
-  x.token = row0 / p.group;
+  x.token = p.by_group.quotient(row0);
   x.off = row0 - x.token * p.group;
-  const int last = (row0 + x.rows - 1) / p.group;
+  const int last = p.by_group.quotient(row0 + x.rows - 1);
   x.pos = r.kv - r.n + x.token;
   x.hi = p.causal ? min(r.kv - r.n + last + 1, r.kv) : r.kv;
   x.lo = p.window > 0 ? max(0, x.pos - p.window + 1) : 0;
   x.n = 0;
   x.tile0 = 0;
   if (x.hi > x.lo) {
-    x.tile0 = x.lo / F::kKeys;
-    x.n = (x.hi + F::kKeys - 1) / F::kKeys - x.tile0;
+    x.tile0 = (uint32_t)x.lo / F::kKeys;
+    x.n = (uint32_t)(x.hi + F::kKeys - 1) / F::kKeys - x.tile0;
   }
   return x;
 }
@@ -126,13 +126,14 @@ struct Walk {
   int b, u;
   Request r;
 
-  __device__ __forceinline__ void start(const AttnParams& p, int64_t first, int64_t last, int b0, int64_t base0) {
+  template <class S>
+  __device__ __forceinline__ void start(int64_t first, int64_t last, const S& s, int list) {
     at = first;
     end = last;
-    base = base0;
-    b = b0;
+    base = s.base[list];
+    b = s.b[list];
     u = 0;
-    if (at < end) r = request_of(p, b);
+    r = s.r[list];
   }
   // The next piece, or one with n < 0; a unit that begins here and is cut goes to `cut` (if given).
   __device__ __forceinline__ Piece next(const AttnParams& p, int unit_rows, CutUnit* cut, int64_t total) {
@@ -148,14 +149,15 @@ struct Walk {
         continue;
       }
       const Unit y = make_unit<F>(p, r, u, unit_rows);
-      const int64_t w = y.n + kUnitCost, all = w * p.pool.n_kv_heads;
+      // (at most 2^23 + 1 tiles and 256 heads: 32 bits)
+      const uint32_t w = y.n + kUnitCost, all = w * p.pool.n_kv_heads;
       if (at >= base + all) {
         base += all;
         ++u;
         continue;
       }
-      const int h = (int)((at - base) / w);
-      const int64_t first = base + h * w;
+      const int h = (int)((uint32_t)(at - base) / w);
+      const int64_t first = base + (int64_t)((uint32_t)h * w);
       const int t0 = tiles_before(at, first, y.n), t1 = tiles_before(end, first, y.n);
       const bool here = y.n == 0 ? at == first : t1 > t0;
       at = first + w;
@@ -188,61 +190,66 @@ template <int kThreads, int kLists>
 struct ShareStart {
   int64_t scan[kThreads / 32];
   int64_t base[kLists];
+  Request r[kLists];
   int b[kLists];
 };
 
 // Fills it in (whole block, kThreads threads); the work list's length. Not
-// filled in for shares that are empty.
+// filled in for shares that are empty. kThreads requests at a time; with no more
+// of them than that, which is the rule, one pass does for sum and search.
 template <class F, int kThreads, int kLists, int kMax>
 __device__ __forceinline__ int64_t locate_shares(const AttnParams& p, int unit_rows, int v0,
                                                  ShareStart<kThreads, kMax>& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int64_t mine = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
-    const Request r = request_of(p, b);
-    if (!r.ok && blockIdx.x == 0) report(p.status, kErrBounds);
-    mine += request_work<F>(p, r, unit_rows);
-  }
-  int64_t sum = mine;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane == 0) s.scan[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, base = 0;
+  const bool once = p.B <= kThreads;
+  // pass 0 sums up, pass 1 searches (both in one if `once`)
 #pragma unroll 1
-  for (int i = 0; i < kThreads / 32; ++i) total += s.scan[i];
-  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) return total;
-  __syncthreads();
-  int64_t base = 0;
+  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
 #pragma unroll 1
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int64_t w = p.B <= kThreads ? mine : b < p.B ? request_work<F>(p, request_of(p, b), unit_rows) : 0;
-    int64_t inc = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) s.scan[warp] = inc;
-    __syncthreads();
-    int64_t before = base, all = base;
-#pragma unroll 1
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += s.scan[i];
-      all += s.scan[i];
-    }
-    const int64_t a = before + inc - w;
-    for (int l = 0; l < kLists; ++l) {
-      const int64_t x = F::begin(total, v0 + l);
-      if (w > 0 && a <= x && x < a + w) {
-        s.b[l] = b;
-        s.base[l] = a;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      Request r;
+      int64_t w = 0;
+      if (b < p.B) {
+        r = request_of(p, b);
+        if (!r.ok && blockIdx.x == 0) report(p.status, kErrBounds);
+        w = request_work<F>(p, r, unit_rows);
       }
+      int64_t inc = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += v;
+      }
+      if (lane == 31) s.scan[warp] = inc;
+      __syncthreads();
+      int64_t before = base, all = base;
+#pragma unroll 4
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += s.scan[i];
+        all += s.scan[i];
+      }
+      base = all;
+      if (once) total = all;
+      if (pass == 1 && w > 0) {
+        const int64_t a = before + inc - w;
+#pragma unroll
+        for (int l = 0; l < kLists; ++l) {
+          const int64_t x = F::begin(total, v0 + l);
+          if (a <= x && x < a + w) {
+            s.b[l] = b;
+            s.base[l] = a;
+            s.r[l] = r;
+          }
+        }
+      }
+      __syncthreads();
     }
-    base = all;
-    __syncthreads();
-    if (F::begin(total, v0 + kLists - 1) < base) break;
+    if (pass == 0) {
+      total = base;
+      base = 0;
+    }
   }
   return total;
 }
@@ -263,20 +270,23 @@ constexpr float kLn2 = 0.693147180559945f;
 template <class F, int D, typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int tile, int used) {
   sm100::pdl_launch_dependents();
-  sm100::pdl_wait();
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;
+  const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int in_tile = prow % tile, row = prow / tile * used + in_tile;
+  auto at = [&](int k) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + prow; };
+  constexpr int N = D / 32;
+  sm100::pdl_wait();
+  // The record, and, before it has arrived, the row's statistics in this share and
+  // the 31 after it (looked at only if the record says that they have parts).
   CutUnit cu;
   static_assert(sizeof(CutUnit) == 40, "five 8-byte words");
 #pragma unroll
   for (int i = 0; i < 5; ++i)
     reinterpret_cast<long long*>(&cu)[i] = __ldcg(reinterpret_cast<const long long*>(part.cut + share) + i);
-  if (!cu.valid) return;
-  const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int in_tile = prow % tile, row = prow / tile * used + in_tile;
-  if (in_tile >= used || row >= cu.rows) return;
-  auto at = [&](int k) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + prow; };
-  constexpr int N = D / 32;
+  float2 ahead = make_float2(kNegInf, 0.f);
+  if (share + lane < F::kShares) ahead = __ldcg(part.stat + at(share + lane));
+  if (!cu.valid || in_tile >= used || row >= cu.rows) return;
   float m = kNegInf, l = 0.f, o[N];
 #pragma unroll
   for (int d = 0; d < N; ++d) o[d] = 0.f;
@@ -288,7 +298,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
     const int z = k < F::kShares ? tiles_before(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
     before = __shfl_sync(0xffffffffu, z, 31);
     float2 st = make_float2(kNegInf, 0.f);
-    if (a < z) st = __ldcg(part.stat + at(k));  // (with little work some shares have nothing and have written nothing)
+    // (with little work some shares have nothing and have written nothing)
+    if (a < z) st = k0 == share ? ahead : __ldcg(part.stat + at(k));
     float top = st.x;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -302,20 +313,34 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
     }
     const float f = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
     const float w = st.y * f;
+    // (parts stand in consecutive shares, up to empty ones)
     unsigned todo = __ballot_sync(0xffffffffu, a < z);
+#pragma unroll 1
     while (todo) {
-      const int q = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const float fq = __shfl_sync(0xffffffffu, f, q);
-      l += __shfl_sync(0xffffffffu, w, q);
-      const float* y = part.out + at(k0 + q) * D + lane * N;
+      constexpr int kBatch = 4;  // rows of partial results in flight
+      float y[kBatch][N], fq[kBatch];
 #pragma unroll
-      for (int d = 0; d < N; ++d) o[d] = fmaf(__ldcg(y + d), fq, o[d]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int q = todo ? __ffs(todo) - 1 : 0;
+        const bool there = todo != 0;
+        todo &= todo - 1;
+        fq[i] = __shfl_sync(0xffffffffu, f, q);
+        const float wq = __shfl_sync(0xffffffffu, w, q);
+        l += there ? wq : 0.f;
+        const float* from = part.out + at(k0 + q) * D + lane * N;
+#pragma unroll
+        for (int d = 0; d < N; ++d) y[i][d] = there ? __ldcg(from + d) : 0.f;
+        if (!there) fq[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int d = 0; d < N; ++d) o[d] = fmaf(y[i][d], fq[i], o[d]);
     }
   }
   const bool some = l > 0.f || l != l;
   const float inv = some ? 1.f / l : 0.f;
-  const int at_head = cu.off + row, tok = at_head / p.group;
+  const int at_head = cu.off + row, tok = p.by_group.quotient(at_head);
   const int head = cu.h * p.group + at_head - tok * p.group;
   const int64_t t = cu.token + tok;
   char* to = p.out + t * p.o_token + head * p.o_head;

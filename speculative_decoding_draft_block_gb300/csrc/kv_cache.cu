@@ -222,6 +222,7 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   p.max_q = a->max_q < a->T ? a->max_q : a->T;
   p.n_heads = a->n_heads;
   p.group = a->n_heads / a->pool.n_kv_heads;
+  p.by_group.set((uint32_t)p.group);
   p.causal = a->causal;
   // a window as long as the table hides nothing
   p.window = (int64_t)a->window >= (int64_t)a->max_pages * a->pool.page_size ? 0 : a->window;

@@ -28,10 +28,25 @@ struct AppendParams {
   int32_t* status;
 };
 
+// Quotients of 0 <= n < 2^31 by a divisor d fixed on the host, 1 <= d <= 128: with
+// l = ceil(log2 d) and m = ceil(2^(31 + l) / d) <= 2^32 - 1 (or 2^31 for d = 1),
+// floor(n / d) = floor(n m / 2^(31 + l)) (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t m, shift;
+  void set(uint32_t d) {
+    uint32_t l = 0;
+    while ((1u << l) < d) ++l;
+    shift = 31 + l;
+    m = (uint32_t)(((1ull << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ int quotient(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
 struct AttnParams {
   PoolView pool;  // k, v of the layer
   int32_t dtype, D;
   int32_t B, T, max_pages, max_q, n_heads, group;
+  Divisor by_group;
   int32_t causal, window;
   float scale;
   const char* q;
