@@ -60,24 +60,36 @@ struct Counts {
   int b, c;
 };
 
-__device__ __forceinline__ Counts cluster_exchange(cg::cluster_group& cl, Counts* slot, Counts mine, Counts& before) {
-  if (threadIdx.x == 0) *slot = mine;
+struct Exchange {
+  Counts mine, before, all;
+};
+
+__device__ __forceinline__ Counts cluster_exchange(cg::cluster_group& cl, Exchange* x, Counts mine, Counts& before) {
+  if (threadIdx.x == 0) x->mine = mine;
   cl.sync();
-  before = Counts{0, 0, 0};
-  Counts all = {0, 0, 0};
+  if (threadIdx.x < 32) {  // a lane a CTA (the other lanes' words are zero)
+    const int r = threadIdx.x;
+    Counts u = {0, 0, 0};
+    if (r < kCluster) u = *cl.map_shared_rank(&x->mine, r);
+    const bool lower = r < (int)cl.block_rank();
+    Counts v = lower ? u : Counts{0, 0, 0};
 #pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    const Counts u = *cl.map_shared_rank(slot, r);
-    if (r < (int)cl.block_rank()) {
-      before.a += u.a;
-      before.b += u.b;
-      before.c += u.c;
+    for (int d = kCluster / 2; d > 0; d >>= 1) {
+      u.a += __shfl_xor_sync(0xffffffffu, u.a, d);
+      v.a += __shfl_xor_sync(0xffffffffu, v.a, d);
     }
-    all.a += u.a;
-    all.b += u.b;
-    all.c += u.c;
+    u.b = __reduce_add_sync(0xffffffffu, u.b);
+    u.c = __reduce_add_sync(0xffffffffu, u.c);
+    v.b = __reduce_add_sync(0xffffffffu, v.b);
+    v.c = __reduce_add_sync(0xffffffffu, v.c);
+    if (r == 0) {
+      x->all = u;
+      x->before = v;
+    }
   }
-  return all;
+  __syncthreads();
+  before = x->before;
+  return x->all;
 }
 
 // Range of n items that CTA `rank` of the cluster takes, a multiple of 4 at its start.
@@ -92,30 +104,31 @@ __device__ __forceinline__ void share(int n, int rank, int& first, int& last) {
 // What the plan leaves for the second launch, and works with.
 struct UpdateWs {
   int32_t* fail;       // [4]: 1 if the state does not change
+  int4* row;           // [B] parent, pages shared with it, pages wanted, place of the first new one in free_list
+  int2* copy;          // [B] page to copy into the first new one (or -1), its tokens
   int32_t* count;      // [N] holders
   int32_t* writers;    // [N] requests that will write into the page (entries of touched pages only)
   int32_t* first;      // [N] lowest of them
   int32_t* free_list;  // [N] free pages in ascending order, as many as are given out
-  int32_t* start;      // [B] place of the request's first new page in free_list
-  int32_t* copy_of;    // [B] page whose tokens the request copies into its first new page, or -1
 };
 
 __host__ __device__ inline UpdateWs update_ws(int32_t* ws, int32_t B, int32_t N) {
   const int64_t n = (N + 3) & ~3, b = (B + 3) & ~3;
   UpdateWs w;
   w.fail = ws;
-  w.count = ws + 4;
+  w.row = reinterpret_cast<int4*>(ws + 4);
+  w.copy = reinterpret_cast<int2*>(w.row + b);
+  w.count = reinterpret_cast<int32_t*>(w.copy + b);
   w.writers = w.count + n;
   w.first = w.writers + n;
   w.free_list = w.first + n;
-  w.start = w.free_list + n;
-  w.copy_of = w.start + b;
   return w;
 }
 
-// One request's move, from device memory.
+// One request's move.
 struct Move {
   int32_t parent, keep, kept, want, old;  // old: pages it holds now
+  int32_t page;                           // partly filled page that it will write into, -1: none
   bool ok;
 };
 
@@ -138,26 +151,58 @@ __device__ __forceinline__ Move load_move(const UpdateParams& p, int b) {
   m.kept = m.ok ? pages_of(m.keep, p.pool.page_shift) : 0;
   m.want = m.ok ? pages_of(next, p.pool.page_shift) : 0;
   m.old = m.ok ? pages_of(now, p.pool.page_shift) : 0;
+  m.page = -1;
+  if (m.ok && (m.keep & ((1 << p.pool.page_shift) - 1)) != 0 && next > m.keep) {
+    m.page = __ldg(p.table + (int64_t)m.parent * p.max_pages + m.kept - 1);
+    if (m.page < 0 || m.page >= p.pool.n_pages) m.ok = false;
+  }
   return m;
 }
 
-// The partly filled page that request b will write into, or -1.
-__device__ __forceinline__ int written_page(const UpdateParams& p, const Move& m, int next) {
-  const int mask = (1 << p.pool.page_shift) - 1;
-  if ((m.keep & mask) == 0 || next <= m.keep) return -1;
-  const int page = __ldg(p.table + (int64_t)m.parent * p.max_pages + m.kept - 1);
-  return page >= 0 && page < p.pool.n_pages ? page : -2;
+// A CTA's requests beyond the first kPlanThreads are looked up anew in each phase.
+struct PlanShared {
+  int sums[kPlanWarps];
+  Exchange exchange;
+  // what the requests ask for may pass 32 bits (a length's limit is the table's,
+  // not the pool's), and has to be compared with the free pages all the same
+  unsigned long long need;
+  Move move[kPlanThreads];
+};
+
+// Four pages' words at once (the arrays are 16-byte aligned, i a multiple of 4):
+// of an input, or past the first-level cache of what this kernel writes.
+template <bool kInput>
+__device__ __forceinline__ int4 load_four(const int32_t* from, int i, int end, int none) {
+  if (i + 4 <= end) {
+    const int4* f = reinterpret_cast<const int4*>(from + i);
+    return kInput ? __ldg(f) : __ldcg(f);
+  }
+  int4 v = make_int4(none, none, none, none);
+  if (i < end) v.x = kInput ? __ldg(from + i) : __ldcg(from + i);
+  if (i + 1 < end) v.y = kInput ? __ldg(from + i + 1) : __ldcg(from + i + 1);
+  if (i + 2 < end) v.z = kInput ? __ldg(from + i + 2) : __ldcg(from + i + 2);
+  return v;
+}
+__device__ __forceinline__ void store_four(int32_t* to, int i, int end, int4 v) {
+  if (i + 4 <= end) {
+    *reinterpret_cast<int4*>(to + i) = v;
+    return;
+  }
+  if (i < end) to[i] = v.x;
+  if (i + 1 < end) to[i + 1] = v.y;
+  if (i + 2 < end) to[i + 2] = v.z;
 }
 
+// Three phases between cluster barriers: holders as they are, holders afterwards,
+// pages given out. What bounds it is the chain of dependent reads (a length, the
+// parent's length, its table entry, that page's holders) at the latency of the L2,
+// so a request's move is looked up once and kept in shared memory, and four pages
+// go to a thread, so that a pool of 32768 pages takes one scan.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     update_plan_kernel(const UpdateParams p) {
   cg::cluster_group cl = cg::this_cluster();
   sm100::pdl_launch_dependents();
-  __shared__ int sums[kPlanWarps];
-  __shared__ Counts slot;
-  // what the requests ask for may pass 32 bits (a length's limit is the table's,
-  // not the pool's), and has to be compared with the free pages all the same
-  __shared__ unsigned long long need_sum;
+  __shared__ PlanShared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int rank = (int)cl.block_rank();
   const int N = p.pool.n_pages, B = p.B;
@@ -165,48 +210,58 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   int p0, p1, b0, b1;
   share(N, rank, p0, p1);
   share(B, rank, b0, b1);
+  auto move_of = [&](int b) { return b - b0 < kPlanThreads ? sh.move[b - b0] : load_move(p, b); };
 
   // holders as they are; the entries of `writers` and `first` that will be used
   int bad = 0;
-  for (int i = p0 + tid; i < p1; i += kPlanThreads) {
-    const int r = __ldg(p.ref + i);
-    bad |= r < 0;
-    w.count[i] = r;
-  }
+  if (tid == 0) sh.need = 0;
   for (int b = b0 + tid; b < b1; b += kPlanThreads) {
     const Move m = load_move(p, b);
-    const int page = m.ok ? written_page(p, m, __ldg(p.new_len + b)) : -1;
-    bad |= !m.ok || page == -2;
-    if (page >= 0) {
-      w.writers[page] = 0;
-      w.first[page] = INT32_MAX;
+    if (b - b0 < kPlanThreads) sh.move[b - b0] = m;
+    bad |= !m.ok;
+    if (m.ok && m.page >= 0) {
+      w.writers[m.page] = 0;
+      w.first[m.page] = INT32_MAX;
     }
+  }
+  for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
+    const int4 r = load_four<true>(p.ref, i, p1, 0);
+    bad |= (r.x | r.y | r.z | r.w) < 0;
+    store_four(w.count, i, p1, r);
   }
   cl.sync();
 
   // holders afterwards: a warp a request, only the entries that change
   for (int b = b0 + (tid >> 5); b < b1; b += kPlanWarps) {
-    const Move m = load_move(p, b);
+    const Move m = move_of(b);
     if (!m.ok) continue;
     const int32_t* now = p.table + (int64_t)b * p.max_pages;
     const int32_t* past = p.table + (int64_t)max(m.parent, 0) * p.max_pages;
     const int from = m.parent == b ? m.kept : 0;
-    for (int j = from + lane; j < max(m.old, m.kept); j += 32) {
-      const int o = j < m.old ? __ldg(now + j) : -1;
-      const int h = j < m.kept ? __ldg(past + j) : -1;
-      if ((j < m.old && (o < 0 || o >= N)) || (j < m.kept && (h < 0 || h >= N))) {
-        bad = 1;
-      } else if (o != h) {
-        if (o >= 0) atomicSub(w.count + o, 1);
-        if (h >= 0) atomicAdd(w.count + h, 1);
+    const int to = max(m.old, m.kept);
+    constexpr int kAhead = 8;  // entries in flight a lane: a long row is one or two round trips
+    for (int j0 = from + lane; j0 < to; j0 += 32 * kAhead) {
+      int o[kAhead], h[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + 32 * i;
+        o[i] = j < m.old ? __ldg(now + j) : -1;
+        h[i] = j < m.kept ? __ldg(past + j) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + 32 * i;
+        if ((j < m.old && (o[i] < 0 || o[i] >= N)) || (j < m.kept && (h[i] < 0 || h[i] >= N))) {
+          bad = 1;
+        } else if (o[i] != h[i]) {
+          if (o[i] >= 0) atomicSub(w.count + o[i], 1);
+          if (h[i] >= 0) atomicAdd(w.count + h[i], 1);
+        }
       }
     }
-    if (lane == 0) {
-      const int page = written_page(p, m, __ldg(p.new_len + b));
-      if (page >= 0) {
-        atomicAdd(w.writers + page, 1);
-        atomicMin(w.first + page, b);
-      }
+    if (lane == 0 && m.page >= 0) {
+      atomicAdd(w.writers + m.page, 1);
+      atomicMin(w.first + m.page, b);
     }
   }
   cl.sync();
@@ -214,31 +269,29 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   // new pages per request and free pages, summed over the cluster
   long long need = 0;
   int free = 0;
-  if (tid == 0) need_sum = 0;
-  __syncthreads();
   for (int b = b0 + tid; b < b1; b += kPlanThreads) {
-    const Move m = load_move(p, b);
+    const Move m = move_of(b);
     int copy = -1;
-    if (m.ok) {
-      const int page = written_page(p, m, __ldg(p.new_len + b));
-      if (page >= 0) {
-        const int holders = __ldcg(w.count + page);
-        if (holders > 1 && !(holders == __ldcg(w.writers + page) && b == __ldcg(w.first + page))) copy = page;
-      }
-      need += m.want - m.kept + (copy >= 0);
+    if (m.ok && m.page >= 0) {
+      const int holders = __ldcg(w.count + m.page), writers = __ldcg(w.writers + m.page), first = __ldcg(w.first + m.page);
+      if (holders > 1 && !(holders == writers && b == first)) copy = m.page;
     }
-    w.copy_of[b] = copy;
+    need += m.want - m.kept + (copy >= 0);
+    w.copy[b] = make_int2(copy, m.keep & ((1 << p.pool.page_shift) - 1));
+    if (b - b0 < kPlanThreads) sh.move[b - b0].page = copy;
   }
-  for (int i = p0 + tid; i < p1; i += kPlanThreads) {
-    const int c = __ldcg(w.count + i);
-    bad |= c < 0;
-    free += c == 0;
+  int4 counts = make_int4(1, 1, 1, 1);  // of this thread's first four pages
+  for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
+    const int4 c = load_four<false>(w.count, i, p1, 1);
+    if (i == p0 + 4 * tid) counts = c;
+    bad |= (c.x | c.y | c.z | c.w) < 0;
+    free += (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0);
   }
-  if (need > 0) atomicAdd(&need_sum, (unsigned long long)need);
-  const int free_sum = block_sum(free, sums);
+  if (need > 0) atomicAdd(&sh.need, (unsigned long long)need);
+  const int free_sum = block_sum(free, sh.sums);
   const int bad_any = __syncthreads_or(bad);
   Counts before;
-  const Counts all = cluster_exchange(cl, &slot, Counts{(long long)need_sum, free_sum, bad_any}, before);
+  const Counts all = cluster_exchange(cl, &sh.exchange, Counts{(long long)sh.need, free_sum, bad_any}, before);
   const long long need_all = all.a;
   const bool bad_all = all.c > 0, fail = bad_all || need_all > all.b;
   if (fail && rank == 0 && tid == 0) report(p.status, bad_all ? kErrBounds : kErrPages);
@@ -248,26 +301,38 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   int at = fail ? 0 : (int)before.a;
   for (int base = b0; base < b1; base += kPlanThreads) {
     const int b = base + tid;
-    int n = 0;
+    int shared = 0, want = 0, parent = 0;
     if (b < b1) {
-      const Move m = load_move(p, b);
-      n = m.want - m.kept + (w.copy_of[b] >= 0);
+      Move m = move_of(b);
+      if (b - b0 >= kPlanThreads) m.page = w.copy[b].x;  // (this thread's own)
+      shared = m.kept - (m.page >= 0);
+      want = m.want;
+      parent = m.parent;
     }
     int total;
-    const int ex = block_exclusive(n, sums, total);
-    if (b < b1) w.start[b] = at + ex;
+    const int ex = block_exclusive(want - shared, sh.sums, total);
+    if (b < b1) w.row[b] = make_int4(parent, shared, want, at + ex);
     at += total;
   }
   at = before.b;
-  for (int base = p0; base < p1; base += kPlanThreads) {
-    const int i = base + tid;
-    const int c = i < p1 ? __ldcg(w.count + i) : 1;
+  for (int base = p0; base < p1; base += 4 * kPlanThreads) {
+    const int i = base + 4 * tid;
+    const int4 c = base == p0 ? counts : load_four<false>(w.count, i, p1, 1);
     int total;
-    const int r = at + block_exclusive(c == 0, sums, total);
-    if (i < p1) {
-      if (!fail && c == 0 && r < need_all) w.free_list[r] = i;
-      p.ref_out[i] = fail ? __ldg(p.ref + i) : c == 0 ? (r < need_all ? 1 : 0) : c;
-    }
+    int r = at + block_exclusive((c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0), sh.sums, total);
+    auto give = [&](int count, int page) {
+      if (count != 0) return count;
+      const bool given = r < need_all;
+      if (!fail && given) w.free_list[r] = page;
+      ++r;
+      return given ? 1 : 0;
+    };
+    int4 out;
+    out.x = give(c.x, i);
+    out.y = give(c.y, i + 1);
+    out.z = give(c.z, i + 2);
+    out.w = give(c.w, i + 3);
+    store_four(p.ref_out, i, p1, fail ? load_four<true>(p.ref, i, p1, 0) : out);
     at += total;
   }
   cl.sync();  // no CTA leaves while another may read its shared memory
@@ -279,7 +344,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 // runs along memory (heads inside tokens, or tokens inside heads) over runs of
 // contiguous bytes, as long as the strides allow: a whole page as a rule. A thread
 // has kFlight loads in flight before it stores.
-constexpr int kFlight = 4;
+constexpr int kFlight = 8;
 __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int src, int dst, int tokens, int tid,
                                             int threads) {
   const char* from = base + (int64_t)src * v.page_stride;
@@ -297,31 +362,37 @@ __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int s
   }
   run >>= 4;
   const int n = run * n1 * n2;
-  for (int x0 = tid; x0 < n; x0 += kFlight * threads) {
-    uint4 y[kFlight];
-    int64_t off[kFlight];
+  const uint4* src4 = reinterpret_cast<const uint4*>(from);
+  uint4* dst4 = reinterpret_cast<uint4*>(to);
+  if (n == run) {
+    for (int x = tid; x < n; x += kFlight * threads) {
+      uint4 y[kFlight];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int x = x0 + f * threads;
-      int64_t o = (int64_t)x * 16;
-      if (n1 * n2 > 1) {
-        const int q = x / run, i2 = q / n1;
-        o = i2 * s2 + (q - i2 * n1) * s1 + (x - q * run) * 16;
-      }
-      off[f] = o;
-      if (x < n) y[f] = __ldcs(reinterpret_cast<const uint4*>(from + o));
+      for (int f = 0; f < kFlight; ++f)
+        if (x + f * threads < n) y[f] = __ldcs(src4 + x + f * threads);
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f)
+        if (x + f * threads < n) dst4[x + f * threads] = y[f];
     }
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f)
-      if (x0 + f * threads < n) *reinterpret_cast<uint4*>(to + off[f]) = y[f];
+    return;
+  }
+#pragma unroll 2
+  for (int x = tid; x < n; x += threads) {
+    const int q = x / run, i2 = q / n1;
+    const int64_t o = (i2 * s2 + (q - i2 * n1) * s1) / 16 + (x - q * run);
+    dst4[o] = __ldcs(src4 + o);
   }
 }
 
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
-  sm100::pdl_wait();
   const int b = blockIdx.x, part = blockIdx.y;  // part: 2 * layer + (0: K, 1: V)
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
-  if (__ldcg(w.fail)) {
+  sm100::pdl_wait();
+  const int fail = __ldcg(w.fail);
+  const int2 copy = __ldcg(w.copy + b);
+  const int4 row = __ldcg(w.row + b);
+  const int parent = row.x, shared = row.y, want = row.z, start = row.w;
+  if (fail) {
     if (part == 0) {
       for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
         p.table_out[(int64_t)b * p.max_pages + j] = __ldg(p.table + (int64_t)b * p.max_pages + j);
@@ -329,24 +400,21 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
     }
     return;
   }
-  const int copy = __ldcg(w.copy_of + b);
-  if (part > 0 && copy < 0) return;
-  const Move m = load_move(p, b);
-  const int start = __ldcg(w.start + b), shared = m.kept - (copy >= 0);
+  if (part > 0 && copy.x < 0) return;
   if (part == 0) {
-    const int32_t* past = p.table + (int64_t)max(m.parent, 0) * p.max_pages;
+    const int32_t* past = p.table + (int64_t)max(parent, 0) * p.max_pages;
     for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
       p.table_out[(int64_t)b * p.max_pages + j] =
-          j < shared ? __ldg(past + j) : j < m.want ? __ldcg(w.free_list + start + j - shared) : -1;
+          j < shared ? __ldg(past + j) : j < want ? __ldcg(w.free_list + start + j - shared) : -1;
     if (threadIdx.x == 0) {
       p.len_out[b] = __ldg(p.new_len + b);
-      if (copy >= 0) atomicSub(p.ref_out + copy, 1);
+      if (copy.x >= 0) atomicSub(p.ref_out + copy.x, 1);
     }
-    if (copy < 0) return;
+    if (copy.x < 0) return;
   }
   const int dst = __ldcg(w.free_list + start);
   char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
-  copy_tokens(p.pool, base, copy, dst, m.keep & ((1 << p.pool.page_shift) - 1), threadIdx.x, blockDim.x);
+  copy_tokens(p.pool, base, copy.x, dst, copy.y, threadIdx.x, blockDim.x);
 }
 
 // ---- compact -------------------------------------------------------------------------------
@@ -370,40 +438,54 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   cg::cluster_group cl = cg::this_cluster();
   sm100::pdl_launch_dependents();
   __shared__ int sums[kPlanWarps];
-  __shared__ Counts slot[2];
+  __shared__ Exchange exchange[2];
   const int tid = threadIdx.x, rank = (int)cl.block_rank();
   const int N = p.pool.n_pages;
   const CompactWs w = compact_ws(p.ws, N);
   int p0, p1;
   share(N, rank, p0, p1);
   int held = 0, bad = 0;
-  for (int i = p0 + tid; i < p1; i += kPlanThreads) {
-    const int r = __ldg(p.ref + i);
-    bad |= r < 0;
-    held += r > 0;
+  for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
+    const int4 r = load_four<true>(p.ref, i, p1, 0);
+    bad |= (r.x | r.y | r.z | r.w) < 0;
+    held += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
   const int held_sum = block_sum(held, sums), bad_any = __syncthreads_or(bad);
   Counts before, none;
-  const Counts all = cluster_exchange(cl, &slot[0], Counts{0, held_sum, bad_any}, before);
+  const Counts all = cluster_exchange(cl, &exchange[0], Counts{0, held_sum, bad_any}, before);
   const int used = all.b;
   const bool fail = all.c > 0;
   int below = 0;  // held pages below `used`
-  for (int i = p0 + tid; i < min(p1, used); i += kPlanThreads) below += __ldg(p.ref + i) > 0;
-  const int held_below = cluster_exchange(cl, &slot[1], Counts{0, block_sum(below, sums), 0}, none).b;
+  for (int i = p0 + 4 * tid; i < min(p1, used); i += 4 * kPlanThreads) {
+    const int4 r = load_four<true>(p.ref, i, min(p1, used), 0);
+    below += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+  }
+  const int held_below = cluster_exchange(cl, &exchange[1], Counts{0, block_sum(below, sums), 0}, none).b;
 
   int at = before.b;
-  for (int base = p0; base < p1; base += kPlanThreads) {
-    const int i = base + tid;
-    const int r = i < p1 ? __ldg(p.ref + i) : 0;
+  for (int base = p0; base < p1; base += 4 * kPlanThreads) {
+    const int i = base + 4 * tid;
+    const int4 r = load_four<true>(p.ref, i, p1, 0);
     int total;
-    const int before = at + block_exclusive(r > 0, sums, total);  // held pages before page i
+    // held pages before the next page
+    int held_before = at + block_exclusive((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), sums, total);
     at += total;
+    auto place = [&](int count, int page, int& map) {
+      const bool moves = !fail && count > 0 && page >= used;
+      if (moves) w.src[held_before - held_below] = page;
+      if (!fail && count == 0 && page < used) w.dst[page - held_before] = page;
+      map = count > 0 ? page : -1;
+      held_before += count > 0;
+      return moves ? 0 : count;
+    };
+    int4 map, out;
+    out.x = i < p1 ? place(r.x, i, map.x) : 0;
+    out.y = i + 1 < p1 ? place(r.y, i + 1, map.y) : 0;
+    out.z = i + 2 < p1 ? place(r.z, i + 2, map.z) : 0;
+    out.w = i + 3 < p1 ? place(r.w, i + 3, map.w) : 0;
     if (i >= p1) continue;
-    const bool moves = !fail && r > 0 && i >= used, hole = !fail && r == 0 && i < used;
-    if (moves) w.src[before - held_below] = i;
-    if (hole) w.dst[i - before] = i;
-    p.page_map[i] = r > 0 ? i : -1;
-    p.ref_out[i] = moves ? 0 : r;
+    store_four(p.page_map, i, p1, map);
+    store_four(p.ref_out, i, p1, out);
   }
   cl.sync();
   const int n = fail ? 0 : used - held_below;
@@ -421,20 +503,26 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   cl.sync();
 }
 
-// One block a table row or a (move, layer, K or V); the number of moves is
-// known on the device only, so a fixed grid walks over them.
+// A block takes (move, layer, K or V) items; the number of moves is known on the
+// device only, so a fixed grid walks over them. The table's entries go to the
+// blocks from the last one down: with few moves those have nothing to copy.
 __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams p) {
-  sm100::pdl_wait();
   const CompactWs w = compact_ws(p.ws, p.pool.n_pages);
+  const int parts = 2 * p.pool.n_layers, tokens = 1 << p.pool.page_shift;
   const int64_t entries = (int64_t)p.B * p.max_pages;
-  const bool fail = __ldcg(w.moves + 1) != 0;
-  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < entries; x += (int64_t)gridDim.x * blockDim.x) {
-    const int e = __ldg(p.table + x);
-    p.table_out[x] = fail ? e : e >= 0 && e < p.pool.n_pages ? __ldcg(p.page_map + e) : -1;
+  int64_t x = blockIdx.x, e = (int64_t)(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
+  int page = e < entries ? __ldg(p.table + e) : -1;
+  sm100::pdl_wait();
+  const int2 moves = __ldcg(reinterpret_cast<const int2*>(w.moves));
+  const int n = moves.x;
+  const bool fail = moves.y != 0;
+  for (; e < entries; e += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t next = e + (int64_t)gridDim.x * blockDim.x;
+    const int now = page;
+    if (next < entries) page = __ldg(p.table + next);
+    p.table_out[e] = fail ? now : now >= 0 && now < p.pool.n_pages ? __ldcg(p.page_map + now) : -1;
   }
-  const int n = __ldcg(w.moves), parts = 2 * p.pool.n_layers;
-  const int tokens = 1 << p.pool.page_shift;
-  for (int64_t x = blockIdx.x; x < (int64_t)n * parts; x += gridDim.x) {
+  for (; x < (int64_t)n * parts; x += gridDim.x) {
     const int i = (int)(x / parts), part = (int)(x - (int64_t)i * parts);
     char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
     copy_tokens(p.pool, base, __ldcg(w.src + i), __ldcg(w.dst + i), tokens, threadIdx.x, blockDim.x);
@@ -445,7 +533,7 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams 
 
 size_t update_ws_bytes(int32_t B, int32_t n_pages) {
   const size_t n = ((size_t)n_pages + 3) & ~(size_t)3, b = ((size_t)B + 3) & ~(size_t)3;
-  return (4 + 4 * n + 2 * b) * sizeof(int32_t);
+  return (4 + 6 * b + 4 * n) * sizeof(int32_t);
 }
 
 size_t compact_ws_bytes(int32_t n_pages) {
