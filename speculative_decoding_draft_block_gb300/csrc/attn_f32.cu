@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;
+  sm100::pdl_wait();
   const int64_t total = locate_shares<F, kThreads, 1>(p, kBM, share, sh.work);
   if (tid == 0) part.cut[share].valid = 0;
   sm100::pdl_launch_dependents();
@@ -255,20 +256,12 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
   static const cudaError_t ready = cudaFuncSetAttribute(
       attn_f32_kernel<D, kBM>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Tiles<D, kBM>));
   if (ready != cudaSuccess) return ready;
-  attn_f32_kernel<D, kBM><<<F::kShares, kThreads, sizeof(Tiles<D, kBM>), s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_early(attn_f32_kernel<D, kBM>, dim3(F::kShares), dim3(kThreads), sizeof(Tiles<D, kBM>), s, p);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.max_q * p.group;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(F::kShares, (unsigned)(((most < kBM ? most : kBM) + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<F, D, float>, p, kBM, kBM);
+  return launch_early(attn_join_kernel<F, D, float>, dim3(F::kShares, (unsigned)(((most < kBM ? most : kBM) + 7) / 8)),
+                      dim3(256), 0, s, p, kBM, kBM);
 }
 
 }  // namespace

@@ -225,10 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile_rows = per_tile * p.group;      // rows in use of a row tile
   const int unit_rows = (kPair ? 2 : 1) * tile_rows;
 
-  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle is taken from address bits
-    if (tid == 0) report(p.status, kErrCuda);
-    return;
-  }
+  // the swizzle is taken from address bits (the array's alignment; never seen otherwise)
+  const bool misplaced = (smem_u32(smem) & 1023u) != 0;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
@@ -266,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  if (F::begin(total, v0) >= F::begin(total, v0 + kLists)) {
+  if (misplaced || F::begin(total, v0) >= F::begin(total, v0 + kLists)) {
+    if (misplaced && tid == 0) report(p.status, kErrCuda);
     if (tid < kLists) part.cut[v0 + tid].valid = 0;
     if (warp == 2) tmem_dealloc(tmem, 512);
     return;
@@ -837,24 +836,13 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     if (!encode_tmap_bf16(&mk, p.pool.k, 4, dims, str, box) || !encode_tmap_bf16(&mv, p.pool.v, 4, dims, str, box))
       return cudaErrorInvalidValue;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kMaxAttnCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, kPair>, p, mq, mk, mv);
+  cudaError_t e = launch_early(attn_tc_kernel<D, kPair>, dim3(kMaxAttnCtas), dim3(kThreads), Layout<D>::kBytes, s, p, mq,
+                               mk, mv);
   if (e != cudaSuccess) return e;
   using F = Form<kPair>;
   const int rows = p.max_q <= per_tile ? p.max_q * p.group : F::kPartRows;
-  cfg.gridDim = dim3(F::kShares, (rows + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<F, D, __nv_bfloat16>, p, kTile, per_tile * p.group);
+  return launch_early(attn_join_kernel<F, D, __nv_bfloat16>, dim3(F::kShares, (rows + 7) / 8), dim3(256), 0, s, p, kTile,
+                      per_tile * p.group);
 }
 
 }  // namespace

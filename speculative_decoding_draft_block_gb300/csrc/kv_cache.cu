@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv_internal.h"
+#include "sm100.cuh"
 
 namespace ds {
 namespace {
@@ -31,6 +32,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int tid = threadIdx.x;
   if (tid < kAppendTokens) ends[tid] = 0;
   int before = 0;
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   __syncthreads();
   for (int i = tid; i < p.B; i += kAppendThreads) {
     const int e = __ldg(p.q_start + i + 1);
@@ -139,8 +142,7 @@ bool overlap(const void* a, const void* b, size_t na, size_t nb) {
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   const int blocks = (p.T + kAppendTokens - 1) / kAppendTokens;
-  append_kernel<<<blocks, kAppendThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, s, p);
 }
 
 }  // namespace ds

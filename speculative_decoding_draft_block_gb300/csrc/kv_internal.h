@@ -108,6 +108,24 @@ __device__ __forceinline__ Request load_request(const int32_t* q_start, const in
   return r;
 }
 
+// A launch that is set up while the kernel before it on the stream finishes; the
+// kernel waits for that one (griddepcontrol.wait) before it touches any memory
+// that another kernel may write.
+template <class... A, class... B>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const B&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are built for
 
 size_t update_ws_bytes(int32_t B, int32_t n_pages);

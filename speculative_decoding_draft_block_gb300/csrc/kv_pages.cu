@@ -5,7 +5,8 @@
 // counts and prefix sums over the pool's pages and the requests need a few
 // barriers over all of the work, and a cluster's hardware barrier gives them
 // without a grid-wide wait. The second launch spreads what is left (tables and
-// page contents) over the whole GPU, reading the plan from the workspace.
+// page contents) over the whole GPU, reading the plan from the workspace (past the
+// first-level cache: it is set up, and may be resident, while the plan runs).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -17,7 +18,6 @@ namespace cg = cooperative_groups;
 namespace ds {
 namespace {
 
-constexpr int kCluster = 8;  // portable size
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
@@ -64,6 +64,7 @@ struct Exchange {
   Counts mine, before, all;
 };
 
+template <int kCluster>
 __device__ __forceinline__ Counts cluster_exchange(cg::cluster_group& cl, Exchange* x, Counts mine, Counts& before) {
   if (threadIdx.x == 0) x->mine = mine;
   cl.sync();
@@ -93,6 +94,7 @@ __device__ __forceinline__ Counts cluster_exchange(cg::cluster_group& cl, Exchan
 }
 
 // Range of n items that CTA `rank` of the cluster takes, a multiple of 4 at its start.
+template <int kCluster>
 __device__ __forceinline__ void share(int n, int rank, int& first, int& last) {
   const int per = ((n + kCluster - 1) / kCluster + 3) & ~3;
   first = min(n, rank * per);
@@ -198,18 +200,20 @@ __device__ __forceinline__ void store_four(int32_t* to, int i, int end, int4 v) 
 // parent's length, its table entry, that page's holders) at the latency of the L2,
 // so a request's move is looked up once and kept in shared memory, and four pages
 // go to a thread, so that a pool of 32768 pages takes one scan.
+template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     update_plan_kernel(const UpdateParams p) {
   cg::cluster_group cl = cg::this_cluster();
   sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   __shared__ PlanShared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int rank = (int)cl.block_rank();
   const int N = p.pool.n_pages, B = p.B;
   const UpdateWs w = update_ws(p.ws, B, N);
   int p0, p1, b0, b1;
-  share(N, rank, p0, p1);
-  share(B, rank, b0, b1);
+  share<kCluster>(N, rank, p0, p1);
+  share<kCluster>(B, rank, b0, b1);
   auto move_of = [&](int b) { return b - b0 < kPlanThreads ? sh.move[b - b0] : load_move(p, b); };
 
   // holders as they are; the entries of `writers` and `first` that will be used
@@ -291,7 +295,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   const int free_sum = block_sum(free, sh.sums);
   const int bad_any = __syncthreads_or(bad);
   Counts before;
-  const Counts all = cluster_exchange(cl, &sh.exchange, Counts{(long long)sh.need, free_sum, bad_any}, before);
+  const Counts all = cluster_exchange<kCluster>(cl, &sh.exchange, Counts{(long long)sh.need, free_sum, bad_any}, before);
   const long long need_all = all.a;
   const bool bad_all = all.c > 0, fail = bad_all || need_all > all.b;
   if (fail && rank == 0 && tid == 0) report(p.status, bad_all ? kErrBounds : kErrPages);
@@ -387,6 +391,7 @@ __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int s
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
   const int b = blockIdx.x, part = blockIdx.y;  // part: 2 * layer + (0: K, 1: V)
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
+  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
   const int fail = __ldcg(w.fail);
   const int2 copy = __ldcg(w.copy + b);
@@ -433,17 +438,19 @@ __host__ __device__ inline CompactWs compact_ws(int32_t* ws, int32_t N) {
   return w;
 }
 
+template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const CompactParams p) {
   cg::cluster_group cl = cg::this_cluster();
   sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   __shared__ int sums[kPlanWarps];
   __shared__ Exchange exchange[2];
   const int tid = threadIdx.x, rank = (int)cl.block_rank();
   const int N = p.pool.n_pages;
   const CompactWs w = compact_ws(p.ws, N);
   int p0, p1;
-  share(N, rank, p0, p1);
+  share<kCluster>(N, rank, p0, p1);
   int held = 0, bad = 0;
   for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
     const int4 r = load_four<true>(p.ref, i, p1, 0);
@@ -452,7 +459,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
   const int held_sum = block_sum(held, sums), bad_any = __syncthreads_or(bad);
   Counts before, none;
-  const Counts all = cluster_exchange(cl, &exchange[0], Counts{0, held_sum, bad_any}, before);
+  const Counts all = cluster_exchange<kCluster>(cl, &exchange[0], Counts{0, held_sum, bad_any}, before);
   const int used = all.b;
   const bool fail = all.c > 0;
   int below = 0;  // held pages below `used`
@@ -460,7 +467,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     const int4 r = load_four<true>(p.ref, i, min(p1, used), 0);
     below += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
-  const int held_below = cluster_exchange(cl, &exchange[1], Counts{0, block_sum(below, sums), 0}, none).b;
+  const int held_below = cluster_exchange<kCluster>(cl, &exchange[1], Counts{0, block_sum(below, sums), 0}, none).b;
 
   int at = before.b;
   for (int base = p0; base < p1; base += 4 * kPlanThreads) {
@@ -511,8 +518,9 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams 
   const int parts = 2 * p.pool.n_layers, tokens = 1 << p.pool.page_shift;
   const int64_t entries = (int64_t)p.B * p.max_pages;
   int64_t x = blockIdx.x, e = (int64_t)(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
-  int page = e < entries ? __ldg(p.table + e) : -1;
+  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
+  int page = e < entries ? __ldg(p.table + e) : -1;
   const int2 moves = __ldcg(reinterpret_cast<const int2*>(w.moves));
   const int n = moves.x;
   const bool fail = moves.y != 0;
@@ -540,34 +548,26 @@ size_t compact_ws_bytes(int32_t n_pages) {
   return (4 + 2 * (((size_t)n_pages / 2 + 4) & ~(size_t)3)) * sizeof(int32_t);
 }
 
-// The second launch is set up while the plan runs and waits for it (what the plan
-// writes is read past the first-level cache, __ldcg).
-template <class P>
-cudaError_t launch_apply(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t s) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
+// Whether one CTA plans: its barriers are cheaper than a cluster's (8 is the
+// portable size), its reads fewer at a time. Update of 16 requests and 1024 pages:
+// 11.0 us, by a cluster 12.3; of 128 and 4096: 17.2 and 12.3. Compaction of 1024
+// pages: 12.5 and 14.4 us; of 8192: 36.9 and 33.9.
+bool one_cta(int32_t B, int32_t n_pages) { return n_pages <= 1024 && B <= 64; }
 
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s) {
-  update_plan_kernel<<<kCluster, kPlanThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = one_cta(p.B, p.pool.n_pages)
+                            ? launch_early(update_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, s, p)
+                            : launch_early(update_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, s, p);
   if (e != cudaSuccess) return e;
-  return launch_apply(update_apply_kernel, p, dim3(p.B, 2 * p.pool.n_layers), s);
+  return launch_early(update_apply_kernel, dim3(p.B, 2 * p.pool.n_layers), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  compact_plan_kernel<<<kCluster, kPlanThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = one_cta(0, p.pool.n_pages)
+                            ? launch_early(compact_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, s, p)
+                            : launch_early(compact_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, s, p);
   if (e != cudaSuccess) return e;
-  return launch_apply(compact_apply_kernel, p, dim3(152 * 8), s);
+  return launch_early(compact_apply_kernel, dim3(152 * 8), dim3(256), 0, s, p);
 }
 
 }  // namespace ds
