@@ -99,6 +99,7 @@ struct Header {
   uint64_t drain[2];
   uint32_t info[kMaxSlots];
   uint32_t entry[kMaxSlots];  // 1 + the number of the entry that the slot was last given to
+  uint32_t staged[2];         // softmax warps that are done with a piece's staging slot
   int ended[2];         // tiles of a stream's share, -1 while not known
   uint32_t tmem;
   int abort_flag;
@@ -115,10 +116,9 @@ static_assert(sizeof(Header) <= kHeader, "header");
 //   - The solo issuers pass their own stream's entries only, and with five slots
 //     the slot's last entry is the other stream's. So they wait for the entry's
 //     number in `entry` first: the producer writes it once the slot is released.
-//   - Producers wait for the release of the entry kSlots before theirs. The slot's
-//     entry before that, 2 * kSlots back, was released earlier: it is an earlier
-//     entry of the producer's own list or precedes, in its issuer's order, one
-//     whose release this producer has waited for (releases are commits, in order).
+//   - So do the producers, before they wait for the release of the entry kSlots
+//     before theirs: that its number stands there means that the one before it,
+//     which may be another producer's, has been released.
 template <int kSlots>
 struct RingPos {
   uint32_t slot = 0, parity = 0, number = 0;
@@ -135,6 +135,23 @@ struct RingPos {
 // Key tiles, shares of the work list and rows of partial results of a form.
 template <bool kPair>
 struct Form : WorkForm<kTile, kPair ? kMaxAttnCtas : 2 * kMaxAttnCtas, kPair ? 2 * kTile : kTile> {};
+
+// Waits until the entry before this filling of a slot stands in it (bounded).
+__device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile int* abort_flag,
+                                            int32_t* status) {
+  const volatile uint32_t* at = entry;
+#pragma unroll 1
+  for (uint32_t i = 0; *at != number; ++i) {
+    __nanosleep(40);
+    if ((i & 255) != 255) continue;
+    if (i >= (kWaitPolls << 8)) {
+      *abort_flag = 1;
+      report(status, kErrTimeout);
+    }
+    if (*abort_flag) return false;
+  }
+  return true;
+}
 
 // Bounded wait of one thread (about a second with kWaitPolls, a minute with
 // kIdlePolls, for roles that may have nothing to do for as long as a unit lasts).
@@ -187,24 +204,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 32 result columns of a row to memory, times `f`: bfloat16 output or float32 partial.
-__device__ __forceinline__ void store_bf16(char* to, const float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 x;
-    x.x = to_bf16x2(v[8 * i], v[8 * i + 1]);
-    x.y = to_bf16x2(v[8 * i + 2], v[8 * i + 3]);
-    x.z = to_bf16x2(v[8 * i + 4], v[8 * i + 5]);
-    x.w = to_bf16x2(v[8 * i + 6], v[8 * i + 7]);
-    reinterpret_cast<uint4*>(to)[i] = x;
-  }
-}
-__device__ __forceinline__ void store_f32(float* to, const float* v) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    reinterpret_cast<float4*>(to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-}
-
 // ---- the kernel --------------------------------------------------------------------------
 
 template <int D, bool kPair>
@@ -236,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.drain[i], 1);
       sh.ended[i] = -1;
+      sh.staged[i] = 0;
       for (int k = 0; k < kAhead; ++k) {
         mbar_init(&sh.piece_full[i][k], 1);
         mbar_init(&sh.piece_empty[i][k], kPair ? 8 : 4);  // softmax warps
@@ -308,6 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return 0;
       };
       auto wait_empty = [&](const RingPos<kSlots>& at) {
+        if (at.number >= (uint32_t)kSlots) {
+          ok = __all_sync(0xffffffffu, wait_number(&sh.entry[at.slot], at.number - kSlots + 1, abort_flag, p.status));
+          if (!ok) return false;
+        }
         ok = wait_bar(&sh.empty[at.slot], at.parity ^ 1, abort_flag, p.status);
         return ok;
       };
@@ -447,21 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         good = good && wait_one(bar, parity, abort_flag, p.status, kWaitPolls);
       };
       auto wait_entry = [&](const RingPos<kSlots>& at) {
-        if (!kPair) {
-          volatile uint32_t* entry = &sh.entry[at.slot];
-          for (uint32_t i = 0; good && *entry != at.number + 1; ++i) {
-            __nanosleep(40);
-            if ((i & 255) == 255 && *abort_flag) good = false;
-            if (i > (kWaitPolls << 8)) {
-              *abort_flag = 1;
-              report(p.status, kErrTimeout);
-              good = false;
-            }
-          }
-        }
+        if (!kPair) good = good && wait_number(&sh.entry[at.slot], at.number + 1, abort_flag, p.status);
         wait1(&sh.full[at.slot], at.parity);
       };
-      // S = Q K^T of stream s with the keys in `slot`; `free_k`: no other stream reads them
+      // S = Q K^T of stream s with the keys in `slot`; `free_k`: nothing else needs the slot
       auto qk = [&](int s, uint32_t slot, bool last, bool free_k) {
         if (!good) return;
         tc_fence_after();
@@ -548,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (good) mma_commit(&sh.empty[v_at]);
             } else {
               wait_entry(vp);
-              pv(s0, v_at, info & kFirst, info & kLast, true);
+              pv(s0, v_at, info & kFirst, info & kLast, !(info & kLast));
             }
             wait_entry(kp);
             next = info_of(kp);
@@ -569,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool two = info & kTwo;
           if (s == 1 && !two) return;
           if (info & kFirst) wait1(&sh.q_full[s], (q_par >> s) & 1);
-          qk(s, at, info & kLast, s == 1 || !two);
+          qk(s, at, info & kLast, (s == 1 || !two) && !(info & kLast));
         };
         uint32_t next = 0;
         if (elect_one()) {
@@ -607,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               pv(0, v_at, first, true, !two);
-              if (two) pv(1, v_at, first, true, true);
+              if (two) pv(1, v_at, first, true, false);
               wait_entry(kp);
               next = info_of(kp);
               if (!(next & kEnd)) {
@@ -637,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_tok = p.by_group.quotient(row), g = row - tile_tok * p.group;
     const int v = v0 + (kPair ? 0 : s);            // share
     uint32_t ns = 0, np = 0;                       // score tiles and pieces so far
+    uint32_t list_tiles = 0;                       // key tiles of the list so far
     const int list = kPair ? 0 : s;
     for (uint32_t k = 0;; ++k) {
       const uint32_t at = k % kAhead;
@@ -645,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.piece_empty[list][at]);
       if (x.n < 0) break;
+      list_tiles += x.n;
       if (kPair && s == 1 && x.rows <= tile_rows) continue;
       const int i = (kPair ? s * per_tile : 0) + tile_tok;  // token of the unit
       const bool valid = tile_tok < per_tile && i * p.group < x.rows;
@@ -761,32 +756,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++np;
       tc_fence_after();
-      // the result: the output, or a row of partial results
+      // The result: the output, or a row of partial results. A thread has a row and
+      // would store it in 32 pieces of 16 bytes, each to a line of its own across
+      // the warp (3.2 us for 256 rows). So the rows go through shared memory, a
+      // warp's 32 at a time, and leave in whole lines. The staging is the ring slot of
+      // the piece's last values (stream 0 of a pair: keys, since the other stream may
+      // still read the values); the last warp to finish releases it.
       const float ref = m == kNegInf ? kNegInf : m * c;
       const bool some = l > 0.f || l != l;
       const float f = !x.whole ? 1.f : some ? 1.f / l : 0.f;
       const size_t prow = (size_t)(v * 2 + x.slot) * F::kPartRows + (kPair ? s * kTile : 0) + row;
+      const uint32_t last_tile = list_tiles - 1;
+      const uint32_t stage_at = (kPair ? 2 * last_tile + s : 4 * last_tile + (s == 0 ? 2 : 4)) % kSlots;
       if (work) {
+        constexpr int kChunks = D / 8;       // 16-byte pieces of a staged row: D bfloat16 or D / 2 float32
+        constexpr int kAtOnce = 32 / kChunks;  // rows a warp stores with one instruction
+        uint4* stage = reinterpret_cast<uint4*>(sRing + stage_at * L::kTileBytes) + (warp & 3) * 32 * kChunks;
+        char* to = x.whole ? out : reinterpret_cast<char*>(part.out + prow * D);
+        const uint32_t there = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32_issue(tO + 32 * q, o);
-          tmem_ld_wait(o);
-          float y[32];
+        for (int pass = 0; pass < (x.whole ? 1 : 2); ++pass) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {  // four pieces a time
+            uint4 y[4];
+            if (x.whole) {
+              uint32_t o[32];
+              tmem_ld32_issue(tO + 32 * q, o);
+              tmem_ld_wait(o);
 #pragma unroll
-          for (int w = 0; w < 32; ++w) y[w] = __uint_as_float(o[w]) * f;
-          if (valid) {
-            if (x.whole)
-              store_bf16(out + q * 64, y);
-            else
-              store_f32(part.out + prow * D + 32 * q, y);
+              for (int w = 0; w < 32; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const float* z = reinterpret_cast<const float*>(o + 8 * w);
+                y[w] = make_uint4(to_bf16x2(z[0], z[1]), to_bf16x2(z[2], z[3]), to_bf16x2(z[4], z[5]), to_bf16x2(z[6], z[7]));
+              }
+            } else {
+              uint32_t o[16];
+              tmem_ld16_issue(tO + pass * (D / 2) + 16 * q, o);
+              tmem_ld16_wait(o);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) y[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) stage[lane * kChunks + ((4 * q + w) ^ (lane & 7))] = y[w];
           }
+          __syncwarp();
+          const int r0 = lane / kChunks, ch = lane % kChunks;
+#pragma unroll 4
+          for (int r = r0; r < 32; r += kAtOnce) {
+            const uint4 y = stage[r * kChunks + (ch ^ (r & 7))];
+            char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+            if ((there >> r) & 1) reinterpret_cast<uint4*>(dst)[pass * kChunks + ch] = y;
+          }
+          __syncwarp();
         }
         if (valid) {
           if (!x.whole)
             part.stat[prow] = make_float2(ref, l);
           else if (lse != nullptr)
             *lse = some ? (ref + log2f(l)) * kLn2 : kNegInf;
+        }
+        fence_proxy_async_smem();  // the slot's next filling comes by TMA
+      }
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence_block();
+        if ((atomicAdd(&sh.staged[s], 1u) & 3u) == 3u) {
+          __threadfence_block();
+          mbar_arrive(&sh.empty[stage_at]);
         }
       }
       tc_fence_before();
@@ -848,7 +885,10 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s) {
-  const bool pair = p.max_q > kTile / p.group;
+  // Two row tiles a unit if the requests fill more than one on average. 128 requests
+  // of 136 rows each: pair 258 us, solo 386; of 8 to 136 rows: 236 and 216.
+  const int per_tile = kTile / p.group;
+  const bool pair = p.max_q > per_tile && p.T > (int64_t)p.B * per_tile;
   if (p.D == 128) return pair ? launch<128, true>(p, s) : launch<128, false>(p, s);
   return pair ? launch<64, true>(p, s) : launch<64, false>(p, s);
 }
