@@ -136,44 +136,40 @@ struct RingPos {
 template <bool kPair>
 struct Form : WorkForm<kTile, kPair ? kMaxAttnCtas : 2 * kMaxAttnCtas, kPair ? 2 * kTile : kTile> {};
 
-// Waits until the entry before this filling of a slot stands in it (bounded).
-__device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile int* abort_flag,
-                                            int32_t* status) {
+// Bounded waits. One that gives up sets the abort flag, which ends every role's
+// loop; the status is reported once, at the kernel's end (the waits are many and
+// inlined, and the warps' loops share one instruction cache).
+
+// Waits until the entry of that number stands in a slot.
+__device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile int* abort_flag) {
   const volatile uint32_t* at = entry;
 #pragma unroll 1
   for (uint32_t i = 0; *at != number; ++i) {
     __nanosleep(40);
     if ((i & 255) != 255) continue;
-    if (i >= (kWaitPolls << 8)) {
-      *abort_flag = 1;
-      report(status, kErrTimeout);
-    }
+    if (i >= (kWaitPolls << 8)) *abort_flag = 1;
     if (*abort_flag) return false;
   }
   return true;
 }
 
-// Bounded wait of one thread (about a second with kWaitPolls, a minute with
-// kIdlePolls, for roles that may have nothing to do for as long as a unit lasts).
+// By one thread: about a second with kWaitPolls, a minute with kIdlePolls, for
+// roles that may have nothing to do for as long as a unit lasts.
 constexpr uint32_t kIdlePolls = 1u << 22;
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
-                                         uint32_t polls) {
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t polls) {
 #pragma unroll 1
   for (uint32_t i = 0; !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {
     if ((i & 15) != 15) continue;
-    if (i >= polls) {
-      *abort_flag = 1;
-      report(status, kErrTimeout);
-    }
+    if (i >= polls) *abort_flag = 1;
     if (*abort_flag) return false;
   }
   return true;
 }
 
 // The same by a whole warp, with one answer for all lanes: warp-wide instructions follow.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                          uint32_t polls = kWaitPolls) {
-  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, status, polls));
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, polls));
 }
 
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
@@ -291,8 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       vp.add(kPair ? 1 : l == 0 ? 2 : 4);
       uint32_t q_par[2] = {1, 1}, np = 0;
       int n_tiles = 0;                                     // of the share so far
-      bool ok = true;
+      bool ok = true, ended = false;
       Piece x = {};
+      int j = 0;                                           // next tile of the piece
       const int32_t* table = nullptr;
       // Table entry of this lane's box of a key tile, kNoPage: no row of the unit sees
       // it. (Looked at when the tile is loaded, a tile later as a rule.)
@@ -302,129 +299,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return kNoPage;
         return __ldcg(table + (key >> shift));
       };
-      auto checked = [&](int page) {
-        if (page == kNoPage || (page >= 0 && page < p.pool.n_pages)) return page;
-        report(p.status, kErrBounds);
-        return 0;
-      };
-      auto wait_empty = [&](const RingPos<kSlots>& at) {
-        if (at.number >= (uint32_t)kSlots) {
-          ok = __all_sync(0xffffffffu, wait_number(&sh.entry[at.slot], at.number - kSlots + 1, abort_flag, p.status));
-          if (!ok) return false;
+      int page = kNoPage;                                  // of the next tile
+      volatile int* ends = sh.ended;
+      while (true) {
+        if (!ended && j == x.n) {  // the next piece
+          x = wk.next(p, unit_rows, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
+          j = 0;
+          // its first tile's page is on its way while it goes to the softmax
+          if (x.n > 0) {
+            table = p.block_table + (int64_t)x.b * p.max_pages;
+            page = page_of(x.tile0);
+          }
+          if (does_k) {
+            const uint32_t i = np % kAhead;
+            ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, kIdlePolls);
+            if (!ok) break;
+            if (lane == 0) {
+              sh.piece[l][i] = x;
+              mbar_arrive(&sh.piece_full[l][i]);
+            }
+            ++np;
+          }
+          if (x.n == 0) continue;
+          ended = x.n < 0;
+          if (ended) {
+            if (!does_k) break;
+            if (lane == 0) ends[l] = n_tiles;
+          } else if (does_k) {
+            const int s0 = kPair ? 0 : l, s1 = kPair ? (x.rows > tile_rows ? 1 : 0) : l;
+#pragma unroll 1
+            for (int s = s0; s <= s1; ++s) {
+              ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], abort_flag);
+              if (!ok) break;
+              if (s == 0) q_par[0] ^= 1;
+              if (s == 1) q_par[1] ^= 1;
+              if (elect_one()) {
+                mbar_expect_tx(&sh.q_full[s], (uint32_t)tile_rows * D * 2);
+                for (int y = 0; y < kHalves; ++y)
+                  tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128), &tmQ, &sh.q_full[s], y * 64,
+                                    x.h * p.group, x.token + (kPair ? s * per_tile : 0));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
         }
-        ok = wait_bar(&sh.empty[at.slot], at.parity ^ 1, abort_flag, p.status);
-        return ok;
-      };
-      auto load = [&](const CUtensorMap* map, const RingPos<kSlots>& at, int tile, int page, uint32_t info) {
-        if (!wait_empty(at)) return;
-        page = checked(page);
-        const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) {
-          sh.info[at.slot] = info;
-          *(volatile uint32_t*)&sh.entry[at.slot] = at.number + 1;
-          mbar_expect_tx(&sh.full[at.slot], __popc(some) * kHalves * box_bytes);
+        // The tile's entries; once the share has ended (solo) empty ones, since the
+        // other stream may have more tiles, until both have.
+        const int tile = x.tile0 + j;
+        int now = kNoPage;
+        uint32_t word = 0;
+        if (!ended) {
+          now = page;
+          if (j + 1 < x.n) page = page_of(tile + 1);
+          word = (x.rows > tile_rows ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
+          if (F::partly_seen(tile, x.lo, x.hi))
+            word |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
+          if (now != kNoPage && (now < 0 || now >= p.pool.n_pages)) {
+            report(p.status, kErrBounds);
+            now = 0;
+          }
         }
-        __syncwarp();
-        uint8_t* dst = sRing + at.slot * L::kTileBytes;
+        const uint32_t some = __ballot_sync(0xffffffffu, now != kNoPage);
         const int token = (tile * kTile) & (page_size - 1);
 #pragma unroll 1
-        for (int i = 0; i < boxes; ++i) {
-          const int pg = __shfl_sync(0xffffffffu, page, i);
-          if (pg >= 0 && elect_one()) {
-#pragma unroll
-            for (int y = 0; y < kHalves; ++y)
-              tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[at.slot], y * 64, token, x.h, pg);
+        for (int kv = does_k ? 0 : 1; kv < (does_v ? 2 : 1); ++kv) {
+          const uint32_t slot = kv ? vp.slot : kp.slot, parity = kv ? vp.parity : kp.parity;
+          const uint32_t number = kv ? vp.number : kp.number;
+          if (number >= (uint32_t)kSlots)
+            ok = __all_sync(0xffffffffu, wait_number(&sh.entry[slot], number - kSlots + 1, abort_flag));
+          ok = ok && wait_bar(&sh.empty[slot], parity ^ 1, abort_flag);
+          if (!ok) break;
+          if (ended) {
+            // (whether the other stream has ended is read after the wait for a slot: what
+            // is waited for may be its last entry, and no entry follows that one)
+            const int other = kPair ? 0 : __shfl_sync(0xffffffffu, ends[l ^ 1], 0);
+            word = kv == 0 && other >= 0 && (kPair || n_tiles >= other) ? kEnd : kNull;
+          }
+          if (lane == 0) {
+            sh.info[slot] = word;
+            *(volatile uint32_t*)&sh.entry[slot] = number + 1;
+            mbar_expect_tx(&sh.full[slot], __popc(some) * kHalves * box_bytes);
           }
           __syncwarp();
-        }
-      };
-      // an entry without a tile
-      auto mark = [&](const RingPos<kSlots>& at, uint32_t info) {
-        if (lane == 0) {
-          sh.info[at.slot] = info;
-          *(volatile uint32_t*)&sh.entry[at.slot] = at.number + 1;
-          mbar_arrive(&sh.full[at.slot]);
-        }
-        __syncwarp();
-      };
-      auto next_k = [&] {
-        // (solo: K0 is followed by three other entries' places, then by four)
-        kp.add(kPair ? 2 : l == 0 && n_tiles == 1 ? 3 : 4);
-      };
-      while (ok) {
-        x = wk.next(p, unit_rows, does_k && lane == 0 ? part.cut + v0 + l : nullptr, total);
-        // the first tile's page is on its way while the piece goes to the softmax
-        int page = kNoPage;
-        if (x.n > 0) {
-          table = p.block_table + (int64_t)x.b * p.max_pages;
-          page = page_of(x.tile0);
-        }
-        if (does_k) {
-          const uint32_t i = np % kAhead;
-          ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, p.status, kIdlePolls);
-          if (!ok) break;
-          if (lane == 0) {
-            sh.piece[l][i] = x;
-            mbar_arrive(&sh.piece_full[l][i]);
-          }
-          ++np;
-        }
-        if (x.n < 0) break;
-        if (x.n == 0) continue;
-        if (does_k) {
-          const bool two = x.rows > tile_rows;
-          for (int s = kPair ? 0 : l; s <= (kPair ? (int)two : l); ++s) {
-            ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], abort_flag, p.status);
-            if (!ok) break;
-            if (s == 0) q_par[0] ^= 1;
-            if (s == 1) q_par[1] ^= 1;
-            if (elect_one()) {
-              mbar_expect_tx(&sh.q_full[s], (uint32_t)per_tile * p.group * D * 2);
+          if (word & kEnd) break;
+          const CUtensorMap* map = kv ? &tmV : &tmK;
+          uint8_t* dst = sRing + slot * L::kTileBytes;
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, now, i);
+            if (pg != kNoPage && elect_one()) {
+#pragma unroll
               for (int y = 0; y < kHalves; ++y)
-                tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128), &tmQ, &sh.q_full[s], y * 64, x.h * p.group,
-                                  x.token + (kPair ? s * per_tile : 0));
+                tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[slot], y * 64, token, x.h, pg);
             }
             __syncwarp();
           }
-          if (!ok) break;
         }
-        for (int j = 0; j < x.n && ok; ++j) {
-          const int tile = x.tile0 + j, now = page;
-          if (j + 1 < x.n) page = page_of(tile + 1);
-          if (does_k) {
-            uint32_t info = (x.rows > tile_rows ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
-            if (F::partly_seen(tile, x.lo, x.hi))
-              info |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
-            load(&tmK, kp, tile, now, info);
-            if (!ok) break;
-          }
-          ++n_tiles;
-          next_k();
-          if (does_v) {
-            load(&tmV, vp, tile, now, 0);
-            vp.add(kPair ? 2 : 4);
-          }
-        }
-      }
-      if (kPair) {
-        if (ok && does_k && wait_empty(kp)) mark(kp, kEnd);
-      } else if (ok) {
-        // The other stream may have more tiles: fill this one's places until both have
-        // ended. Whether the other has is read after the wait for a slot: what is
-        // waited for may be the other's last entry, and no entry follows that one.
-        volatile int* ended = sh.ended;
-        if (lane == 0) ended[l] = n_tiles;
-        while (wait_empty(kp)) {
-          const int other = __shfl_sync(0xffffffffu, ended[l ^ 1], 0);
-          const bool end = other >= 0 && n_tiles >= other;
-          mark(kp, end ? kEnd : kNull);
-          if (end) break;
-          ++n_tiles;
-          next_k();
-          if (!wait_empty(vp)) break;
-          mark(vp, kNull);
-          vp.add(4);
-        }
+        if (!ok || (ended && (word & kEnd))) break;
+        ++n_tiles;
+        // (solo: K0 is followed by three other entries' places, then by four)
+        kp.add(kPair ? 2 : l == 0 && n_tiles == 1 ? 3 : 4);
+        vp.add(kPair ? 2 : 4);
+        if (!ended) ++j;
       }
       __syncwarp();
     } else {
@@ -448,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // as three products. `good`: no wait has given up (that lane's flag).
       bool good = true;
       auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-        good = good && wait_one(bar, parity, abort_flag, p.status, kWaitPolls);
+        good = good && wait_one(bar, parity, abort_flag, kWaitPolls);
       };
       auto wait_entry = [&](const RingPos<kSlots>& at) {
-        if (!kPair) good = good && wait_number(&sh.entry[at.slot], at.number + 1, abort_flag, p.status);
+        if (!kPair) good = good && wait_number(&sh.entry[at.slot], at.number + 1, abort_flag);
         wait1(&sh.full[at.slot], at.parity);
       };
       // S = Q K^T of stream s with the keys in `slot`; `free_k`: nothing else needs the slot
@@ -510,38 +487,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
+      uint32_t info = 0;
       if (!kPair) {
+        bool due = false;  // a tile's scores are made, its product with the values is due
         // S | O S' | O' S'' ...: a region does the product with the weights and the next scores
-        uint32_t next = 0;
-        if (elect_one()) {
-          wait_entry(kp);
-          next = info_of(kp);
-          if (!(next & (kNull | kEnd))) {
-            wait1(&sh.q_full[s0], q_par);
-            qk(s0, kp.slot, next & kLast, true);
-          }
-        }
-        uint32_t info = share_info(next);
+        uint32_t k_was = 0;
         while (true) {
-          if (info & kEnd) {
-            if (!(info & kNull) && elect_one()) mma_commit(&sh.empty[kp.slot]);
-            __syncwarp();
-            break;
-          }
-          const uint32_t k_was = uniform(kp.slot);
-          next_k();
+          if (due && (info & (kPart | kNull)) == kPart) clear(info);
           const uint32_t k_at = uniform(kp.slot), v_at = uniform(vp.slot);
-          if (info & kFirst) q_par ^= 1;
-          if ((info & (kPart | kNull)) == kPart) clear(info);
-          next = 0;
+          uint32_t next = 0;
           if (elect_one()) {
-            if (info & kNull) {  // releases of unused entries, after those before them
-              mma_commit(&sh.empty[k_was]);
+            if (due) {
+              if (info & kNull) mma_commit(&sh.empty[k_was]);  // (unused entries: releases after those before them)
               wait_entry(vp);
-              if (good) mma_commit(&sh.empty[v_at]);
-            } else {
-              wait_entry(vp);
-              pv(s0, v_at, info & kFirst, info & kLast, !(info & kLast));
+              if (info & kNull) {
+                if (good) mma_commit(&sh.empty[v_at]);
+              } else {
+                pv(s0, v_at, info & kFirst, info & kLast, !(info & kLast));
+              }
             }
             wait_entry(kp);
             next = info_of(kp);
@@ -550,19 +513,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               qk(s0, k_at, next & kLast, true);
             }
           }
-          if (!(info & kNull)) p_par ^= 1u << s0;
-          next_v();
+          if (due) {
+            if (!(info & kNull)) p_par ^= 1u << s0;
+            next_v();
+          }
           info = share_info(next);
+          if (info & kEnd) break;
+          due = true;
+          k_was = k_at;
+          if (info & kFirst) q_par ^= 1;
+          next_k();
         }
       } else if (warp == 2) {
         // S0 S1 | O0 S0' O1 S1' | ...: a stream's scores are made while the other's go
         // through the softmax. One warp for both streams: products of two warps
         // interleave on the tensor core and take longer (1.01 against 1.31 PFLOP/s).
-        auto scores = [&](int s, uint32_t at, uint32_t info) {
-          const bool two = info & kTwo;
+        auto scores = [&](int s, uint32_t at, uint32_t word) {
+          const bool two = word & kTwo;
           if (s == 1 && !two) return;
-          if (info & kFirst) wait1(&sh.q_full[s], (q_par >> s) & 1);
-          qk(s, at, info & kLast, (s == 1 || !two) && !(info & kLast));
+          if (word & kFirst) wait1(&sh.q_full[s], (q_par >> s) & 1);
+          qk(s, at, word & kLast, (s == 1 || !two) && !(word & kLast));
         };
         uint32_t next = 0;
         if (elect_one()) {
@@ -573,13 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             scores(1, kp.slot, next);
           }
         }
-        uint32_t info = share_info(next);
-        while (true) {
-          if (info & kEnd) {
-            if (!(info & kNull) && elect_one()) mma_commit(&sh.empty[kp.slot]);
-            __syncwarp();
-            break;
-          }
+        info = share_info(next);
+        while (!(info & kEnd)) {
           const bool two = info & kTwo, first = info & kFirst, last = info & kLast;
           if (first) q_par ^= two ? 3u : 1u;
           next_k();
@@ -614,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           info = share_info(next);
         }
       }
+      if ((info & (kEnd | kNull)) == kEnd && elect_one()) mma_commit(&sh.empty[kp.slot]);
+      __syncwarp();
       if (elect_one()) mma_commit(&sh.drain[warp - 2]);
       __syncwarp();
       drain_bar(&sh.drain[warp - 2], 0);  // no product in flight when TMEM is freed
@@ -634,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int list = kPair ? 0 : s;
     for (uint32_t k = 0;; ++k) {
       const uint32_t at = k % kAhead;
-      if (!wait_bar(&sh.piece_full[list][at], (k / kAhead) & 1, abort_flag, p.status, kIdlePolls)) break;
+      if (!wait_bar(&sh.piece_full[list][at], (k / kAhead) & 1, abort_flag, kIdlePolls)) break;
       const Piece x = sh.piece[list][at];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.piece_empty[list][at]);
@@ -664,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int it = 0; it < x.n; ++it) {
         const int key = (x.tile0 + it) * kTile;
-        ok = wait_bar(&sh.s_full[s], ns & 1, abort_flag, p.status);
+        ok = wait_bar(&sh.s_full[s], ns & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (work) {
@@ -752,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
       }
       if (!ok) break;
-      ok = wait_bar(&sh.pv_done[s], np & 1, abort_flag, p.status);
+      ok = wait_bar(&sh.pv_done[s], np & 1, abort_flag);
       if (!ok) break;
       ++np;
       tc_fence_after();
@@ -833,8 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Each load has been waited for by an issuer, except after an abort: then wait
   // (with a limit) until nothing can be in flight when the CTA exits.
-  if (*abort_flag)
+  if (*abort_flag) {
+    if (tid == 0) report(p.status, kErrTimeout);
     for (int i = 0; i < 64; ++i) __nanosleep(20000);
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
