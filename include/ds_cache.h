@@ -96,8 +96,10 @@ ds_status ds_cache_append(const ds_append_args* args, ds_stream_t stream);
  * and gets, with s_j = scale * (q . k_j),
  *     lse = ln sum_j exp(s_j),   out = sum_j exp(s_j - lse) v_j.
  * A row that sees nothing gets out = 0 and lse = -inf. What lies in the pages
- * outside every row's view (past kv_len, before the window) has no effect
- * whatever its bits; pages that no row sees need no table entry.
+ * outside a row's view (past kv_len, before the window, later tokens) has no
+ * effect on it, whatever its bits; pages that no row sees need no table entry.
+ * (Values that are not finite, seen by some rows of a request and not by others,
+ * cost those others a second, slow computation.)
  * bfloat16: products and sums in float32, the weights exp(s_j - r) of the
  * value product rounded to bfloat16. float32: all in float32.
  */

@@ -227,10 +227,43 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
         copies_commit();
     }
     copies_wait<0>();
+    const int key0 = max(x.lo, x.tile0 * kKeyTile), key1 = min(x.hi, (x.tile0 + x.n) * kKeyTile);
 #pragma unroll
     for (int i = 0; i < kRM; ++i) {
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      // A value that is not finite, of a key that other rows of the unit see and this
+      // one does not, has come in with its weight of zero: the row's sums again, from
+      // what it sees (each thread its columns).
+      float probe = 0.f;
+#pragma unroll
+      for (int k = 0; k < kC; ++k)
+        probe = fmaf(o[i][k].x, 0.f, fmaf(o[i][k].y, 0.f, fmaf(o[i][k].z, 0.f, fmaf(o[i][k].w, 0.f, probe))));
+      if (valid[i] && probe != probe && l[i] == l[i] && (lo[i] > key0 || hi[i] < key1)) {
+#pragma unroll
+        for (int k = 0; k < kC; ++k) o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float ref = m[i] == kNegInf ? 0.f : m[i];
+#pragma unroll 1
+        for (int key = max(key0, lo[i]); key < min(key1, hi[i]); ++key) {
+          const int page = __ldg(table + (key >> shift));
+          if (page < 0 || page >= p.pool.n_pages) break;  // (reported above)
+          const int64_t at = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride + (int64_t)(key & mask) * p.pool.token_stride;
+          const float* kk = reinterpret_cast<const float*>(p.pool.k + at);
+          const float* vv = reinterpret_cast<const float*>(p.pool.v + at);
+          float s = 0.f;
+#pragma unroll 1
+          for (int d = 0; d < D; ++d) s = fmaf(sh.q[ty * kRM + i][d], kk[d], s);
+          const float w = ex2_approx(s * c - ref);
+#pragma unroll
+          for (int k = 0; k < kC; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(vv + tx * 4 + 64 * k);
+            o[i][k].x = fmaf(w, v.x, o[i][k].x);
+            o[i][k].y = fmaf(w, v.y, o[i][k].y);
+            o[i][k].z = fmaf(w, v.z, o[i][k].z);
+            o[i][k].w = fmaf(w, v.w, o[i][k].w);
+          }
+        }
+      }
       if (!valid[i]) continue;
       const bool some = l[i] > 0.f || l[i] != l[i];
       const float f = !x.whole ? 1.f : some ? 1.f / l[i] : 0.f;
@@ -247,6 +280,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
           *lse[i] = some ? (m[i] + log2f(l[i])) * kLn2 : kNegInf;
       }
     }
+    __syncthreads();  // Q is read
   }
 }
 

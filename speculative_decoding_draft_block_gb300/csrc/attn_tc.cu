@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4* stage = reinterpret_cast<uint4*>(sRing + stage_at * L::kTileBytes) + (warp & 3) * 32 * kChunks;
         char* to = x.whole ? out : reinterpret_cast<char*>(part.out + prow * D);
         const uint32_t there = __ballot_sync(0xffffffffu, valid);
+        float probe = 0.f;  // NaN once a sum is not finite
 #pragma unroll 1
         for (int pass = 0; pass < (x.whole ? 1 : 2); ++pass) {
 #pragma unroll 1
@@ -751,7 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32_issue(tO + 32 * q, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int w = 0; w < 32; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
+              for (int w = 0; w < 32; ++w) {
+                o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
+                probe = fmaf(__uint_as_float(o[w]), 0.f, probe);
+              }
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
                 const float* z = reinterpret_cast<const float*>(o + 8 * w);
@@ -761,6 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t o[16];
               tmem_ld16_issue(tO + pass * (D / 2) + 16 * q, o);
               tmem_ld16_wait(o);
+#pragma unroll
+              for (int w = 0; w < 16; ++w) probe = fmaf(__uint_as_float(o[w]), 0.f, probe);
 #pragma unroll
               for (int w = 0; w < 4; ++w) y[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
             }
@@ -776,6 +782,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((there >> r) & 1) reinterpret_cast<uint4*>(dst)[pass * kChunks + ch] = y;
           }
           __syncwarp();
+        }
+        // A value that is not finite, of a key that other rows of the unit see and this
+        // one does not, has come in with its weight of zero. Such rows are computed
+        // again from what they see, in float32: each lane has D / 32 columns.
+        const int key0 = max(x.lo, x.tile0 * kTile), key1 = min(x.hi, (x.tile0 + x.n) * kTile);
+        uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
+#pragma unroll 1
+        while (again != 0) {
+          const int r = __ffs(again) - 1;
+          again &= again - 1;
+          constexpr int N = D / 32;
+          const char* q_row = p.q + t_out * p.q_token + head * p.q_head;
+          q_row = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q_row), r));
+          char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+          const int a = max(key0, __shfl_sync(0xffffffffu, lo, r)), z = min(key1, __shfl_sync(0xffffffffu, hi, r));
+          const float r_ref = __shfl_sync(0xffffffffu, ref, r), r_f = __shfl_sync(0xffffffffu, f, r);
+          float q[N], o[N];
+#pragma unroll
+          for (int d = 0; d < N; ++d) {
+            q[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q_row)[lane * N + d]);
+            o[d] = 0.f;
+          }
+#pragma unroll 1
+          for (int k = a; k < z; ++k) {
+            const int page = __ldcg(p.block_table + (int64_t)x.b * p.max_pages + (k >> p.pool.page_shift));
+            if (page < 0 || page >= p.pool.n_pages) break;  // (reported by the producer)
+            const int64_t off = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride +
+                                (int64_t)(k & ((1 << p.pool.page_shift) - 1)) * p.pool.token_stride;
+            const __nv_bfloat16* kk = reinterpret_cast<const __nv_bfloat16*>(p.pool.k + off) + lane * N;
+            const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.pool.v + off) + lane * N;
+            float score = 0.f;
+#pragma unroll
+            for (int d = 0; d < N; ++d) score = fmaf(q[d], __bfloat162float(kk[d]), score);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) score += __shfl_xor_sync(0xffffffffu, score, d);
+            const float w = ex2_approx(fmaf(score, c, -r_ref));
+#pragma unroll
+            for (int d = 0; d < N; ++d) o[d] = fmaf(w, __bfloat162float(vv[d]), o[d]);
+          }
+#pragma unroll
+          for (int d = 0; d < N; ++d) {
+            if (x.whole)
+              reinterpret_cast<__nv_bfloat16*>(dst)[lane * N + d] = __float2bfloat16_rn(o[d] * r_f);
+            else
+              reinterpret_cast<float*>(dst)[lane * N + d] = o[d];
+          }
         }
         if (valid) {
           if (!x.whole)

@@ -168,6 +168,41 @@ def test_attention_rising_scores(kv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,window", [(128, 4, 0), (64, 1, 0), (128, 2, 40), (64, 8, 20)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_attention_of_values_that_some_rows_do_not_see(kv, dtype, D, G, window, what):
+    """A later token's value, or one before a row's window, that is not finite: rows that do not see it are as
+    without it, rows that do are not finite in its columns."""
+    lens = [(9, 300), (70, 200), (40, 40), (20, 1400), (5, 130)]
+    x = Batch(dtype, D, 16, 2, G, lens, window=window, seed=31)
+    x.verify(kv)
+    clean = x.out.clone()
+    table, spots = x.table.cpu().numpy(), []
+    for b, (nq, n) in enumerate(lens):
+        spots.append((b, n - 1 - nq // 3))                       # a new token that the first rows do not see
+        if window:
+            spots.append((b, max(0, n - nq - window + 1) + 2))   # at the window's edge: the last rows do not see it
+    for b, j in spots:
+        x.v[0, int(table[b, j // 16]), j % 16, 1, 3] = what
+    assert x.call(kv) == 0 and int(x.status[0]) == 0
+    got, want = _host(x.out), _host(clean)
+    _, _, tol, _ = ref.attend(_host(x.q), np.nan_to_num(_host(x.k[0])), np.nan_to_num(_host(x.v[0]), posinf=0, neginf=0), table,
+                              x.kv_len.cpu().numpy(), x.q_start.cpu().numpy(), True, window, ref.default_scale(D), dtype == "bf16")
+    row = 0
+    for b, (nq, n) in enumerate(lens):
+        for i in range(nq):
+            p = n - nq + i
+            sees = [j for c, j in spots if c == b and j <= p and (not window or j > p - window)]
+            bad = np.zeros(got.shape[1:], dtype=bool)
+            if sees:
+                bad[G:, 3] = True                                # the second KV head's column 3
+            assert np.isfinite(got[row][~bad]).all(), (b, i)
+            assert not np.isfinite(got[row][bad]).any(), (b, i)
+            assert (np.abs(got[row] - want[row])[~bad] <= 2 * tol[row][~bad] + 1e-6).all(), (b, i)
+            row += 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_strided_rows_and_scale(kv, dtype):
     x = Batch(dtype, 128, 16, 2, 4, [(5, 90), (1, 300), (40, 41)], strided=True, seed=6)
     base = x.out._base if x.out._base is not None else x.out
