@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4* stage = reinterpret_cast<uint4*>(sRing + stage_at * L::kTileBytes) + (warp & 3) * 32 * kChunks;
         char* to = x.whole ? out : reinterpret_cast<char*>(part.out + prow * D);
         const uint32_t there = __ballot_sync(0xffffffffu, valid);
-        float probe = 0.f;  // NaN once a sum is not finite
+        uint64_t probe2 = 0;  // (two float32) NaN once a sum is not finite
 #pragma unroll 1
         for (int pass = 0; pass < (x.whole ? 1 : 2); ++pass) {
 #pragma unroll 1
@@ -752,9 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32_issue(tO + 32 * q, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int w = 0; w < 32; ++w) {
-                o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
-                probe = fmaf(__uint_as_float(o[w]), 0.f, probe);
+              for (int w = 0; w < 32; w += 2) {
+                const uint64_t z = fma2(pack2(__uint_as_float(o[w]), __uint_as_float(o[w + 1])), pack2(f, f), 0);
+                probe2 = fma2(z, 0, probe2);
+                const float2 y2 = unpack2(z);
+                o[w] = __float_as_uint(y2.x);
+                o[w + 1] = __float_as_uint(y2.y);
               }
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
@@ -766,7 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld16_issue(tO + pass * (D / 2) + 16 * q, o);
               tmem_ld16_wait(o);
 #pragma unroll
-              for (int w = 0; w < 16; ++w) probe = fmaf(__uint_as_float(o[w]), 0.f, probe);
+              for (int w = 0; w < 16; w += 2)
+                probe2 = fma2(pack2(__uint_as_float(o[w]), __uint_as_float(o[w + 1])), 0, probe2);
 #pragma unroll
               for (int w = 0; w < 4; ++w) y[w] = make_uint4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
             }
@@ -787,6 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one does not, has come in with its weight of zero. Such rows are computed
         // again from what they see, in float32: each lane has D / 32 columns.
         const int key0 = max(x.lo, x.tile0 * kTile), key1 = min(x.hi, (x.tile0 + x.n) * kTile);
+        const float2 probes = unpack2(probe2);
+        const float probe = probes.x + probes.y;
         uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
 #pragma unroll 1
         while (again != 0) {
