@@ -134,6 +134,16 @@ def test_attention_of_many_long_contexts(kv, D, S, Hk, G, lens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,n_q", [(128, 1, 1), (64, 3, 1), (128, 1, 4), (64, 5, 1), (128, 8, 1), (64, 2, 4), (128, 3, 3),
+                                     (64, 16, 1), (128, 17, 1)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 70)])
+def test_attention_of_few_rows(kv, dtype, D, G, n_q, causal, window):
+    """1 to 17 rows a KV head: each form of the kernels for few rows, whole units and cut ones, empty ones between."""
+    lens = [(1, 1), (n_q, 0), (n_q, 63), (0, 10), (n_q, 64), (max(1, n_q - 1), 65), (n_q, 900), (1, 3000), (n_q, n_q)]
+    Batch(dtype, D, 16, 2, G, lens, window=window, causal=causal, seed=D + G + n_q).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [1, 128, 129, 500])
 def test_attention_windows_on_long_contexts(kv, dtype, window):
     """Pages before the window hold NaN or have no entry."""
@@ -173,7 +183,16 @@ def test_attention_rising_scores(kv, dtype):
 def test_attention_of_values_that_some_rows_do_not_see(kv, dtype, D, G, window, what):
     """A later token's value, or one before a row's window, that is not finite: rows that do not see it are as
     without it, rows that do are not finite in its columns."""
-    lens = [(9, 300), (70, 200), (40, 40), (20, 1400), (5, 130)]
+    check_unseen_values(kv, dtype, D, G, window, what, [(9, 300), (70, 200), (40, 40), (20, 1400), (5, 130)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,n_q,window", [(128, 1, 4, 0), (64, 2, 4, 0), (128, 2, 3, 40), (64, 4, 4, 20)])
+def test_attention_of_values_that_some_of_few_rows_do_not_see(kv, dtype, D, G, n_q, window):
+    check_unseen_values(kv, dtype, D, G, window, float("nan"), [(n_q, 300), (3, 70), (n_q, 2100), (n_q, n_q)])
+
+
+def check_unseen_values(kv, dtype, D, G, window, what, lens):
     x = Batch(dtype, D, 16, 2, G, lens, window=window, seed=31)
     x.verify(kv)
     clean = x.out.clone()
