@@ -550,9 +550,10 @@ size_t compact_ws_bytes(int32_t n_pages) {
 
 // Whether one CTA plans: its barriers are cheaper than a cluster's (8 is the
 // portable size), its reads fewer at a time. Update of 16 requests and 1024 pages:
-// 11.0 us, by a cluster 12.3; of 128 and 4096: 17.2 and 12.3. Compaction of 1024
-// pages: 12.5 and 14.4 us; of 8192: 36.9 and 33.9.
-bool one_cta(int32_t B, int32_t n_pages) { return n_pages <= 1024 && B <= 64; }
+// 9.7 us, by a cluster 10.5; of 64 and 1024: 12.0 and 9.9; of 128 and 4096: 15.4 and
+// 10.6. Compaction of 512 pages: 10.0 and 10.4 us; of 2048: 14.4 and 14.2; of 8192:
+// 35.1 and 31.8.
+bool one_cta(int32_t B, int32_t n_pages) { return n_pages <= 1024 && B <= 16; }
 
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s) {
   const cudaError_t e = one_cta(p.B, p.pool.n_pages)
