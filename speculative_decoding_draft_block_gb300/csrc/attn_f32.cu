@@ -540,8 +540,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParam
   const cudaError_t e = launch_early(kernel, dim3(F::kShares), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.max_q * p.group;
-  return launch_early(attn_join_kernel<F, D, float>, dim3(F::kShares, (unsigned)(((most < kBM ? most : kBM) + 7) / 8)),
-                      dim3(256), 0, s, p, kBM, kBM);
+  return launch_join<F, D, float>(p, s, (int)(most < kBM ? most : kBM), kBM, kBM);
 }
 
 template <int D, int kR>

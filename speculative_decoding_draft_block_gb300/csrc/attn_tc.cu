@@ -905,8 +905,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   using F = Form<kPair>;
   const int rows = p.max_q <= per_tile ? p.max_q * p.group : F::kPartRows;
-  return launch_early(attn_join_kernel<F, D, __nv_bfloat16>, dim3(F::kShares, (rows + 7) / 8), dim3(256), 0, s, p, kTile,
-                      per_tile * p.group);
+  return launch_join<F, D, __nv_bfloat16>(p, s, rows, kTile, per_tile * p.group);
 }
 
 }  // namespace

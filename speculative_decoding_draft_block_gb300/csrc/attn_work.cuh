@@ -264,18 +264,51 @@ constexpr float kLn2 = 0.693147180559945f;
 
 // ---- join of the units that were cut -----------------------------------------------------
 //
-// Block (v, y): the unit that share v begins and does not finish, rows 8 y .. 8 y + 7
-// of its slot, a warp a row. Its parts are slot 1 of v and slot 0 of the shares after
+// Block (v, y): the unit that share v begins and does not finish, rows kRowsB y ..
+// kRowsB (y + 1) - 1 of its slot. Its parts are slot 1 of v and slot 0 of the shares after
 // it. A slot's rows come in tiles of `tile`, of which the first `used` stand for rows.
-template <class F, int D, typename T>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int tile, int used) {
+//
+// What bounds it is the chain of loads. With few parts (kAlone shares at most) a warp
+// adds up its row alone; with more (one long request: up to 304 parts a row) the parts
+// go round the warps, each with all of the block's rows, and the warps' sums are
+// added up in their order. One token over 100,000 cached, one KV head: 26.5 us, by
+// warps alone 68; prompt chunks of two row tiles (17 us of floor, up to 16 parts):
+// 64.8 us, by the round of the warps from 5 parts on 70.
+constexpr int kJoinThreads = 256;
+constexpr int kAlone = 16;
+
+// N floats of a row of partial results.
+template <int N>
+struct Floats {
+  float v[N];
+  __device__ __forceinline__ void load(const float* from, bool there) {
+    if (N == 4) {
+      const float4 w = there ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[0] = w.x;
+      v[1] = w.y;
+      v[N - 2] = w.z;
+      v[N - 1] = w.w;
+    } else {
+      const float2 w = there ? __ldcg(reinterpret_cast<const float2*>(from)) : make_float2(0.f, 0.f);
+      v[0] = w.x;
+      v[1] = w.y;
+    }
+  }
+};
+
+template <class F, int D, typename T, int kRowsB>
+__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnParams p, int tile, int used) {
+  constexpr int kWarps = kJoinThreads / 32, N = D / 32, kRounds = (F::kShares + 31) / 32;
+  static_assert((N == 2 || N == 4) && kRowsB <= kWarps && kAlone <= 32, "a warp a row, a lane a part");
+  __shared__ float factor[F::kShares][kRowsB];  // of a part in a row's sums, -1: no part
+  __shared__ __align__(16) float sums[kWarps][kRowsB][D];
   sm100::pdl_launch_dependents();
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;
-  const int lane = threadIdx.x & 31, prow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int prow0 = blockIdx.y * kRowsB, prow = prow0 + warp;  // (warp < kRowsB: its row)
   const int in_tile = prow % tile, row = prow / tile * used + in_tile;
-  auto at = [&](int k) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + prow; };
-  constexpr int N = D / 32;
+  auto at = [&](int k, int r) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + r; };
   sm100::pdl_wait();
   // The record, and, before it has arrived, the row's statistics in this share and
   // the 31 after it (looked at only if the record says that they have parts).
@@ -285,59 +318,123 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
   for (int i = 0; i < 5; ++i)
     reinterpret_cast<long long*>(&cu)[i] = __ldcg(reinterpret_cast<const long long*>(part.cut + share) + i);
   float2 ahead = make_float2(kNegInf, 0.f);
-  if (share + lane < F::kShares) ahead = __ldcg(part.stat + at(share + lane));
-  if (!cu.valid || in_tile >= used || row >= cu.rows) return;
-  float m = kNegInf, l = 0.f, o[N];
-#pragma unroll
-  for (int d = 0; d < N; ++d) o[d] = 0.f;
-  // shares 32 at a time: a lane finds what its share has of the unit
-  int before = 0;
-  for (int k0 = share; before < cu.n; k0 += 32) {
-    const int k = k0 + lane;
+  if (warp < kRowsB && share + lane < F::kShares) ahead = __ldcg(part.stat + at(share + lane, prow));
+  if (!cu.valid || prow0 % tile >= used || prow0 / tile * used + prow0 % tile >= cu.rows) return;
+  const bool here = warp < kRowsB && in_tile < used && row < cu.rows;
+
+  // which lane has a part (share `share` + 32 i + lane; with little work some shares
+  // have nothing and have written nothing), and whether there are more shares
+  auto has_part = [&](int i, bool& more) {
+    const int k = share + 32 * i + lane;
     const int a = k < F::kShares ? tiles_before(F::begin(cu.total, k), cu.first, cu.n) : cu.n;
     const int z = k < F::kShares ? tiles_before(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
-    before = __shfl_sync(0xffffffffu, z, 31);
-    float2 st = make_float2(kNegInf, 0.f);
-    // (with little work some shares have nothing and have written nothing)
-    if (a < z) st = k0 == share ? ahead : __ldcg(part.stat + at(k));
-    float top = st.x;
+    more = __shfl_sync(0xffffffffu, z, 31) < cu.n;
+    return a < z;
+  };
+  bool more;
+  const bool part0 = has_part(0, more);
+  const uint32_t parts0 = __ballot_sync(0xffffffffu, part0);
+  float m = part0 ? ahead.x : kNegInf, l = 0.f, x[N];  // reference, sum of weights, sums
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float m1 = fmaxf(m, top);
-    if (m1 != m) {
-      const float f = m == kNegInf ? 0.f : ex2_approx(m - m1);
-      l *= f;
+  for (int d = 0; d < N; ++d) x[d] = 0.f;
+  if (!more && parts0 >> kAlone == 0) {
+    if (!here) return;
 #pragma unroll
-      for (int d = 0; d < N; ++d) o[d] *= f;
-      m = m1;
-    }
-    const float f = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
-    const float w = st.y * f;
-    // (parts stand in consecutive shares, up to empty ones)
-    unsigned todo = __ballot_sync(0xffffffffu, a < z);
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float f = !part0 || ahead.x == kNegInf ? 0.f : ex2_approx(ahead.x - m);
+    if (part0) l = ahead.y * f;
+    constexpr int kBatch = 4;  // parts in flight
+    const float* from = part.out + lane * N;
 #pragma unroll 1
-    while (todo) {
-      constexpr int kBatch = 4;  // rows of partial results in flight
-      float y[kBatch][N], fq[kBatch];
+    for (int q0 = 0; parts0 >> q0 != 0; q0 += kBatch) {
+      Floats<N> y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) y[i].load(from + at(share + q0 + i, prow) * D, parts0 >> (q0 + i) & 1);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int q = todo ? __ffs(todo) - 1 : 0;
-        const bool there = todo != 0;
-        todo &= todo - 1;
-        fq[i] = __shfl_sync(0xffffffffu, f, q);
-        const float wq = __shfl_sync(0xffffffffu, w, q);
-        l += there ? wq : 0.f;
-        const float* from = part.out + at(k0 + q) * D + lane * N;
+        const float fq = __shfl_sync(0xffffffffu, f, q0 + i);
 #pragma unroll
-        for (int d = 0; d < N; ++d) y[i][d] = there ? __ldcg(from + d) : 0.f;
-        if (!there) fq[i] = 0.f;
+        for (int d = 0; d < N; ++d) x[d] = fmaf(y[i].v[d], fq, x[d]);
+      }
+    }
+  } else {
+    constexpr int kPass = kRowsB < 4 ? kRowsB : 4, kBatch = 8 / kPass;  // rows a pass, parts in flight
+    int n = 32 - __clz(parts0);         // shares from this one to the unit's last
+    {
+      float2 st[kRounds];
+      st[0] = ahead;
+      uint32_t mine = part0 && here ? 1u : 0u;  // rounds in which this lane's share has a part
+#pragma unroll
+      for (int i = 1; i < kRounds; ++i) {
+        if (!more) continue;
+        const bool has = has_part(i, more);
+        const uint32_t all = __ballot_sync(0xffffffffu, has);
+        if (all) n = 32 * i + 32 - __clz(all);
+        if (has && here) {
+          mine |= 1u << i;
+          st[i] = __ldcg(part.stat + at(share + 32 * i + lane, prow));
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
+      for (int i = 1; i < kRounds; ++i)
+        if (mine >> i & 1) m = fmaxf(m, st[i].x);
 #pragma unroll
-        for (int d = 0; d < N; ++d) o[d] = fmaf(y[i][d], fq[i], o[d]);
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int k = 32 * i + lane;
+        if (k >= n || warp >= kRowsB) continue;
+        float f = -1.f;
+        if (mine >> i & 1) {
+          f = st[i].x == kNegInf ? 0.f : ex2_approx(st[i].x - m);
+          l = fmaf(st[i].y, f, l);
+        }
+        factor[k][warp] = f;
+      }
     }
+    __syncthreads();
+#pragma unroll 1
+    for (int r0 = 0; r0 < kRowsB; r0 += kPass) {
+      float o[kPass][N];
+#pragma unroll
+      for (int r = 0; r < kPass; ++r)
+#pragma unroll
+        for (int d = 0; d < N; ++d) o[r][d] = 0.f;
+#pragma unroll 1
+      for (int j0 = warp; j0 < n; j0 += kWarps * kBatch) {
+        Floats<N> y[kBatch][kPass];
+        float f[kBatch][kPass];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int j = j0 + kWarps * i;
+          const float* from = part.out + at(share + j, prow0 + r0) * D + lane * N;
+#pragma unroll
+          for (int r = 0; r < kPass; ++r) {
+            f[i][r] = j < n ? factor[j][r0 + r] : -1.f;
+            y[i][r].load(from + r * D, !(f[i][r] < 0.f));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+          for (int r = 0; r < kPass; ++r)
+#pragma unroll
+            for (int d = 0; d < N; ++d) o[r][d] = fmaf(y[i][r].v[d], f[i][r], o[r][d]);
+      }
+#pragma unroll
+      for (int r = 0; r < kPass; ++r)
+#pragma unroll
+        for (int d = 0; d < N; ++d) sums[warp][r0 + r][lane * N + d] = o[r][d];
+    }
+    __syncthreads();
+    if (!here) return;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int d = 0; d < N; ++d) x[d] += sums[w][warp][lane * N + d];
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const bool some = l > 0.f || l != l;
   const float inv = some ? 1.f / l : 0.f;
   const int at_head = cu.off + row, tok = p.by_group.quotient(at_head);
@@ -347,12 +444,24 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
   if (sizeof(T) == 2) {
 #pragma unroll
     for (int d = 0; d < N / 2; ++d)
-      reinterpret_cast<uint32_t*>(to)[lane * (N / 2) + d] = to_bf16x2(o[2 * d] * inv, o[2 * d + 1] * inv);
+      reinterpret_cast<uint32_t*>(to)[lane * (N / 2) + d] = to_bf16x2(x[2 * d] * inv, x[2 * d + 1] * inv);
   } else {
 #pragma unroll
-    for (int d = 0; d < N; ++d) reinterpret_cast<float*>(to)[lane * N + d] = o[d] * inv;
+    for (int d = 0; d < N; ++d) reinterpret_cast<float*>(to)[lane * N + d] = x[d] * inv;
   }
   if (p.lse != nullptr && lane == 0) p.lse[t * p.n_heads + head] = some ? (m + log2f(l)) * kLn2 : kNegInf;
+}
+
+// Launch of the join for units of at most `rows` rows of a slot. With few rows two a
+// block, so that the parts in flight are more: 10 rows of float32 12.7 us, with eight
+// a block 15.9; with many rows blocks of two are too many.
+template <class F, int D, typename T>
+cudaError_t launch_join(const AttnParams& p, cudaStream_t s, int rows, int tile, int used) {
+  if (rows <= 16)
+    return launch_early(attn_join_kernel<F, D, T, 2>, dim3(F::kShares, (rows + 1) / 2), dim3(kJoinThreads), 0, s, p, tile,
+                        used);
+  return launch_early(attn_join_kernel<F, D, T, 8>, dim3(F::kShares, (rows + 7) / 8), dim3(kJoinThreads), 0, s, p, tile,
+                      used);
 }
 
 }  // namespace
