@@ -19,7 +19,9 @@
 namespace ds {
 namespace {
 
-constexpr int kUnitCost = 1;  // set-up of a unit, in key tiles
+// Set-up of a unit, in key tiles (0, 2 and 3 are slower where units of a few tiles stand
+// beside longer ones).
+constexpr int kUnitCost = 1;
 
 template <int kTileKeys, int kShareCount, int kPartialRows>
 struct WorkForm {
