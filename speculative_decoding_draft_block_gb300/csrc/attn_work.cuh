@@ -313,14 +313,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
   auto at = [&](int k, int r) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + r; };
   sm100::pdl_wait();
   // The record, and, before it has arrived, the row's statistics in this share and
-  // the 31 after it (looked at only if the record says that they have parts).
+  // the ones after it (looked at only if the record says that they have parts): with
+  // few rows the next 31, with many, which have few parts as a rule, the next 3,
+  // since each statistic is a sector of its own.
+  constexpr int kAhead = kRowsB <= 2 ? 32 : 4;
   CutUnit cu;
   static_assert(sizeof(CutUnit) == 40, "five 8-byte words");
 #pragma unroll
   for (int i = 0; i < 5; ++i)
     reinterpret_cast<long long*>(&cu)[i] = __ldcg(reinterpret_cast<const long long*>(part.cut + share) + i);
   float2 ahead = make_float2(kNegInf, 0.f);
-  if (warp < kRowsB && share + lane < F::kShares) ahead = __ldcg(part.stat + at(share + lane, prow));
+  if (warp < kRowsB && lane < kAhead && share + lane < F::kShares) ahead = __ldcg(part.stat + at(share + lane, prow));
   if (!cu.valid || prow0 % tile >= used || prow0 / tile * used + prow0 % tile >= cu.rows) return;
   const bool here = warp < kRowsB && in_tile < used && row < cu.rows;
 
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
   bool more;
   const bool part0 = has_part(0, more);
   const uint32_t parts0 = __ballot_sync(0xffffffffu, part0);
+  if (part0 && here && lane >= kAhead) ahead = __ldcg(part.stat + at(share + lane, prow));
   float m = part0 ? ahead.x : kNegInf, l = 0.f, x[N];  // reference, sum of weights, sums
 #pragma unroll
   for (int d = 0; d < N; ++d) x[d] = 0.f;
@@ -444,9 +448,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
   const int64_t t = cu.token + tok;
   char* to = p.out + t * p.o_token + head * p.o_head;
   if (sizeof(T) == 2) {
+    uint32_t y[N / 2];
 #pragma unroll
-    for (int d = 0; d < N / 2; ++d)
-      reinterpret_cast<uint32_t*>(to)[lane * (N / 2) + d] = to_bf16x2(x[2 * d] * inv, x[2 * d + 1] * inv);
+    for (int d = 0; d < N / 2; ++d) y[d] = to_bf16x2(x[2 * d] * inv, x[2 * d + 1] * inv);
+    if (N == 4)
+      reinterpret_cast<uint2*>(to)[lane] = make_uint2(y[0], y[N / 2 - 1]);
+    else
+      reinterpret_cast<uint32_t*>(to)[lane] = y[0];
   } else {
 #pragma unroll
     for (int d = 0; d < N; ++d) reinterpret_cast<float*>(to)[lane * N + d] = x[d] * inv;
