@@ -22,7 +22,7 @@
 //   solo (requests of one row tile on average): each stream has a share of its
 //        own, 2 x 152 in all, and a unit is one row tile. Bound by the keys' way
 //        from memory; the tensor work of the mostly empty rows stays below it.
-//        128 requests of one token, 500 to 6000 cached (1.24 GB): 192 to 199 us,
+//        128 requests of one token, 300 to 8000 cached (1.24 GB): 192 to 199 us,
 //        6.2 to 6.5 TB/s. Short contexts are bound by the chain of a unit (page
 //        entry, Q, K, product, softmax, product, result: 7 us).
 //   pair (longer requests): a CTA has one share, a unit is two row tiles, one a

@@ -274,8 +274,8 @@ constexpr float kLn2 = 0.693147180559945f;
 // adds up its row alone; with more (one long request: up to 304 parts a row) the parts
 // go round the warps, each with all of the block's rows, and the warps' sums are
 // added up in their order. One token over 100,000 cached, one KV head: 26.5 us, by
-// warps alone 68; prompt chunks of two row tiles (17 us of floor, up to 16 parts):
-// 64.8 us, by the round of the warps from 5 parts on 70.
+// warps alone 68; prompt chunks of two row tiles of 7 requests (up to 16 parts) 61 us,
+// with the round of the warps from 5 parts on 5 us more.
 constexpr int kJoinThreads = 256;
 constexpr int kAlone = 16;
 
