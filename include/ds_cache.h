@@ -7,9 +7,8 @@
  *   [DSpark]  배경: the target scores K drafted tokens and the next one in a
  *             single pass over a cached context, then the sequence falls back
  *             to the accepted prefix.
- *   [DFlash]  DFlashProposer 초기화 (1 + K query tokens per request and cycle)
- *             and the draft backbone's non-causal attention of a block over
- *             the injected context.
+ *   [DFlash]  1 + K query tokens per request and cycle, and the draft backbone's
+ *             non-causal attention of a block over the injected context.
  *   [vLLM-V4] pages of up to 256 tokens, sliding windows.
  *
  * The conventions of ds_draft.h hold: the caller owns every buffer, calls

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
         const int key = (x.tile0 + j) * kKeyTile + tid;
         int64_t at = -1;
         if (key >= x.lo && key < x.hi) {
-          int page = __ldg(table + (key >> shift));
+          int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) {
             report(p.status, kErrBounds);
             page = 0;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
         const float ref = m[i] == kNegInf ? 0.f : m[i];
 #pragma unroll 1
         for (int key = max(key0, lo[i]); key < min(key1, hi[i]); ++key) {
-          const int page = __ldg(table + (key >> shift));
+          const int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) break;  // (reported above)
           const int64_t at = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride + (int64_t)(key & mask) * p.pool.token_stride;
           const float* kk = reinterpret_cast<const float*>(p.pool.k + at);

@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
   static_assert((N == 2 || N == 4) && kRowsB <= kWarps && kAlone <= 32, "a warp a row, a lane a part");
   __shared__ float factor[F::kShares][kRowsB];  // of a part in a row's sums, -1: no part
   __shared__ __align__(16) float sums[kWarps][kRowsB][D];
-  sm100::pdl_launch_dependents();
   const Partials part = partials<D>(p.workspace);
   const int share = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

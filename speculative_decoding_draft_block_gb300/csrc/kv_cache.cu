@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int tid = threadIdx.x;
   if (tid < kAppendTokens) ends[tid] = 0;
   int before = 0;
-  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
   __syncthreads();
   for (int i = tid; i < p.B; i += kAppendThreads) {
-    const int e = __ldg(p.q_start + i + 1);
+    const int e = __ldcg(p.q_start + i + 1);
     if (e <= t0)
       ++before;
     else if (e < t0 + kAppendTokens)
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (!r.ok) {
         report(p.status, kErrBounds);
       } else if (t >= r.q0 && pos >= 0) {
-        const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + (pos >> p.pool.page_shift));
+        const int page = __ldcg(p.block_table + (int64_t)b * p.max_pages + (pos >> p.pool.page_shift));
         if (page < 0 || page >= p.pool.n_pages)
           report(p.status, kErrBounds);
         else
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const int64_t off = at[i];
     if (off < 0) continue;
     const int64_t t = t0 + i;
-    const uint4 kk = __ldg(reinterpret_cast<const uint4*>(p.k_new + t * p.k_token + h * p.k_head) + c);
-    const uint4 vv = __ldg(reinterpret_cast<const uint4*>(p.v_new + t * p.v_token + h * p.v_head) + c);
+    const uint4 kk = __ldcg(reinterpret_cast<const uint4*>(p.k_new + t * p.k_token + h * p.k_head) + c);
+    const uint4 vv = __ldcg(reinterpret_cast<const uint4*>(p.v_new + t * p.v_token + h * p.v_head) + c);
     const int64_t o = off + h * p.pool.head_stride;
     reinterpret_cast<uint4*>(p.pool.k + o)[c] = kk;
     reinterpret_cast<uint4*>(p.pool.v + o)[c] = vv;

@@ -110,7 +110,11 @@ __device__ __forceinline__ Request load_request(const int32_t* q_start, const in
 
 // A launch that is set up while the kernel before it on the stream finishes; the
 // kernel waits for that one (griddepcontrol.wait) before it touches any memory
-// that another kernel may write.
+// that another kernel may write, and only then lets its successor start: what stands
+// before it on the stream is then complete. Kernels that read their inputs
+// before they wait (the draft's logits and states, the confidence head's) may follow.
+// So the last kernel of the attention, whose output may be such an input, lets them
+// start at its end only. What earlier kernels wrote is read past the first-level cache.
 template <class... A, class... B>
 cudaError_t launch_early(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const B&... args) {
   cudaLaunchAttribute at[1];

@@ -143,12 +143,12 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) {
 __device__ __forceinline__ Move load_move(const UpdateParams& p, int b) {
   const int64_t cap = (int64_t)p.max_pages << p.pool.page_shift;
   Move m;
-  m.parent = p.parent != nullptr ? __ldg(p.parent + b) : b;
-  const int now = __ldg(p.kv_len + b), next = __ldg(p.new_len + b);
+  m.parent = p.parent != nullptr ? __ldcg(p.parent + b) : b;
+  const int now = __ldcg(p.kv_len + b), next = __ldcg(p.new_len + b);
   m.ok = m.parent >= -1 && m.parent < p.B && now >= 0 && now <= cap && next >= 0 && next <= cap;
   m.keep = 0;
   if (m.ok && m.parent >= 0) {
-    const int from = m.parent == b ? now : __ldg(p.kv_len + m.parent);
+    const int from = m.parent == b ? now : __ldcg(p.kv_len + m.parent);
     m.ok = from >= 0 && from <= cap;
     m.keep = min(from, next);
   }
@@ -157,7 +157,7 @@ __device__ __forceinline__ Move load_move(const UpdateParams& p, int b) {
   m.old = m.ok ? pages_of(now, p.pool.page_shift) : 0;
   m.page = -1;
   if (m.ok && (m.keep & ((1 << p.pool.page_shift) - 1)) != 0 && next > m.keep) {
-    m.page = __ldg(p.table + (int64_t)m.parent * p.max_pages + m.kept - 1);
+    m.page = __ldcg(p.table + (int64_t)m.parent * p.max_pages + m.kept - 1);
     if (m.page < 0 || m.page >= p.pool.n_pages) m.ok = false;
   }
   return m;
@@ -173,18 +173,13 @@ struct PlanShared {
   Move move[kPlanThreads];
 };
 
-// Four pages' words at once (the arrays are 16-byte aligned, i a multiple of 4):
-// of an input, or past the first-level cache of what this kernel writes.
-template <bool kInput>
+// Four pages' words at once (the arrays are 16-byte aligned, i a multiple of 4).
 __device__ __forceinline__ int4 load_four(const int32_t* from, int i, int end, int none) {
-  if (i + 4 <= end) {
-    const int4* f = reinterpret_cast<const int4*>(from + i);
-    return kInput ? __ldg(f) : __ldcg(f);
-  }
+  if (i + 4 <= end) return __ldcg(reinterpret_cast<const int4*>(from + i));
   int4 v = make_int4(none, none, none, none);
-  if (i < end) v.x = kInput ? __ldg(from + i) : __ldcg(from + i);
-  if (i + 1 < end) v.y = kInput ? __ldg(from + i + 1) : __ldcg(from + i + 1);
-  if (i + 2 < end) v.z = kInput ? __ldg(from + i + 2) : __ldcg(from + i + 2);
+  if (i < end) v.x = __ldcg(from + i);
+  if (i + 1 < end) v.y = __ldcg(from + i + 1);
+  if (i + 2 < end) v.z = __ldcg(from + i + 2);
   return v;
 }
 __device__ __forceinline__ void store_four(int32_t* to, int i, int end, int4 v) {
@@ -206,8 +201,8 @@ template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     update_plan_kernel(const UpdateParams p) {
   cg::cluster_group cl = cg::this_cluster();
-  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
   __shared__ PlanShared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int rank = (int)cl.block_rank();
@@ -231,7 +226,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
   }
   for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
-    const int4 r = load_four<true>(p.ref, i, p1, 0);
+    const int4 r = load_four(p.ref, i, p1, 0);
     bad |= (r.x | r.y | r.z | r.w) < 0;
     store_four(w.count, i, p1, r);
   }
@@ -251,8 +246,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int j = j0 + 32 * i;
-        o[i] = j < m.old ? __ldg(now + j) : -1;
-        h[i] = j < m.kept ? __ldg(past + j) : -1;
+        o[i] = j < m.old ? __ldcg(now + j) : -1;
+        h[i] = j < m.kept ? __ldcg(past + j) : -1;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -288,7 +283,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
   int4 counts = make_int4(1, 1, 1, 1);  // of this thread's first four pages
   for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
-    const int4 c = load_four<false>(w.count, i, p1, 1);
+    const int4 c = load_four(w.count, i, p1, 1);
     if (i == p0 + 4 * tid) counts = c;
     bad |= (c.x | c.y | c.z | c.w) < 0;
     free += (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0);
@@ -323,7 +318,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   at = before.b;
   for (int base = p0; base < p1; base += 4 * kPlanThreads) {
     const int i = base + 4 * tid;
-    const int4 c = base == p0 ? counts : load_four<false>(w.count, i, p1, 1);
+    const int4 c = base == p0 ? counts : load_four(w.count, i, p1, 1);
     int total;
     int r = at + block_exclusive((c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0), sh.sums, total);
     auto give = [&](int count, int page) {
@@ -338,7 +333,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     out.y = give(c.y, i + 1);
     out.z = give(c.z, i + 2);
     out.w = give(c.w, i + 3);
-    store_four(p.ref_out, i, p1, fail ? load_four<true>(p.ref, i, p1, 0) : out);
+    store_four(p.ref_out, i, p1, fail ? load_four(p.ref, i, p1, 0) : out);
     at += total;
   }
   cl.sync();  // no CTA leaves while another may read its shared memory
@@ -393,8 +388,8 @@ __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int s
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
   const int b = blockIdx.x, part = blockIdx.y;  // part: 2 * layer + (0: K, 1: V)
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
-  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
   const int fail = __ldcg(w.fail);
   const int2 copy = __ldcg(w.copy + b);
   const int4 row = __ldcg(w.row + b);
@@ -402,8 +397,8 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
   if (fail) {
     if (part == 0) {
       for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
-        p.table_out[(int64_t)b * p.max_pages + j] = __ldg(p.table + (int64_t)b * p.max_pages + j);
-      if (threadIdx.x == 0) p.len_out[b] = __ldg(p.kv_len + b);
+        p.table_out[(int64_t)b * p.max_pages + j] = __ldcg(p.table + (int64_t)b * p.max_pages + j);
+      if (threadIdx.x == 0) p.len_out[b] = __ldcg(p.kv_len + b);
     }
     return;
   }
@@ -412,9 +407,9 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
     const int32_t* past = p.table + (int64_t)max(parent, 0) * p.max_pages;
     for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
       p.table_out[(int64_t)b * p.max_pages + j] =
-          j < shared ? __ldg(past + j) : j < want ? __ldcg(w.free_list + start + j - shared) : -1;
+          j < shared ? __ldcg(past + j) : j < want ? __ldcg(w.free_list + start + j - shared) : -1;
     if (threadIdx.x == 0) {
-      p.len_out[b] = __ldg(p.new_len + b);
+      p.len_out[b] = __ldcg(p.new_len + b);
       if (copy.x >= 0) atomicSub(p.ref_out + copy.x, 1);
     }
     if (copy.x < 0) return;
@@ -444,8 +439,8 @@ template <int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     compact_plan_kernel(const CompactParams p) {
   cg::cluster_group cl = cg::this_cluster();
-  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
   __shared__ int sums[kPlanWarps];
   __shared__ Exchange exchange[2];
   const int tid = threadIdx.x, rank = (int)cl.block_rank();
@@ -455,7 +450,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   share<kCluster>(N, rank, p0, p1);
   int held = 0, bad = 0;
   for (int i = p0 + 4 * tid; i < p1; i += 4 * kPlanThreads) {
-    const int4 r = load_four<true>(p.ref, i, p1, 0);
+    const int4 r = load_four(p.ref, i, p1, 0);
     bad |= (r.x | r.y | r.z | r.w) < 0;
     held += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
@@ -466,7 +461,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   const bool fail = all.c > 0;
   int below = 0;  // held pages below `used`
   for (int i = p0 + 4 * tid; i < min(p1, used); i += 4 * kPlanThreads) {
-    const int4 r = load_four<true>(p.ref, i, min(p1, used), 0);
+    const int4 r = load_four(p.ref, i, min(p1, used), 0);
     below += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
   const int held_below = cluster_exchange<kCluster>(cl, &exchange[1], Counts{0, block_sum(below, sums), 0}, none).b;
@@ -474,7 +469,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   int at = before.b;
   for (int base = p0; base < p1; base += 4 * kPlanThreads) {
     const int i = base + 4 * tid;
-    const int4 r = load_four<true>(p.ref, i, p1, 0);
+    const int4 r = load_four(p.ref, i, p1, 0);
     int total;
     // held pages before the next page
     int held_before = at + block_exclusive((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), sums, total);
@@ -501,7 +496,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   for (int i = rank * kPlanThreads + tid; i < n; i += kCluster * kPlanThreads) {
     const int s = __ldcg(w.src + i), d = __ldcg(w.dst + i);
     p.page_map[s] = d;
-    p.ref_out[d] = __ldg(p.ref + s);
+    p.ref_out[d] = __ldcg(p.ref + s);
   }
   if (rank == 0 && tid == 0) {
     w.moves[0] = n;
@@ -520,16 +515,16 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams 
   const int parts = 2 * p.pool.n_layers, tokens = 1 << p.pool.page_shift;
   const int64_t entries = (int64_t)p.B * p.max_pages;
   int64_t x = blockIdx.x, e = (int64_t)(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
-  sm100::pdl_launch_dependents();
   sm100::pdl_wait();
-  int page = e < entries ? __ldg(p.table + e) : -1;
+  sm100::pdl_launch_dependents();
+  int page = e < entries ? __ldcg(p.table + e) : -1;
   const int2 moves = __ldcg(reinterpret_cast<const int2*>(w.moves));
   const int n = moves.x;
   const bool fail = moves.y != 0;
   for (; e < entries; e += (int64_t)gridDim.x * blockDim.x) {
     const int64_t next = e + (int64_t)gridDim.x * blockDim.x;
     const int now = page;
-    if (next < entries) page = __ldg(p.table + next);
+    if (next < entries) page = __ldcg(p.table + next);
     p.table_out[e] = fail ? now : now >= 0 && now < p.pool.n_pages ? __ldcg(p.page_map + now) : -1;
   }
   for (; x < (int64_t)n * parts; x += gridDim.x) {

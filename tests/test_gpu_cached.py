@@ -80,3 +80,44 @@ def test_greedy_cycles_are_the_models_own_decoding(cached):
 def test_the_command(cached, capsys):
     cached.main(["--requests", "3", "--cycles", "6", "--temperature", "1.0"])
     assert "6 cycles of 3 requests" in capsys.readouterr().out
+
+
+def test_attention_writes_the_cycles_states(cached):
+    """The attention's output is the draft's hidden states as they stand (heads * head_dim = d): the confidence kernel,
+    which reads the states before it waits for the draft, sees all of them."""
+    from speculative_decoding_draft_block_gb300.cycle import DeviceCycle
+    from speculative_decoding_draft_block_gb300.kv_cache import PagedCache
+    from speculative_decoding_draft_block_gb300.workloads import B256, make_inputs, scaled
+    B, K, H, D, n = 8, 8, 16, 128, 2000
+    cyc = DeviceCycle(make_inputs(scaled(B256, name="states", B=B, K=K, V=2048, r=64, d=H * D, temps=(1.0,), seed=5)))
+    cyc.reset_status()
+    cyc.draft(1)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    cache = PagedCache(1, B * (n // 16) + 8, 16, 4, D, B, n, dtype=torch.bfloat16)
+    cache.update(torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    rows = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((B * n, 4, D), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    cache.append(0, k, v, rows * n)
+    start = rows * K
+    out = cyc.t["h"].view(B * K, H, D)
+    q = torch.zeros((B * K, H, D), device="cuda", dtype=torch.bfloat16)
+
+    def states_and_lengths():
+        out.fill_(0)
+        cache.attend(0, q, start, K, out=out, causal=False)
+        cyc.schedule()
+
+    states_and_lengths()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        states_and_lengths()
+    for i in range(12):
+        q.copy_(torch.randn((B * K, H, D), device="cuda", generator=g) * 3)
+        graph.replay() if i % 2 else states_and_lengths()
+        first = cyc.conf_logit.clone()
+        torch.cuda.synchronize()
+        cyc.schedule()
+        assert torch.equal(first, cyc.conf_logit), i
+    cyc.check_status()
+    cache.check_status()
