@@ -546,3 +546,47 @@ def test_cycles_of_a_paged_cache(kv, dtype):
             assert int(c.n_used[0]) == int((c.ref > 0).sum())
             assert (c.ref[:int(c.n_used[0])] > 0).all()
     c.check_status()
+
+
+@pytest.mark.parametrize("dtype,outside", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_places_past_32_bits(kv, dtype, outside):
+    """Pages more than 2^32 bytes (and 2^31 elements) into a layer: written, read, copied on write and moved."""
+    N, S, Hk, D, G = 140000, 16, 8, 128, 2
+    g = torch.Generator(device="cuda").manual_seed(12)
+    c = kv.PagedCache(1, N, S, Hk, D, 3, 400, dtype=DT[dtype], heads_outside=outside)
+    c.ref[:N - 60] = 1                    # somebody else's: new pages are the last ones
+    lens = [70, 300, 0]
+    c.update(_i32(lens))
+    assert int(c.block_table[0, 0]) == N - 60
+    T = sum(lens)
+    kn, vn = (torch.randn((T, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    c.append(0, kn, vn, _i32([0, 70, 370, 370]))
+    k = [kn[:70], kn[70:], kn[:70]]
+    v = [vn[:70], vn[70:], vn[:70]]
+
+    def check(n, pages):
+        q = torch.randn((2 * sum(n), Hk * G, D), device="cuda", generator=g).to(DT[dtype])[::2]
+        start = _i32([0, n[0], n[0] + n[1], sum(n)])
+        out = c.attend(0, q, start, max(n), out=torch.empty((sum(n), Hk * G, D), dtype=DT[dtype], device="cuda"))
+        c.check_status()
+        held = [x.shape[0] for x in k]
+        kp, vp = (np.zeros((3, max(held), Hk, D)) for _ in range(2))
+        for b in range(3):
+            kp[b, :held[b]], vp[b, :held[b]] = _host(k[b]), _host(v[b])
+        assert c.kv_len.tolist() == held
+        want, _, tol, _ = ref.attend(_host(q), kp, vp, np.arange(3)[:, None], held, start.cpu().numpy(), True, 0,
+                                     ref.default_scale(D), dtype == "bf16")
+        assert (np.abs(_host(out) - want) <= tol).all()
+        table = c.block_table[c.block_table >= 0]
+        assert pages(int(table.min()), int(table.max()))
+
+    c.update(_i32([70, 300, 70]), parent=_i32([0, 1, 0]))
+    check([3, 9, 40], lambda lo, hi: lo >= N - 60)
+    c.update(_i32([75, 300, 73]))         # both write into the shared last page: one copy
+    new = [torch.randn((8, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2)]
+    c.append(0, new[0], new[1], _i32([0, 5, 5, 8]))
+    k, v = ([torch.cat([a[0], x[:5]]), a[1], torch.cat([a[2], x[5:]])] for a, x in ((k, new[0]), (v, new[1])))
+    check([1, 1, 1], lambda lo, hi: lo >= N - 60)
+    c.ref[:N - 60] = 0
+    c.compact()
+    check([20, 1, 7], lambda lo, hi: hi < 60)
