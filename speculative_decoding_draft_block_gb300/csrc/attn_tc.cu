@@ -18,13 +18,19 @@
 //
 // A CTA works with two streams, each with its own score tile, output
 // accumulator and softmax warpgroup: while the scores of one go through the
-// softmax, the tensor core works on the other's. Two forms, chosen on the host:
+// softmax, the tensor core works on the other's. Three forms, chosen on the host:
 //   solo (requests of one row tile on average): each stream has a share of its
 //        own, 2 x 152 in all, and a unit is one row tile. Bound by the keys' way
 //        from memory; the tensor work of the mostly empty rows stays below it.
-//        128 requests of one token, 300 to 8000 cached (1.24 GB): 192 to 199 us,
-//        6.2 to 6.5 TB/s. Short contexts are bound by the chain of a unit (page
-//        entry, Q, K, product, softmax, product, result: 7 us).
+//        128 verify blocks of up to 17 tokens, 500 to 6000 cached (1.18 GB): 198 us,
+//        5.9 TB/s. Short contexts are bound by the chain of a unit (page entry, Q, K,
+//        product, softmax, product, result).
+//   few (up to 16 rows a unit: single tokens, short blocks): as solo, but a row
+//        stands in the lanes of all four softmax warps (Q is loaded four times), and
+//        each of them takes a quarter of a tile's keys, with a reference of its own,
+//        and zeros as the other quarters' weights. A lane has 32 scores to work on
+//        instead of 128, which shortens the chain of a tile; a piece's quarters
+//        are put together at its end, through shared memory.
 //   pair (longer requests): a CTA has one share, a unit is two row tiles, one a
 //        stream, and both read each key tile from shared memory. Bound by the
 //        tensor core and, between its products, by the softmax that feeds it. Units
@@ -67,11 +73,12 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kTile = 128;         // keys a tile, rows a tile
+constexpr int kFewRows = 16;       // rows of a unit in the form for few rows
 constexpr float kSlack = 8.f;      // growth of the exponents that is left in the sums
 constexpr uint32_t kCtrlRegs = 88, kSoftRegs = 208, kLaunchRegs = 168;
 static_assert(128 * kCtrlRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr uint32_t kWaitPolls = 1u << 16;
-constexpr uint32_t kHeader = 2048;  // barriers and small records, before the tiles
+constexpr uint32_t kHeader = 3072;  // barriers and small records, before the tiles
 constexpr int kAhead = 4;           // pieces handed out ahead, per stream
 constexpr int kMaxSlots = 12;
 
@@ -103,6 +110,8 @@ struct Header {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t drain[2];
+  uint64_t merged[2];                   // (few rows) a piece's quarters stand in its staging slot
+  float2 quarter[2][4][kFewRows];       // their references and sums
   uint32_t info[kMaxSlots];
   uint32_t entry[kMaxSlots];  // 1 + the number of the entry that the slot was last given to
   uint32_t staged[2];         // softmax warps that are done with a piece's staging slot
@@ -138,9 +147,12 @@ struct RingPos {
   }
 };
 
+enum : int { kSolo, kPairs, kFew };  // forms
+
 // Key tiles, shares of the work list and rows of partial results of a form.
-template <bool kPair>
-struct Form : WorkForm<kTile, kPair ? kMaxAttnCtas : 2 * kMaxAttnCtas, kPair ? 2 * kTile : kTile> {};
+template <int kForm>
+struct Form : WorkForm<kTile, kForm == kPairs ? kMaxAttnCtas : 2 * kMaxAttnCtas,
+                       kForm == kPairs ? 2 * kTile : kForm == kFew ? kFewRows : kTile> {};
 
 // Bounded waits. One that gives up sets the abort flag, which ends every role's
 // loop; the status is reported once, at the kernel's end (the waits are many and
@@ -208,12 +220,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // ---- the kernel --------------------------------------------------------------------------
 
-template <int D, bool kPair>
+template <int D, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV) {
   using L = Layout<D>;
-  using F = Form<kPair>;
+  using F = Form<kForm>;
+  constexpr bool kPair = kForm == kPairs;
   constexpr int kSlots = L::kSlots;
   constexpr int kHalves = D / 64;
   constexpr int kLists = kPair ? 1 : 2;  // shares of a CTA
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem + L::kOffQ;
   uint8_t* sRing = smem + L::kOffRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_tile = p.by_group.quotient(kTile);  // tokens of a row tile
+  const int per_tile = p.by_group.quotient(kForm == kFew ? kFewRows : kTile);  // tokens of a row tile
   const int tile_rows = per_tile * p.group;      // rows in use of a row tile
   const int unit_rows = (kPair ? 2 : 1) * tile_rows;
 
@@ -236,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.drain[i], 1);
+      mbar_init(&sh.merged[i], 4);
       sh.ended[i] = -1;
       sh.staged[i] = 0;
       for (int k = 0; k < kAhead; ++k) {
@@ -340,10 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (s == 0) q_par[0] ^= 1;
               if (s == 1) q_par[1] ^= 1;
               if (elect_one()) {
-                mbar_expect_tx(&sh.q_full[s], (uint32_t)tile_rows * D * 2);
+                constexpr int kCopies = kForm == kFew ? 4 : 1;  // (few rows: a copy for each softmax warp)
+                mbar_expect_tx(&sh.q_full[s], (uint32_t)tile_rows * D * 2 * kCopies);
                 for (int y = 0; y < kHalves; ++y)
-                  tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128), &tmQ, &sh.q_full[s], y * 64,
-                                    x.h * p.group, x.token + (kPair ? s * per_tile : 0));
+                  for (int i = 0; i < kCopies; ++i)
+                    tma_load_3d_plain(sQ + s * L::kTileBytes + y * (kTile * 128) + i * (32 * 128), &tmQ, &sh.q_full[s],
+                                      y * 64, x.h * p.group, x.token + (kPair ? s * per_tile : 0));
               }
               __syncwarp();
             }
@@ -597,8 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ softmax, epilogue
     setmaxnreg_inc<kSoftRegs>();
     const int s = (warp >> 2) - 1;                 // stream
-    const int row = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int quarter = warp & 3;                  // its TMEM lanes
+    const int row = kForm == kFew ? lane : quarter * 32 + lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lanes + s * kTile, tO = tmem + lanes + 256 + s * D;
     const float c = p.scale * kLog2eHi;
     const int tile_tok = p.by_group.quotient(row), g = row - tile_tok * p.group;
@@ -623,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       char* out = p.out + t_out * p.o_token + head * p.o_head;
       float* lse = p.lse != nullptr ? p.lse + t_out * p.n_heads + head : nullptr;
       if (x.n == 0) {
-        if (valid) {
+        if (valid && (kForm != kFew || quarter == 0)) {
 #pragma unroll 1
           for (int d = 0; d < D / 8; ++d) reinterpret_cast<uint4*>(out)[d] = make_uint4(0, 0, 0, 0);
           if (lse != nullptr) *lse = kNegInf;
@@ -636,12 +653,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool work = __any_sync(0xffffffffu, valid);
       float m = kNegInf, l = 0.f;  // reference (a score, before the factor c) and sum
       bool ok = true;
+      // the reference, with `top` the largest score of tile `it`
+      auto raise_to = [&](float top, int it) {
+        top = fmaxf(m, top);
+        if (it == 0) {
+          m = top;
+          return;
+        }
+        const bool raise = valid && (top - m) * c > kSlack;
+        if (!__any_sync(0xffffffffu, raise)) return;
+        // the accumulator is at rest: the product with the last tile's weights was
+        // issued before these scores, the next one waits for our weights
+        const float f = raise ? ex2_approx((m - top) * c) : 1.f;
+        if (raise) m = top;
+        l *= f;
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t o[16];
+          tmem_ld16_issue(tO + 16 * q, o);
+          tmem_ld16_wait(o);
+#pragma unroll
+          for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
+          tmem_st16(tO + 16 * q, o);
+        }
+      };
       for (int it = 0; it < x.n; ++it) {
         const int key = (x.tile0 + it) * kTile;
         ok = wait_bar(&sh.s_full[s], ns & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (work) {
+        if constexpr (kForm == kFew) {
+          // this warp's keys of the tile: 32 quarter .. + 31
+          const int key0 = key + 32 * quarter;
+          uint32_t y[32];
+          tmem_ld32_issue(tS + 32 * quarter, y);
+          tmem_ld_wait(y);
+          if (__any_sync(0xffffffffu, key0 + 32 > hi || key0 < lo)) {
+            const int a = lo - key0;
+            const uint32_t seen = (uint32_t)max(0, hi - key0 - a);
+#pragma unroll
+            for (int w = 0; w < 32; ++w)
+              if ((uint32_t)(w - a) >= seen) y[w] = __float_as_uint(kNegInf);
+          }
+          float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+          for (int w = 0; w < 32; ++w) mx[w & 3] = fmaxf(mx[w & 3], __uint_as_float(y[w]));
+          raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
+          const float r = m == kNegInf ? 0.f : m * c;
+          const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
+          uint64_t sum2[2] = {0, 0};
+          uint32_t pk[16], none[16];
+#pragma unroll
+          for (int w = 0; w < 16; ++w) {
+            const uint64_t e = fma2(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
+            float2 f = unpack2(e);
+            f.x = ex2_approx(f.x);
+            f.y = ex2_approx(f.y);
+            sum2[w & 1] = add2(sum2[w & 1], pack2(f.x, f.y));
+            pk[w] = to_bf16x2(f.x, f.y);
+            none[w] = 0;
+          }
+          tmem_st16(tS + 16 * quarter, pk);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) tmem_st16(tS + 16 * ((quarter + i) & 3), none);
+          const float2 sum = unpack2(add2(sum2[0], sum2[1]));
+          l += sum.x + sum.y;
+          tmem_st_wait();
+        } else if (work) {
           if (__any_sync(0xffffffffu, key + kTile > hi || key < lo)) {
             // Scores that a row does not see become -inf, in place, 32 keys at a time and
             // only where there are any, so that other tiles do not pay for it. (The
@@ -677,28 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 4; ++w)
               mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
           }
-          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          if (it == 0) {
-            m = top;
-          } else {
-            const bool raise = (top - m) * c > kSlack;
-            if (__any_sync(0xffffffffu, raise)) {
-              // the accumulator is at rest: the product with the last tile's weights was
-              // issued before these scores, the next one waits for our weights
-              const float f = raise ? ex2_approx((m - top) * c) : 1.f;
-              if (raise) m = top;
-              l *= f;
-#pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t o[16];
-                tmem_ld16_issue(tO + 16 * q, o);
-                tmem_ld16_wait(o);
-#pragma unroll
-                for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * f);
-                tmem_st16(tO + 16 * q, o);
-              }
-            }
-          }
+          raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
           const float r = m == kNegInf ? 0.f : m * c;
           const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
           uint64_t sum2[2] = {0, 0};
@@ -740,9 +797,125 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool some = l > 0.f || l != l;
       const float f = !x.whole ? 1.f : some ? 1.f / l : 0.f;
       const size_t prow = (size_t)(v * 2 + x.slot) * F::kPartRows + (kPair ? s * kTile : 0) + row;
+      const int key0 = max(x.lo, x.tile0 * kTile), key1 = min(x.hi, (x.tile0 + x.n) * kTile);
+      // A value that is not finite, of a key that other rows of the unit see and this
+      // one does not, has come in with its weight of zero. Such rows are computed
+      // again from what they see, in float32: each lane has D / 32 columns.
+      auto anew = [&](int t_row, int h_row, char* dst, int a, int z, float r_ref, float r_f) {
+        constexpr int N = D / 32;
+        const char* q_row = p.q + (int64_t)t_row * p.q_token + h_row * p.q_head;
+        float q[N], o[N];
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+          q[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q_row)[lane * N + d]);
+          o[d] = 0.f;
+        }
+#pragma unroll 1
+        for (int k = a; k < z; ++k) {
+          const int page = __ldcg(p.block_table + (int64_t)x.b * p.max_pages + (k >> p.pool.page_shift));
+          if (page < 0 || page >= p.pool.n_pages) break;  // (reported by the producer)
+          const int64_t off = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride +
+                              (int64_t)(k & ((1 << p.pool.page_shift) - 1)) * p.pool.token_stride;
+          const __nv_bfloat16* kk = reinterpret_cast<const __nv_bfloat16*>(p.pool.k + off) + lane * N;
+          const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.pool.v + off) + lane * N;
+          float score = 0.f;
+#pragma unroll
+          for (int d = 0; d < N; ++d) score = fmaf(q[d], __bfloat162float(kk[d]), score);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) score += __shfl_xor_sync(0xffffffffu, score, d);
+          const float w = ex2_approx(fmaf(score, c, -r_ref));
+#pragma unroll
+          for (int d = 0; d < N; ++d) o[d] = fmaf(w, __bfloat162float(vv[d]), o[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+          if (x.whole)
+            reinterpret_cast<__nv_bfloat16*>(dst)[lane * N + d] = __float2bfloat16_rn(o[d] * r_f);
+          else
+            reinterpret_cast<float*>(dst)[lane * N + d] = o[d];
+        }
+      };
       const uint32_t last_tile = list_tiles - 1;
       const uint32_t stage_at = (kPair ? 2 * last_tile + s : 4 * last_tile + (s == 0 ? 2 : 4)) % kSlots;
-      if (work) {
+      if constexpr (kForm == kFew) {
+        // Each warp has the sums over its quarter of the keys: to the slot, and row by row
+        // from there, four quarters on one reference.
+        constexpr int kChunks = D / 4;         // 16-byte pieces of a row of sums
+        constexpr int kAtOnce = 32 / kChunks;  // rows of a warp at a time
+        static_assert(4 * kFewRows * D * 4 <= L::kTileBytes, "the quarters' sums fill a slot at most");
+        float4* stage = reinterpret_cast<float4*>(sRing + stage_at * L::kTileBytes);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32_issue(tO + 32 * q, o);
+          tmem_ld_wait(o);
+          if (valid) {
+            const float* z = reinterpret_cast<const float*>(o);
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+              stage[(quarter * kFewRows + lane) * kChunks + ((8 * q + w) ^ (lane & 7))] =
+                  make_float4(z[4 * w], z[4 * w + 1], z[4 * w + 2], z[4 * w + 3]);
+          }
+        }
+        if (valid) sh.quarter[s][quarter][lane] = make_float2(ref, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.merged[s]);
+        ok = wait_bar(&sh.merged[s], (np - 1) & 1, abort_flag);
+        if (!ok) break;
+#pragma unroll 1
+        for (int r0 = quarter * kAtOnce; r0 < x.rows; r0 += 4 * kAtOnce) {
+          const int r = r0 + lane / kChunks, ch = lane % kChunks;
+          const bool there = r < x.rows;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          float r_ref = kNegInf, r_l = 0.f, r_f = 1.f;
+          const int tok = p.by_group.quotient(r);
+          const int64_t r_t = x.token + tok;
+          const int r_head = x.h * p.group + r - tok * p.group;
+          const size_t r_prow = (size_t)(v * 2 + x.slot) * F::kPartRows + r;
+          char* dst = x.whole ? p.out + r_t * p.o_token + r_head * p.o_head : reinterpret_cast<char*>(part.out + r_prow * D);
+          if (there) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r_ref = fmaxf(r_ref, sh.quarter[s][i][r].x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 st = sh.quarter[s][i][r];
+              const float w = st.x == kNegInf ? 0.f : ex2_approx(st.x - r_ref);
+              if (st.x == kNegInf && st.y == 0.f) continue;  // saw nothing
+              const float4 z = stage[(i * kFewRows + r) * kChunks + (ch ^ (r & 7))];
+              r_l = fmaf(st.y, w, r_l);
+              y = make_float4(fmaf(z.x, w, y.x), fmaf(z.y, w, y.y), fmaf(z.z, w, y.z), fmaf(z.w, w, y.w));
+            }
+            const bool some = r_l > 0.f || r_l != r_l;
+            r_f = !x.whole ? 1.f : some ? 1.f / r_l : 0.f;
+            if (x.whole)
+              reinterpret_cast<uint2*>(dst)[ch] = make_uint2(to_bf16x2(y.x * r_f, y.y * r_f), to_bf16x2(y.z * r_f, y.w * r_f));
+            else
+              reinterpret_cast<float4*>(dst)[ch] = y;
+            if (ch == 0) {
+              if (!x.whole)
+                part.stat[r_prow] = make_float2(r_ref, r_l);
+              else if (p.lse != nullptr)
+                p.lse[r_t * p.n_heads + r_head] = some ? (r_ref + log2f(r_l)) * kLn2 : kNegInf;
+            }
+          }
+          // (also where a row sees all of the unit's keys: the other quarters' zeros
+          // have met the values that are not finite)
+          const float probe = fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, y.w * 0.f)));
+          uint32_t again = __ballot_sync(0xffffffffu, there && probe != probe && r_l == r_l);
+          __syncwarp();
+#pragma unroll 1
+          while (again != 0) {
+            const int from = __ffs(again) - 1, k = from / kChunks;
+            again &= kChunks == 32 ? 0u : ~(0xffffu << (16 * k));
+            const int tok_k = p.by_group.quotient(r0 + k), pos_k = x.pos + tok_k;
+            const int z = p.causal ? min(pos_k + 1, x.kv) : x.kv, a = p.window > 0 ? max(0, pos_k - p.window + 1) : 0;
+            anew(x.token + tok_k, x.h * p.group + r0 + k - tok_k * p.group,
+                 reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from)),
+                 max(key0, a), min(key1, z), __shfl_sync(0xffffffffu, r_ref, from), __shfl_sync(0xffffffffu, r_f, from));
+          }
+        }
+        fence_proxy_async_smem();  // the slot's next filling comes by TMA
+      } else if (work) {
         constexpr int kChunks = D / 8;       // 16-byte pieces of a staged row: D bfloat16 or D / 2 float32
         constexpr int kAtOnce = 32 / kChunks;  // rows a warp stores with one instruction
         uint4* stage = reinterpret_cast<uint4*>(sRing + stage_at * L::kTileBytes) + (warp & 3) * 32 * kChunks;
@@ -794,10 +967,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        // A value that is not finite, of a key that other rows of the unit see and this
-        // one does not, has come in with its weight of zero. Such rows are computed
-        // again from what they see, in float32: each lane has D / 32 columns.
-        const int key0 = max(x.lo, x.tile0 * kTile), key1 = min(x.hi, (x.tile0 + x.n) * kTile);
         const float2 probes = unpack2(probe2);
         const float probe = probes.x + probes.y;
         uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
@@ -805,42 +974,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (again != 0) {
           const int r = __ffs(again) - 1;
           again &= again - 1;
-          constexpr int N = D / 32;
-          const char* q_row = p.q + t_out * p.q_token + head * p.q_head;
-          q_row = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q_row), r));
           char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
-          const int a = max(key0, __shfl_sync(0xffffffffu, lo, r)), z = min(key1, __shfl_sync(0xffffffffu, hi, r));
-          const float r_ref = __shfl_sync(0xffffffffu, ref, r), r_f = __shfl_sync(0xffffffffu, f, r);
-          float q[N], o[N];
-#pragma unroll
-          for (int d = 0; d < N; ++d) {
-            q[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q_row)[lane * N + d]);
-            o[d] = 0.f;
-          }
-#pragma unroll 1
-          for (int k = a; k < z; ++k) {
-            const int page = __ldcg(p.block_table + (int64_t)x.b * p.max_pages + (k >> p.pool.page_shift));
-            if (page < 0 || page >= p.pool.n_pages) break;  // (reported by the producer)
-            const int64_t off = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride +
-                                (int64_t)(k & ((1 << p.pool.page_shift) - 1)) * p.pool.token_stride;
-            const __nv_bfloat16* kk = reinterpret_cast<const __nv_bfloat16*>(p.pool.k + off) + lane * N;
-            const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.pool.v + off) + lane * N;
-            float score = 0.f;
-#pragma unroll
-            for (int d = 0; d < N; ++d) score = fmaf(q[d], __bfloat162float(kk[d]), score);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) score += __shfl_xor_sync(0xffffffffu, score, d);
-            const float w = ex2_approx(fmaf(score, c, -r_ref));
-#pragma unroll
-            for (int d = 0; d < N; ++d) o[d] = fmaf(w, __bfloat162float(vv[d]), o[d]);
-          }
-#pragma unroll
-          for (int d = 0; d < N; ++d) {
-            if (x.whole)
-              reinterpret_cast<__nv_bfloat16*>(dst)[lane * N + d] = __float2bfloat16_rn(o[d] * r_f);
-            else
-              reinterpret_cast<float*>(dst)[lane * N + d] = o[d];
-          }
+          const int t_row = __shfl_sync(0xffffffffu, (int)t_out, r), h_row = __shfl_sync(0xffffffffu, head, r);
+          anew(t_row, h_row, dst, max(key0, __shfl_sync(0xffffffffu, lo, r)), min(key1, __shfl_sync(0xffffffffu, hi, r)),
+               __shfl_sync(0xffffffffu, ref, r), __shfl_sync(0xffffffffu, f, r));
         }
         if (valid) {
           if (!x.whole)
@@ -875,24 +1012,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kPair>
+template <int D, int kForm>
 cudaError_t prepare_kernel() {
   cudaError_t e =
-      cudaFuncSetAttribute(attn_tc_kernel<D, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+      cudaFuncSetAttribute(attn_tc_kernel<D, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
   if (e != cudaSuccess) return e;
   // an increase of registers that the launch pool cannot satisfy would never return
   cudaFuncAttributes a;
-  e = cudaFuncGetAttributes(&a, attn_tc_kernel<D, kPair>);
+  e = cudaFuncGetAttributes(&a, attn_tc_kernel<D, kForm>);
   if (e != cudaSuccess) return e;
   return a.numRegs == (int)kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
-template <int D, bool kPair>
+template <int D, int kForm>
 cudaError_t launch(const AttnParams& p, cudaStream_t s) {
-  static const cudaError_t ready = prepare_kernel<D, kPair>();
+  static const cudaError_t ready = prepare_kernel<D, kForm>();
   if (ready != cudaSuccess) return ready;
   CUtensorMap mq, mk, mv;
-  const int per_tile = kTile / p.group;
+  const int per_tile = (kForm == kFew ? kFewRows : kTile) / p.group;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.n_heads, (cuuint64_t)p.T};
     const cuuint64_t str[2] = {(cuuint64_t)p.q_head, (cuuint64_t)p.q_token};
@@ -907,12 +1044,12 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     if (!encode_tmap_bf16(&mk, p.pool.k, 4, dims, str, box) || !encode_tmap_bf16(&mv, p.pool.v, 4, dims, str, box))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_early(attn_tc_kernel<D, kPair>, dim3(kMaxAttnCtas), dim3(kThreads), Layout<D>::kBytes, s, p, mq,
+  cudaError_t e = launch_early(attn_tc_kernel<D, kForm>, dim3(kMaxAttnCtas), dim3(kThreads), Layout<D>::kBytes, s, p, mq,
                                mk, mv);
   if (e != cudaSuccess) return e;
-  using F = Form<kPair>;
+  using F = Form<kForm>;
   const int rows = p.max_q <= per_tile ? p.max_q * p.group : F::kPartRows;
-  return launch_join<F, D, __nv_bfloat16>(p, s, rows, kTile, per_tile * p.group);
+  return launch_join<F, D, __nv_bfloat16>(p, s, rows, kForm == kFew ? kFewRows : kTile, per_tile * p.group);
 }
 
 }  // namespace
@@ -920,10 +1057,14 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s) {
   // Two row tiles a unit if the requests fill more than one on average. 128 requests
   // of 136 rows each: pair 258 us, solo 386; of 8 to 136 rows: 236 and 216.
+  // Few rows against solo: 128 requests of 4 rows, 300 to 8000 cached 193 us (6.4 TB/s)
+  // and 197, D = 64 158 and 164; 512 of 2 rows, 1 to 300 cached 63 and 85; 64 of 16 rows
+  // 111 and 113. (The quarters' sums of 16 rows fill the staging slot.)
   const int per_tile = kTile / p.group;
   const bool pair = p.max_q > per_tile && p.T > (int64_t)p.B * per_tile;
-  if (p.D == 128) return pair ? launch<128, true>(p, s) : launch<128, false>(p, s);
-  return pair ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  const bool few = (int64_t)p.max_q * p.group <= kFewRows;
+  if (p.D == 128) return few ? launch<128, kFew>(p, s) : pair ? launch<128, kPairs>(p, s) : launch<128, kSolo>(p, s);
+  return few ? launch<64, kFew>(p, s) : pair ? launch<64, kPairs>(p, s) : launch<64, kSolo>(p, s);
 }
 
 }  // namespace ds
