@@ -192,6 +192,27 @@ def test_attention_of_values_that_some_of_few_rows_do_not_see(kv, dtype, D, G, n
     check_unseen_values(kv, dtype, D, G, window, float("nan"), [(n_q, 300), (3, 70), (n_q, 2100), (n_q, n_q)])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,n_q", [(128, 1, 1), (64, 4, 2), (64, 16, 1), (128, 24, 1), (128, 4, 70)])
+def test_attention_of_an_infinite_value(kv, dtype, D, G, n_q):
+    """An infinite value that every row of a request sees is their sum in its column; other columns are as without it."""
+    lens = [(n_q, 300), (n_q, n_q + 3), (n_q, 2500), (n_q, 5000)]
+    x = Batch(dtype, D, 16, 2, G, lens, seed=17)
+    x.verify(kv)
+    clean = x.out.clone()
+    table, row = x.table.cpu().numpy(), 0
+    for b, (nq, n) in enumerate(lens):
+        j = (n - nq) // 2
+        x.v[0, int(table[b, j // 16]), j % 16, 1, 3] = float("inf") if b % 2 else -float("inf")
+    assert x.call(kv) == 0 and int(x.status[0]) == 0
+    got, want = _host(x.out), _host(clean)
+    for b, (nq, n) in enumerate(lens):
+        rows, row = slice(row, row + nq), row + nq
+        assert (got[rows, G:, 3] == (np.inf if b % 2 else -np.inf)).all(), b
+        got[rows, G:, 3] = want[rows, G:, 3]
+    assert (np.abs(got - want) <= 2 ** -7 * np.abs(want).max()).all()
+
+
 def check_unseen_values(kv, dtype, D, G, window, what, lens):
     x = Batch(dtype, D, 16, 2, G, lens, window=window, seed=31)
     x.verify(kv)
