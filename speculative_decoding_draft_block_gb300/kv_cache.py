@@ -10,6 +10,7 @@ the package, PyTorch tensors are device memory only and there is no fallback.
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -60,7 +61,24 @@ class CompactArgs(ctypes.Structure):
                 ("n_used", _vp), ("workspace", _vp), ("workspace_bytes", _sz), ("status", _vp)]
 
 
+# A call's arguments are packed as bytes, the pool's first (filling in a ctypes structure
+# field by field takes a fifth of a small call).
+_CODES = {_i32: "i", _i64: "q", _vp: "P", _sz: "N", ctypes.c_float: "f"}
+
+
+def _packer(args):
+    """struct.pack for an argument structure's fields after the pool, with C's alignment."""
+    assert args._fields_[0] == ("pool", PoolDesc)
+    s = struct.Struct("@" + "".join(_CODES[t] for _, t in args._fields_[1:]) + "0P")
+    assert ctypes.sizeof(PoolDesc) % 8 == 0 and ctypes.sizeof(PoolDesc) + s.size == ctypes.sizeof(args)
+    return s.pack
+
+
+_pack_append, _pack_attention = _packer(AppendArgs), _packer(AttentionArgs)
+_pack_update, _pack_compact = _packer(UpdateArgs), _packer(CompactArgs)
+
 _bound = None
+_entries = {}   # the calls, taking packed arguments
 
 
 def load():
@@ -72,6 +90,7 @@ def load():
                            ("ds_cache_update", UpdateArgs), ("ds_cache_compact", CompactArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
             getattr(lib, name).restype = ctypes.c_int
+            _entries[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, _vp)((name, lib))
         for name, args in (("ds_paged_attention_workspace_bytes", [_i32, _i32]),
                            ("ds_cache_update_workspace_bytes", [_i32, _i32]),
                            ("ds_cache_compact_workspace_bytes", [_i32])):
@@ -81,33 +100,42 @@ def load():
     return _bound
 
 
-def _words(t, name, n=None):
+def _entry(name):
+    if _bound is None:
+        load()
+    return _entries[name]
+
+
+def _words(t, name, n=None, _int32=torch.int32):
     """Device address of a contiguous int32 tensor (of n elements, if given)."""
-    if t.dtype is not torch.int32:
+    if t.dtype is _int32 and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n):
+        return t.data_ptr()
+    if t.dtype is not _int32:
         raise ValueError("%s must be int32" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if n is not None and t.numel() != n:
-        raise ValueError("%s must have %d elements" % (name, n))
-    return t.data_ptr()
+    raise ValueError("%s must have %d elements" % (name, n))
 
 
-def _rows(t, name, pool, heads=None):
-    """Device address, token and head stride of [T, heads, head_dim] of the pool's dtype."""
+def _rows(t, name, pool, shape, heads=None):
+    """Device address, token and head stride of a tensor [T, heads, head_dim] (of that
+    `shape`) of the pool's dtype."""
     if t.dtype is not pool.dtype:
         raise ValueError("%s must have the pool's dtype" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    shape, st = t.shape, t.stride()
     if len(shape) != 3 or shape[2] != pool.head_dim or (heads is not None and shape[1] != heads):
         raise ValueError("%s must be [T, heads, head_dim]" % name)
-    if st[2] != 1:
+    ts, hs, one = t.stride()
+    if one != 1:
         raise ValueError("%s: the last index must be contiguous" % name)
     # a stride that is never taken may be anything in torch: give the natural one
-    hs = st[1] if shape[1] > 1 else pool.head_dim
-    ts = st[0] if shape[0] > 1 else shape[1] * pool.head_dim
+    if shape[1] == 1:
+        hs = pool.head_dim
+    if shape[0] <= 1:
+        ts = shape[1] * pool.head_dim
     return t.data_ptr(), ts, hs
 
 
@@ -153,19 +181,21 @@ class KvPool:
             st[1] = self.page_size * self.n_kv_heads * self.head_dim
         self.desc = PoolDesc(_lib._dtype_code(k), self.n_layers, self.n_pages, self.page_size, self.n_kv_heads,
                              self.head_dim, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3])
+        self.packed = bytes(self.desc)
 
 
 def ds_cache_append(pool, layer, k_new, v_new, q_start, block_table, kv_len, status, stream=None):
     """New keys and values [T, n_kv_heads, head_dim] into their pages."""
     B, M = block_table.shape
-    k, kt, kh = _rows(k_new, "k_new", pool, pool.n_kv_heads)
-    v, vt, vh = _rows(v_new, "v_new", pool, pool.n_kv_heads)
-    if v_new.shape != k_new.shape:
+    shape = k_new.shape
+    k, kt, kh = _rows(k_new, "k_new", pool, shape, pool.n_kv_heads)
+    v, vt, vh = _rows(v_new, "v_new", pool, v_new.shape, pool.n_kv_heads)
+    if v_new.shape != shape:
         raise ValueError("k_new and v_new must have one shape")
-    a = AppendArgs(pool.desc, layer, B, k_new.shape[0], M, k, v, kt, kh, vt, vh,
+    a = pool.packed + _pack_append(layer, B, shape[0], M, k, v, kt, kh, vt, vh,
                    _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
                    _words(kv_len, "kv_len", B), _words(status, "status"))
-    return load().ds_cache_append(a, _stream(stream, pool))
+    return _entry("ds_cache_append")(a, _stream(stream, pool))
 
 
 def ds_paged_attention_workspace_bytes(pool, n_heads):
@@ -180,22 +210,23 @@ def ds_paged_attention(pool, layer, q, q_start, max_q, block_table, kv_len, out,
     """Attention of ragged rows q [T, n_heads, head_dim] over the cache; `scale`
     defaults to 1 / sqrt(head_dim). Writes out and, if given, lse [T, n_heads] float32."""
     B, M = block_table.shape
-    T, H = q.shape[0], q.shape[1]
-    qp, qt, qh = _rows(q, "q", pool)
-    op, ot, oh = _rows(out, "out", pool, H)
+    shape = q.shape
+    qp, qt, qh = _rows(q, "q", pool, shape)
+    T, H = shape[0], shape[1]
+    op, ot, oh = _rows(out, "out", pool, out.shape, H)
     if out.shape[0] != T:
         raise ValueError("out must have q's shape")
-    lp = None
+    lp = 0
     if lse is not None:
         if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.numel() != T * H:
             raise ValueError("lse must be a contiguous float32 CUDA tensor [T, n_heads]")
         lp = lse.data_ptr()
     wp, wn = _bytes(workspace, "workspace")
-    a = AttentionArgs(pool.desc, layer, B, T, M, max_q, H, 1 if causal else 0, window,
+    a = pool.packed + _pack_attention(layer, B, T, M, max_q, H, 1 if causal else 0, window,
                       1.0 / math.sqrt(pool.head_dim) if scale is None else scale, qp, qt, qh,
                       _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
                       _words(kv_len, "kv_len", B), op, ot, oh, lp, wp, wn, _words(status, "status"))
-    return load().ds_paged_attention(a, _stream(stream, pool))
+    return _entry("ds_paged_attention")(a, _stream(stream, pool))
 
 
 def ds_cache_update_workspace_bytes(B, n_pages):
@@ -208,12 +239,12 @@ def ds_cache_update(pool, block_table, kv_len, ref, new_len, table_out, len_out,
     B, M = block_table.shape
     N = pool.n_pages
     wp, wn = _bytes(workspace, "workspace")
-    a = UpdateArgs(pool.desc, B, M, _words(block_table, "block_table"), _words(kv_len, "kv_len", B),
-                   _words(ref, "ref", N), None if parent is None else _words(parent, "parent", B),
+    a = pool.packed + _pack_update(B, M, _words(block_table, "block_table"), _words(kv_len, "kv_len", B),
+                   _words(ref, "ref", N), 0 if parent is None else _words(parent, "parent", B),
                    _words(new_len, "new_len", B), _words(table_out, "table_out", B * M),
                    _words(len_out, "len_out", B), _words(ref_out, "ref_out", N), wp, wn,
                    _words(status, "status"))
-    return load().ds_cache_update(a, _stream(stream, pool))
+    return _entry("ds_cache_update")(a, _stream(stream, pool))
 
 
 def ds_cache_compact_workspace_bytes(n_pages):
@@ -225,10 +256,10 @@ def ds_cache_compact(pool, block_table, ref, table_out, ref_out, page_map, n_use
     B, M = block_table.shape
     N = pool.n_pages
     wp, wn = _bytes(workspace, "workspace")
-    a = CompactArgs(pool.desc, B, M, _words(block_table, "block_table"), _words(ref, "ref", N),
+    a = pool.packed + _pack_compact(B, M, _words(block_table, "block_table"), _words(ref, "ref", N),
                     _words(table_out, "table_out", B * M), _words(ref_out, "ref_out", N),
                     _words(page_map, "page_map", N), _words(n_used, "n_used", 1), wp, wn, _words(status, "status"))
-    return load().ds_cache_compact(a, _stream(stream, pool))
+    return _entry("ds_cache_compact")(a, _stream(stream, pool))
 
 
 class PagedCache:
