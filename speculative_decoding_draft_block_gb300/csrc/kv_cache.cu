@@ -22,7 +22,7 @@ namespace {
 // threads find the rows' requests together by counting the requests that end
 // at or before each row (one coalesced pass over q_start, no chain of
 // dependent loads as in a bisection per row). Bound by memory: prompts of 16 requests
-// (462 MB) 71.7 us, 6.4 TB/s; below a few MB by the launch, 8 us.
+// (462 MB) 71.7 us, 6.4 TB/s; below a few MB by the launch, 6 to 7 us.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;
 
