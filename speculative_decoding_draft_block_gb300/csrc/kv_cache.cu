@@ -18,20 +18,22 @@ namespace {
 //
 // pool[table[b][p / S]][p % S] = new[q_start[b] + i], p = kv_len[b] - n_b + i:
 // a gather of ragged rows into pages, 4 * T * Hk * D * e bytes moved and
-// nothing computed. A block takes kAppendTokens consecutive rows; all its
+// nothing computed. A block takes kTokens consecutive rows; all its
 // threads find the rows' requests together by counting the requests that end
 // at or before each row (one coalesced pass over q_start, no chain of
 // dependent loads as in a bisection per row). Bound by memory: prompts of 16 requests
 // (462 MB) 71.7 us, 6.4 TB/s; below a few MB by the launch, 6 to 7 us.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 8;
 
+// kTokens rows a block: see launch_append.
+template <int kTokens>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  __shared__ int ends[kAppendTokens];
-  __shared__ int64_t at[kAppendTokens];  // byte offset of the row's place in the pool, -1: none
-  const int t0 = blockIdx.x * kAppendTokens;
+  static_assert(kTokens <= 32, "a lane a row");
+  __shared__ int ends[kTokens];
+  __shared__ int64_t at[kTokens];  // byte offset of the row's place in the pool, -1: none
+  const int t0 = blockIdx.x * kTokens;
   const int tid = threadIdx.x;
-  if (tid < kAppendTokens) ends[tid] = 0;
+  if (tid < kTokens) ends[tid] = 0;
   int before = 0;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -40,7 +42,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const int e = __ldcg(p.q_start + i + 1);
     if (e <= t0)
       ++before;
-    else if (e < t0 + kAppendTokens)
+    else if (e < t0 + kTokens)
       atomicAdd(&ends[e - t0], 1);
   }
   // requests that end at or before t0, over the block
@@ -48,10 +50,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __shared__ int warp_before[kAppendThreads / 32];
   if ((tid & 31) == 0) warp_before[tid >> 5] = before;
   __syncthreads();
-  if (tid < kAppendTokens) {
+  if (tid < kTokens) {
     int b = 0;
     for (int w = 0; w < kAppendThreads / 32; ++w) b += warp_before[w];
-    for (int i = 1; i <= tid; ++i) b += ends[i];
+    int here = tid > 0 ? ends[tid] : 0;  // requests that end at the block's rows 1 .. tid
+    constexpr uint32_t kLanes = kTokens == 32 ? 0xffffffffu : (1u << kTokens) - 1;
+#pragma unroll
+    for (int d = 1; d < kTokens; d <<= 1) {
+      const int v = __shfl_up_sync(kLanes, here, d);
+      if (tid >= d) here += v;
+    }
+    b += here;
     const int t = t0 + tid;
     int64_t off = -1;
     if (t < p.T && b < p.B) {
@@ -74,7 +83,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __syncthreads();
   const int chunks = p.pool.row_bytes >> 4;        // 16-byte pieces of a head's row
   const int per_token = chunks * p.pool.n_kv_heads;
-  for (int x = tid; x < kAppendTokens * per_token; x += kAppendThreads) {
+  for (int x = tid; x < kTokens * per_token; x += kAppendThreads) {
     const int i = x / per_token, y = x - i * per_token;
     const int h = y / chunks, c = y - h * chunks;
     const int64_t off = at[i];
@@ -142,8 +151,13 @@ bool overlap(const void* a, const void* b, size_t na, size_t nb) {
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
-  const int blocks = (p.T + kAppendTokens - 1) / kAppendTokens;
-  return launch_early(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, s, p);
+  const int pieces = p.pool.n_kv_heads * (p.pool.row_bytes >> 4);  // 16-byte pieces of a row
+  // Eight rows of 1 KB and more keep a block's threads busy, of smaller rows it takes
+  // more: 16 prompts (56 k rows) of 128 bytes 6.2 us by 32 rows a block, 12.3 by 8;
+  // of 512 bytes 22.0 and 23.1; of 1 KB 39.3 and 38.4; of 2 KB 74.4 and 71.8.
+  const int tokens = pieces >= 64 ? 8 : 32;
+  const dim3 blocks((p.T + tokens - 1) / tokens);
+  return launch_early(tokens == 8 ? append_kernel<8> : append_kernel<32>, blocks, dim3(kAppendThreads), 0, s, p);
 }
 
 }  // namespace ds
