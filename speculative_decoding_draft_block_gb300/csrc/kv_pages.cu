@@ -507,14 +507,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   cl.sync();
 }
 
-// A block takes (move, layer, K or V) items; the number of moves is known on the
-// device only, so a fixed grid walks over them. The table's entries go to the
+// Groups of threads take (move, layer, K or V) items; the number of moves is known on
+// the device only, so a fixed grid walks over them. The table's entries go to the
 // blocks from the last one down: with few moves those have nothing to copy.
-__global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams p) {
+// Pages smaller than what a block has in flight (32 KB) go to smaller groups: 15410
+// pages of 2 KB a layer, 4 layers, 32.7 us, by whole blocks 85; 58450 of 4 KB 160 and
+// 325. Three blocks an SM: left to itself the compiler takes 64 registers, which has
+// four, and 4 GB take 340 us instead of 323.
+__global__ void __launch_bounds__(256, 3) compact_apply_kernel(const CompactParams p) {
   const CompactWs w = compact_ws(p.ws, p.pool.n_pages);
   const int parts = 2 * p.pool.n_layers, tokens = 1 << p.pool.page_shift;
   const int64_t entries = (int64_t)p.B * p.max_pages;
-  int64_t x = blockIdx.x, e = (int64_t)(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
+  // threads of an item
+  int threads = blockDim.x;
+  while (threads > 32 && threads * kFlight * 16 > tokens * p.pool.n_kv_heads * p.pool.row_bytes) threads >>= 1;
+  const int step = gridDim.x * (blockDim.x / threads), first = blockIdx.x + threadIdx.x / threads * gridDim.x;
+  int i = first / parts, part = first % parts;  // item: move, layer and K or V
+  int64_t e = (int64_t)(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   int page = e < entries ? __ldcg(p.table + e) : -1;
@@ -527,10 +536,15 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams 
     if (next < entries) page = __ldcg(p.table + next);
     p.table_out[e] = fail ? now : now >= 0 && now < p.pool.n_pages ? __ldcg(p.page_map + now) : -1;
   }
-  for (; x < (int64_t)n * parts; x += gridDim.x) {
-    const int i = (int)(x / parts), part = (int)(x - (int64_t)i * parts);
+  while (i < n) {
     char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
-    copy_tokens(p.pool, base, __ldcg(w.src + i), __ldcg(w.dst + i), tokens, threadIdx.x, blockDim.x);
+    copy_tokens(p.pool, base, __ldcg(w.src + i), __ldcg(w.dst + i), tokens, threadIdx.x & (threads - 1), threads);
+    i += step / parts;
+    part += step % parts;
+    if (part >= parts) {
+      part -= parts;
+      ++i;
+    }
   }
 }
 
