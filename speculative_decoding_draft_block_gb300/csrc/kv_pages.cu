@@ -7,7 +7,7 @@
 // without a grid-wide wait. The second launch spreads what is left (tables and
 // page contents) over the whole GPU, reading the plan from the workspace (past the
 // first-level cache: it is set up, and may be resident, while the plan runs).
-// Update of 128 requests and 16384 pages: 12.5 us (the plan alone 11). Compaction of
+// Update of 128 requests and 16384 pages: 12.0 us (the plan alone 10.6). Compaction of
 // 4 GB, half of it held (2.06 GB read and written): 323 us, 6.4 TB/s.
 #include <cooperative_groups.h>
 
