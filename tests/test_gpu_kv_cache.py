@@ -362,6 +362,47 @@ def test_append_places_rows(kv):
         assert int(status[0]) == (6 if lost else 0)
 
 
+@pytest.mark.parametrize("dtype,Hk", [("bf16", 8), ("f32", 1)])
+@pytest.mark.parametrize("q_start,kv_len", [([0, 20, 3, 4], [30, 32, 32]), ([0, 100, 1, 2], [30, 32, 32]),
+                                            ([0, 4, 8, 25], [30, 31, 32]), ([-1, 4, 8, 20], [32, 9, 32]),
+                                            ([0, 20, 12, 20], [32, 32, 32]), ([-1, -1, -1, -1], [32, 32, 32]),
+                                            ([0, 4, 8, 20], [30, 33, 32]), ([0, 4, 8, 20], [4, -1, 12]),
+                                            ([21, 21, 21, 21], [8, 8, 8]), ([5, 3, 0, 2], [32, 32, 32])])
+def test_append_refuses_malformed_requests(kv, dtype, Hk, q_start, kv_len):
+    """Row starts that decrease or leave the rows, lengths out of range: reported, and only rows of a well-formed request
+    are written, each to its own place. Behind the table stand words that would pass for pages."""
+    S, M, N, T, D = 16, 2, 90, 20, 64
+    B = len(kv_len)
+    ok = [0 <= q_start[b] <= q_start[b + 1] <= T and 0 <= kv_len[b] <= M * S for b in range(B)]
+    g = torch.Generator(device="cuda").manual_seed(2)
+    words = _i32(np.arange(B * M + 64))
+    table = words[:B * M].view(B, M)
+    k, v = (torch.randn((1, N, S, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    kn, vn = (torch.randn((T, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    old_k, old_v = k.clone(), v.clone()
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    kv.check(kv.ds_cache_append(kv.KvPool(k, v), 0, kn, vn, _i32(q_start), table, _i32(kv_len), status))
+    assert int(status[0]) == 6
+    free = torch.ones((N, S), dtype=torch.bool, device="cuda")
+    for b in range(B):
+        n = q_start[b + 1] - q_start[b]
+        for i in range(n if ok[b] else 0):
+            p, t = kv_len[b] - n + i, q_start[b] + i
+            if p < 0:
+                continue
+            page, at = b * M + p // S, p % S
+            free[page, at] = False
+            for x, new, old in ((k, kn, old_k), (v, vn, old_v)):
+                assert torch.equal(x[0, page, at], new[t]) or torch.equal(x[0, page, at], old[0, page, at])
+    assert torch.equal(k[0][free], old_k[0][free]) and torch.equal(v[0][free], old_v[0][free])
+    if q_start == sorted(q_start) and 0 <= q_start[0] and q_start[-1] <= T:      # the rows of the others stand
+        for b in range(B):
+            n = q_start[b + 1] - q_start[b]
+            for i in range(n if ok[b] else 0):
+                p = kv_len[b] - n + i
+                assert p < 0 or torch.equal(k[0, b * M + p // S, p % S], kn[q_start[b] + i])
+
+
 def _state(rng, B, S, N, width, M, pins):
     """Requests in groups that share their first pages; some empty; some pages pinned from outside."""
     pages = list(rng.permutation(N))
