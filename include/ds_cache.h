@@ -98,7 +98,9 @@ ds_status ds_cache_append(const ds_append_args* args, ds_stream_t stream);
  * outside a row's view (past kv_len, before the window, later tokens) has no
  * effect on it, whatever its bits; pages that no row sees need no table entry.
  * (Values that are not finite, seen by some rows of a request and not by others,
- * cost those others a second, slow computation.)
+ * cost those others a second, slow computation: bfloat16 58 to 217 rows x keys a
+ * us and SM, float32 2 to 4. In bfloat16 calls of up to 16 rows a KV head it is done
+ * for the rows that see the value, too.)
  * bfloat16: products and sums in float32, the weights exp(s_j - r) of the
  * value product rounded to bfloat16. float32: all in float32.
  */

@@ -103,6 +103,12 @@ enum : uint32_t {
   kPart = 32u   // only keys [bits 8..15, bits 16..23) of the tile are seen
 };
 
+// What the waits look at beside their barrier.
+struct Watch {
+  int abort;  // a wait has given up
+  int beat;   // counts up while rows are computed again (see `anew`), which may take long
+};
+
 struct Header {
   Piece piece[2][kAhead];
   uint64_t piece_full[2][kAhead], piece_empty[2][kAhead];
@@ -117,7 +123,7 @@ struct Header {
   uint32_t staged[2];         // softmax warps that are done with a piece's staging slot
   int ended[2];         // tiles of a stream's share, -1 while not known
   uint32_t tmem;
-  int abort_flag;
+  Watch watch;
   ShareStart<kThreads, 2> work;
 };
 static_assert(sizeof(Header) <= kHeader, "header");
@@ -156,17 +162,27 @@ struct Form : WorkForm<kTile, kForm == kPairs ? kMaxAttnCtas : 2 * kMaxAttnCtas,
 
 // Bounded waits. One that gives up sets the abort flag, which ends every role's
 // loop; the status is reported once, at the kernel's end (the waits are many and
-// inlined, and the warps' loops share one instruction cache).
+// inlined, and the warps' loops share one instruction cache). A wait gives up once
+// the beat has stood still for its limit; the beat comes every 32 keys of a
+// recomputation, so that one of any length is waited for.
+__device__ __forceinline__ bool given_up(volatile Watch* watch, int& beat, uint32_t& polled, uint32_t limit) {
+  if (polled >= limit) {
+    const int now = watch->beat;
+    if (now == beat) watch->abort = 1;
+    beat = now;
+    polled = 0;
+  }
+  return watch->abort != 0;
+}
 
 // Waits until the entry of that number stands in a slot.
-__device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile Watch* watch) {
   const volatile uint32_t* at = entry;
+  int beat = 0;
 #pragma unroll 1
-  for (uint32_t i = 0; *at != number; ++i) {
+  for (uint32_t i = 1; *at != number; ++i) {
     __nanosleep(40);
-    if ((i & 255) != 255) continue;
-    if (i >= (kWaitPolls << 8)) *abort_flag = 1;
-    if (*abort_flag) return false;
+    if ((i & 255) == 0 && given_up(watch, beat, i, kWaitPolls << 8)) return false;
   }
   return true;
 }
@@ -174,20 +190,18 @@ __device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t numb
 // By one thread: about a second with kWaitPolls, a minute with kIdlePolls, for
 // roles that may have nothing to do for as long as a unit lasts.
 constexpr uint32_t kIdlePolls = 1u << 22;
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t polls) {
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile Watch* watch, uint32_t polls) {
+  int beat = 0;
 #pragma unroll 1
-  for (uint32_t i = 0; !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {
-    if ((i & 15) != 15) continue;
-    if (i >= polls) *abort_flag = 1;
-    if (*abort_flag) return false;
-  }
+  for (uint32_t i = 1; !mbar_try_wait_sleep(bar, parity, 20000u); ++i)
+    if ((i & 15) == 0 && given_up(watch, beat, i, polls)) return false;
   return true;
 }
 
 // The same by a whole warp, with one answer for all lanes: warp-wide instructions follow.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile Watch* watch,
                                          uint32_t polls = kWaitPolls) {
-  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, polls));
+  return __all_sync(0xffffffffu, wait_one(bar, parity, watch, polls));
 }
 
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
@@ -216,6 +230,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// One or two words, zeros if they are not there.
+__device__ __forceinline__ void load_words(uint32_t (&to)[1], const char* from, bool there) {
+  to[0] = there ? __ldcg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+}
+__device__ __forceinline__ void load_words(uint32_t (&to)[2], const char* from, bool there) {
+  const uint2 y = there ? __ldcg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+  to[0] = y.x;
+  to[1] = y.y;
 }
 
 // ---- the kernel --------------------------------------------------------------------------
@@ -262,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.empty[i], 1);
       sh.entry[i] = 0;
     }
-    sh.abort_flag = 0;
+    sh.watch.abort = 0;
+    sh.watch.beat = 0;
     fence_barrier_init();
   }
 
@@ -286,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) tmem_dealloc(tmem, 512);
     return;
   }
-  volatile int* abort_flag = &sh.abort_flag;
+  volatile Watch* watch = &sh.watch;
   pdl_launch_dependents();
 
   if (warp < 4) {
@@ -332,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (does_k) {
             const uint32_t i = np % kAhead;
-            ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, abort_flag, kIdlePolls);
+            ok = wait_bar(&sh.piece_empty[l][i], ((np / kAhead) & 1) ^ 1, watch, kIdlePolls);
             if (!ok) break;
             if (lane == 0) {
               sh.piece[l][i] = x;
@@ -349,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s0 = kPair ? 0 : l, s1 = kPair ? (x.rows > tile_rows ? 1 : 0) : l;
 #pragma unroll 1
             for (int s = s0; s <= s1; ++s) {
-              ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], abort_flag);
+              ok = wait_bar(&sh.q_empty[s], s == 0 ? q_par[0] : q_par[1], watch);
               if (!ok) break;
               if (s == 0) q_par[0] ^= 1;
               if (s == 1) q_par[1] ^= 1;
@@ -389,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = kv ? vp.slot : kp.slot, parity = kv ? vp.parity : kp.parity;
           const uint32_t number = kv ? vp.number : kp.number;
           if (number >= (uint32_t)kSlots)
-            ok = __all_sync(0xffffffffu, wait_number(&sh.entry[slot], number - kSlots + 1, abort_flag));
-          ok = ok && wait_bar(&sh.empty[slot], parity ^ 1, abort_flag);
+            ok = __all_sync(0xffffffffu, wait_number(&sh.entry[slot], number - kSlots + 1, watch));
+          ok = ok && wait_bar(&sh.empty[slot], parity ^ 1, watch);
           if (!ok) break;
           if (ended) {
             // (whether the other stream has ended is read after the wait for a slot: what
@@ -447,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // as three products. `good`: no wait has given up (that lane's flag).
       bool good = true;
       auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-        good = good && wait_one(bar, parity, abort_flag, kWaitPolls);
+        good = good && wait_one(bar, parity, watch, kWaitPolls);
       };
       auto wait_entry = [&](const RingPos<kSlots>& at) {
-        if (!kPair) good = good && wait_number(&sh.entry[at.slot], at.number + 1, abort_flag);
+        if (!kPair) good = good && wait_number(&sh.entry[at.slot], at.number + 1, watch);
         wait1(&sh.full[at.slot], at.parity);
       };
       // S = Q K^T of stream s with the keys in `slot`; `free_k`: nothing else needs the slot
@@ -495,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto clear = [&](uint32_t info) {
         if (elect_one()) wait_entry(vp);
         __syncwarp();
-        if (__any_sync(0xffffffffu, *abort_flag)) return;
+        if (__any_sync(0xffffffffu, watch->abort)) return;
         const int head = (info >> 8) & 255, tail = (info >> 16) & 255;
         uint8_t* tile = sRing + vp.slot * L::kTileBytes;
 #pragma unroll 1
@@ -625,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int list = kPair ? 0 : s;
     for (uint32_t k = 0;; ++k) {
       const uint32_t at = k % kAhead;
-      if (!wait_bar(&sh.piece_full[list][at], (k / kAhead) & 1, abort_flag, kIdlePolls)) break;
+      if (!wait_bar(&sh.piece_full[list][at], (k / kAhead) & 1, watch, kIdlePolls)) break;
       const Piece x = sh.piece[list][at];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.piece_empty[list][at]);
@@ -679,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int it = 0; it < x.n; ++it) {
         const int key = (x.tile0 + it) * kTile;
-        ok = wait_bar(&sh.s_full[s], ns & 1, abort_flag);
+        ok = wait_bar(&sh.s_full[s], ns & 1, watch);
         if (!ok) break;
         tc_fence_after();
         if constexpr (kForm == kFew) {
@@ -783,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
       }
       if (!ok) break;
-      ok = wait_bar(&sh.pv_done[s], np & 1, abort_flag);
+      ok = wait_bar(&sh.pv_done[s], np & 1, watch);
       if (!ok) break;
       ++np;
       tc_fence_after();
@@ -799,40 +824,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t prow = (size_t)(v * 2 + x.slot) * F::kPartRows + (kPair ? s * kTile : 0) + row;
       const int key0 = max(x.lo, x.tile0 * kTile), key1 = min(x.hi, (x.tile0 + x.n) * kTile);
       // A value that is not finite, of a key that other rows of the unit see and this
-      // one does not, has come in with its weight of zero. Such rows are computed
-      // again from what they see, in float32: each lane has D / 32 columns.
-      auto anew = [&](int t_row, int h_row, char* dst, int a, int z, float r_ref, float r_f) {
-        constexpr int N = D / 32;
-        const char* q_row = p.q + (int64_t)t_row * p.q_token + h_row * p.q_head;
-        float q[N], o[N];
-#pragma unroll
-        for (int d = 0; d < N; ++d) {
-          q[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q_row)[lane * N + d]);
-          o[d] = 0.f;
-        }
+      // one does not, has come in with its weight of zero. Such rows (`again`: a bit a
+      // lane that has a row's place, keys, reference and factor) are computed again from
+      // what they see, in float32, four at a time over the same keys: each lane has D / 32
+      // columns; of eight keys' 32 products every lane ends up with one sum, its weight
+      // (-1: unseen), and hands it to all. A piece may be as long as the cache, so
+      // the other roles' waits follow the beat.
+      // 58 to 217 rows x keys a us and SM: 210 rows over 100,000 keys (D = 64) 95 ms.
+      auto anew = [&](uint32_t again, int t_row, int h_row, char* dst, int a, int z, float r_ref, float r_f) {
+        constexpr int N = D / 32, kR = 4, kK = 8;  // columns, rows, keys
+        static_assert(kR * kK == 32, "a lane a row and key");
+        const int shift = p.pool.page_shift;
+        __syncwarp();  // the rows as they were first stored
 #pragma unroll 1
-        for (int k = a; k < z; ++k) {
-          const int page = __ldcg(p.block_table + (int64_t)x.b * p.max_pages + (k >> p.pool.page_shift));
-          if (page < 0 || page >= p.pool.n_pages) break;  // (reported by the producer)
-          const int64_t off = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride +
-                              (int64_t)(k & ((1 << p.pool.page_shift) - 1)) * p.pool.token_stride;
-          const __nv_bfloat16* kk = reinterpret_cast<const __nv_bfloat16*>(p.pool.k + off) + lane * N;
-          const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.pool.v + off) + lane * N;
-          float score = 0.f;
+        while (again != 0) {
+          float q[kR][N], o[kR][N];
+          int from[kR];
+          int my_a = 0, my_z = 0;  // of row lane % kR
+          float my_ref = 0.f;
 #pragma unroll
-          for (int d = 0; d < N; ++d) score = fmaf(q[d], __bfloat162float(kk[d]), score);
+          for (int r = 0; r < kR; ++r) {
+            const bool there = again != 0;
+            from[r] = there ? __ffs(again) - 1 : 0;
+            again &= again - 1;
+            const int t = __shfl_sync(0xffffffffu, t_row, from[r]), h = __shfl_sync(0xffffffffu, h_row, from[r]);
+            const __nv_bfloat16* q_row = reinterpret_cast<const __nv_bfloat16*>(p.q + (int64_t)t * p.q_token + h * p.q_head);
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) score += __shfl_xor_sync(0xffffffffu, score, d);
-          const float w = ex2_approx(fmaf(score, c, -r_ref));
+            for (int d = 0; d < N; ++d) {
+              q[r][d] = there ? __bfloat162float(q_row[lane * N + d]) : 0.f;
+              o[r][d] = 0.f;
+            }
+            const int ra = __shfl_sync(0xffffffffu, a, from[r]), rz = __shfl_sync(0xffffffffu, z, from[r]);
+            const float rr = __shfl_sync(0xffffffffu, r_ref, from[r]);
+            if ((lane & (kR - 1)) == r && there) {
+              my_a = ra;
+              my_z = rz;
+              my_ref = rr;
+            }
+            if (!there) from[r] = -1;
+          }
+          // keys that some of the rows sees
+          const int a_all = __reduce_min_sync(0xffffffffu, my_a < my_z ? my_a : INT32_MAX);
+          const int z_all = __reduce_max_sync(0xffffffffu, my_a < my_z ? my_z : 0);
+#pragma unroll 1
+          for (int k0 = a_all; k0 < z_all; k0 += 32) {
+            if (lane == 0) atomicAdd(&sh.watch.beat, 1);
+            // where this lane's key of 32 stands, -1: nowhere (a page out of range has been reported)
+            int64_t place = -1;
+            if (k0 + lane < z_all) {
+              const int key = k0 + lane;
+              const int page = __ldcg(p.block_table + (int64_t)x.b * p.max_pages + (key >> shift));
+              if (page >= 0 && page < p.pool.n_pages)
+                place = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride +
+                        (int64_t)(key & ((1 << shift) - 1)) * p.pool.token_stride;
+            }
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32 && k0 + j0 < z_all; j0 += kK) {
+              uint32_t kk[kK][N / 2], vv[kK][N / 2];
 #pragma unroll
-          for (int d = 0; d < N; ++d) o[d] = fmaf(w, __bfloat162float(vv[d]), o[d]);
-        }
+              for (int j = 0; j < kK; ++j) {
+                const int64_t off = __shfl_sync(0xffffffffu, (long long)place, j0 + j);
+                load_words(kk[j], p.pool.k + off + lane * (2 * N), off >= 0);
+                load_words(vv[j], p.pool.v + off + lane * (2 * N), off >= 0);
+              }
+              float w[32];  // [key][row]
 #pragma unroll
-        for (int d = 0; d < N; ++d) {
-          if (x.whole)
-            reinterpret_cast<__nv_bfloat16*>(dst)[lane * N + d] = __float2bfloat16_rn(o[d] * r_f);
-          else
-            reinterpret_cast<float*>(dst)[lane * N + d] = o[d];
+              for (int j = 0; j < kK; ++j)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                  w[j * kR + r] = 0.f;
+#pragma unroll
+                  for (int d = 0; d < N / 2; ++d)
+                    w[j * kR + r] = fmaf(q[r][2 * d], __uint_as_float(kk[j][d] << 16),
+                                         fmaf(q[r][2 * d + 1], __uint_as_float(kk[j][d] & 0xffff0000u), w[j * kR + r]));
+                }
+              // 32 sums over the lanes, that of [i] to lane i
+#pragma unroll
+              for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int i = 0; i < d; ++i) {
+                  const bool upper = lane & d;
+                  const float other = __shfl_xor_sync(0xffffffffu, upper ? w[i] : w[i + d], d);
+                  w[i] = (upper ? w[i + d] : w[i]) + other;
+                }
+              const int key = k0 + j0 + lane / kR;
+              const bool seen = __shfl_sync(0xffffffffu, place >= 0, j0 + lane / kR) && key >= my_a && key < my_z;
+              const float mine = seen ? ex2_approx(fmaf(w[0], c, -my_ref)) : -1.f;
+#pragma unroll
+              for (int j = 0; j < kK; ++j)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                  const float f = __shfl_sync(0xffffffffu, mine, j * kR + r);
+                  if (f >= 0.f)
+#pragma unroll
+                    for (int d = 0; d < N / 2; ++d) {
+                      o[r][2 * d] = fmaf(f, __uint_as_float(vv[j][d] << 16), o[r][2 * d]);
+                      o[r][2 * d + 1] = fmaf(f, __uint_as_float(vv[j][d] & 0xffff0000u), o[r][2 * d + 1]);
+                    }
+                }
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            if (from[r] < 0) continue;
+            const float f = __shfl_sync(0xffffffffu, r_f, from[r]);
+            char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from[r]));
+#pragma unroll
+            for (int d = 0; d < N; ++d) {
+              if (x.whole)
+                reinterpret_cast<__nv_bfloat16*>(to)[lane * N + d] = __float2bfloat16_rn(o[r][d] * f);
+              else
+                reinterpret_cast<float*>(to)[lane * N + d] = o[r][d];
+            }
+          }
         }
       };
       const uint32_t last_tile = list_tiles - 1;
@@ -860,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) sh.quarter[s][quarter][lane] = make_float2(ref, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.merged[s]);
-        ok = wait_bar(&sh.merged[s], (np - 1) & 1, abort_flag);
+        ok = wait_bar(&sh.merged[s], (np - 1) & 1, watch);
         if (!ok) break;
 #pragma unroll 1
         for (int r0 = quarter * kAtOnce; r0 < x.rows; r0 += 4 * kAtOnce) {
@@ -901,17 +1005,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (also where a row sees all of the unit's keys: the other quarters' zeros
           // have met the values that are not finite)
           const float probe = fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, y.w * 0.f)));
-          uint32_t again = __ballot_sync(0xffffffffu, there && probe != probe && r_l == r_l);
-          __syncwarp();
-#pragma unroll 1
-          while (again != 0) {
-            const int from = __ffs(again) - 1, k = from / kChunks;
-            again &= kChunks == 32 ? 0u : ~(0xffffu << (16 * k));
-            const int tok_k = p.by_group.quotient(r0 + k), pos_k = x.pos + tok_k;
-            const int z = p.causal ? min(pos_k + 1, x.kv) : x.kv, a = p.window > 0 ? max(0, pos_k - p.window + 1) : 0;
-            anew(x.token + tok_k, x.h * p.group + r0 + k - tok_k * p.group,
-                 reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from)),
-                 max(key0, a), min(key1, z), __shfl_sync(0xffffffffu, r_ref, from), __shfl_sync(0xffffffffu, r_f, from));
+          const uint32_t bad = __ballot_sync(0xffffffffu, there && probe != probe && r_l == r_l);
+          if (bad != 0) {
+            const int r_pos = x.pos + tok, z = p.causal ? min(r_pos + 1, x.kv) : x.kv;
+            const int a = p.window > 0 ? max(0, r_pos - p.window + 1) : 0;
+            // (a bit a row: its first lane's)
+            const uint32_t again = kChunks == 32 ? 1u : ((bad & 0xffffu) != 0 ? 1u : 0u) | (bad >> 16 != 0 ? 0x10000u : 0u);
+            anew(again, (int)r_t, r_head, dst, max(key0, a), min(key1, z), r_ref, r_f);
           }
         }
         fence_proxy_async_smem();  // the slot's next filling comes by TMA
@@ -969,16 +1069,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float2 probes = unpack2(probe2);
         const float probe = probes.x + probes.y;
-        uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
-#pragma unroll 1
-        while (again != 0) {
-          const int r = __ffs(again) - 1;
-          again &= again - 1;
-          char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
-          const int t_row = __shfl_sync(0xffffffffu, (int)t_out, r), h_row = __shfl_sync(0xffffffffu, head, r);
-          anew(t_row, h_row, dst, max(key0, __shfl_sync(0xffffffffu, lo, r)), min(key1, __shfl_sync(0xffffffffu, hi, r)),
-               __shfl_sync(0xffffffffu, ref, r), __shfl_sync(0xffffffffu, f, r));
-        }
+        const uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
+        if (again != 0) anew(again, (int)t_out, head, to, max(key0, lo), min(key1, hi), ref, f);
         if (valid) {
           if (!x.whole)
             part.stat[prow] = make_float2(ref, l);
@@ -1002,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Each load has been waited for by an issuer, except after an abort: then wait
   // (with a limit) until nothing can be in flight when the CTA exits.
-  if (*abort_flag) {
+  if (watch->abort) {
     if (tid == 0) report(p.status, kErrTimeout);
     for (int i = 0; i < 64; ++i) __nanosleep(20000);
   }

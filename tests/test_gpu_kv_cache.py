@@ -242,6 +242,49 @@ def check_unseen_values(kv, dtype, D, G, window, what, lens):
             row += 1
 
 
+@pytest.mark.parametrize("G,n_q,B", [(3, 70, 304), (4, 8, 608), (4, 4, 608)])
+def test_attention_waits_for_a_long_recomputation(kv, G, n_q, B):
+    """A NaN in the last new token's value and two whole units of 100,000 keys for every share: up to 32 rows a warp are
+    computed again over 100,000 keys while the next unit waits (seconds, if a key and a row at a time). All requests
+    hold the same pages. Values grow along the context, so that keys left out or counted twice show."""
+    n, S, D = 100000, 256, 64
+    g = torch.Generator(device="cuda").manual_seed(G)
+    pages = ref.ceil_div(n, S)
+    k = torch.randn((1, pages, S, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    ramp = torch.arange(pages * S, device="cuda").view(1, pages, S, 1, 1) / n
+    v = (torch.rand(k.shape, device="cuda", generator=g) + 3 * ramp).to(torch.bfloat16)
+    q = torch.randn((B * n_q, G, D), device="cuda", generator=g).to(torch.bfloat16)
+    pool, status = kv.KvPool(k, v), torch.zeros(4, dtype=torch.int32, device="cuda")
+    table, q_start = _i32(np.tile(np.arange(pages), (B, 1))), _i32(np.arange(B + 1) * n_q)
+    ws = torch.empty(kv.ds_paged_attention_workspace_bytes(pool, G), dtype=torch.uint8, device="cuda")
+
+    def call():
+        out, lse = torch.full_like(q, 7.0), torch.full((B * n_q, G), 7.0, device="cuda")
+        kv.check(kv.ds_paged_attention(pool, 0, q, q_start, n_q, table, _i32([n] * B), out, ws, status, lse=lse))
+        assert int(status[0]) == 0
+        return out.float().view(B, n_q, G, D), lse
+
+    clean, lse = call()
+    last = divmod(n - 1, S)
+    v[0, last[0], last[1], 0, 3] = float("nan")
+    got, lse_got = call()
+    assert torch.equal(lse, lse_got)
+    assert got[:, -1, :, 3].isnan().all()
+    got[:, -1, :, 3] = clean[:, -1, :, 3]
+    # Values are positive, so both are within their bound of the exact sum relative to themselves: J + 32 roundings of
+    # float32 and, at most, two of bfloat16 (and a quarter); scores of size 5 add (D + 4) 5 * 2^-24 twice.
+    bound = 2 * ((n + 32 + 10 * (D + 4)) * ref.U32 + 2.5 * ref.UBF)
+    assert ((got - clean).abs() <= bound * clean).all()
+    # float64, a few requests
+    kk, vv = (x[0].reshape(-1, D)[:n].double() for x in (k, v))
+    vv[-1, 3] = 0
+    for b in (0, B // 2, B - 1):
+        s = torch.einsum("igd,jd->igj", q[b * n_q:(b + 1) * n_q].double(), kk) * D ** -0.5
+        s = s.masked_fill((torch.arange(n, device="cuda") > torch.arange(n - n_q, n, device="cuda")[:, None])[:, None], -np.inf)
+        want = torch.softmax(s, -1) @ vv
+        assert ((got[b][:-1] - want[:-1]).abs() <= bound / 2 * want[:-1]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_strided_rows_and_scale(kv, dtype):
     x = Batch(dtype, 128, 16, 2, 4, [(5, 90), (1, 300), (40, 41)], strided=True, seed=6)
