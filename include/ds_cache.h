@@ -16,7 +16,8 @@
  * anything is launched, conditions only the device can see go to `status`
  * (first error wins), no call synchronises, allocates or keeps a pointer, and
  * every call can be captured into a CUDA graph. Pointers are 16-byte aligned
- * unless a field says otherwise. Strides are in elements.
+ * unless a field says otherwise. Strides are in elements. Calls launch on the
+ * current device, where the buffers have to be.
  *
  * One cycle with a cache:
  *   ds_cache_update  (new_len = kv_len + n)      pages for the n new tokens

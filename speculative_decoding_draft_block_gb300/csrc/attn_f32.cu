@@ -534,10 +534,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
 
 // A form of the kernel with its shared memory, and the join of its cut units.
 template <int D, int kBM>
-cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParams), size_t smem, cudaError_t ready) {
+cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParams), size_t smem, Readiness& readiness) {
   using F = Form32<kBM>;
-  if (ready != cudaSuccess) return ready;
-  const cudaError_t e = launch_early(kernel, dim3(F::kShares), dim3(kThreads), smem, s, p);
+  cudaError_t e = readiness.get(
+      [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
+  if (e != cudaSuccess) return e;
+  e = launch_early(kernel, dim3(F::kShares), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)p.max_q * p.group;
   return launch_join<F, D, float>(p, s, (int)(most < kBM ? most : kBM), kBM, kBM);
@@ -545,18 +547,14 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParam
 
 template <int D, int kR>
 cudaError_t launch_few(const AttnParams& p, cudaStream_t s) {
-  constexpr size_t smem = sizeof(FewTiles<D, kR>);
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(attn_f32_few_kernel<D, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return launch<D, kR>(p, s, attn_f32_few_kernel<D, kR>, smem, ready);
+  static Readiness readiness;
+  return launch<D, kR>(p, s, attn_f32_few_kernel<D, kR>, sizeof(FewTiles<D, kR>), readiness);
 }
 
 template <int D, int kBM>
 cudaError_t launch_tiles(const AttnParams& p, cudaStream_t s) {
-  constexpr size_t smem = sizeof(Tiles<D, kBM>);
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(attn_f32_kernel<D, kBM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return launch<D, kBM>(p, s, attn_f32_kernel<D, kBM>, smem, ready);
+  static Readiness readiness;
+  return launch<D, kBM>(p, s, attn_f32_kernel<D, kBM>, sizeof(Tiles<D, kBM>), readiness);
 }
 
 // Measured on 64 requests of one token over 500 to 4000 cached, 8 KV heads (D = 128:

@@ -59,9 +59,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <atomic>
-#include <mutex>
-
 #include "attn_work.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -1118,7 +1115,8 @@ cudaError_t prepare_kernel() {
 
 template <int D, int kForm>
 cudaError_t launch(const AttnParams& p, cudaStream_t s) {
-  static const cudaError_t ready = prepare_kernel<D, kForm>();
+  static Readiness readiness;
+  const cudaError_t ready = readiness.get(prepare_kernel<D, kForm>);
   if (ready != cudaSuccess) return ready;
   CUtensorMap mq, mk, mv;
   const int per_tile = (kForm == kFew ? kFewRows : kTile) / p.group;

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ds_cache.h"
 
 namespace ds {
@@ -129,6 +131,27 @@ cudaError_t launch_early(void (*kernel)(A...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// What a kernel needs once on each device before its first launch there (a function's
+// attributes hold for the device that was current when they were set). Two threads
+// may both do it.
+struct Readiness {
+  static constexpr int kDevices = 64;
+  std::atomic<int> state[kDevices];  // 0: not yet, else 1 + the preparation's result
+  template <class F>
+  cudaError_t get(F prepare) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    int s = state[dev].load(std::memory_order_acquire);
+    if (s == 0) {
+      s = 1 + (int)prepare();
+      state[dev].store(s, std::memory_order_release);
+    }
+    return (cudaError_t)(s - 1);
+  }
+};
 
 constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are built for
 

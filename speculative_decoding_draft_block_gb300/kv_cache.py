@@ -106,17 +106,21 @@ def _entry(name):
     return _entries[name]
 
 
-def _words(t, name, n=None, _int32=torch.int32):
-    """Device address of a contiguous int32 tensor (of n elements, if given)."""
-    if t.dtype is _int32 and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n):
+def _words(t, name, device=None, n=None, _int32=torch.int32):
+    """Device address of a contiguous int32 tensor on CUDA device `device` (of n elements, if given)."""
+    if t.dtype is _int32 and t.get_device() == device and t.is_contiguous() and (n is None or t.numel() == n):
         return t.data_ptr()
     if t.dtype is not _int32:
         raise ValueError("%s must be int32" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    _on_device(t, name, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     raise ValueError("%s must have %d elements" % (name, n))
+
+
+def _on_device(t, name, device):
+    if t.get_device() != device:
+        raise ValueError("%s must be a CUDA tensor on the pool's device (cuda:%s)" % (name, device))
 
 
 def _rows(t, name, pool, shape, heads=None):
@@ -124,8 +128,8 @@ def _rows(t, name, pool, shape, heads=None):
     `shape`) of the pool's dtype."""
     if t.dtype is not pool.dtype:
         raise ValueError("%s must have the pool's dtype" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != pool.device_index:
+        _on_device(t, name, pool.device_index)
     if len(shape) != 3 or shape[2] != pool.head_dim or (heads is not None and shape[1] != heads):
         raise ValueError("%s must be [T, heads, head_dim]" % name)
     ts, hs, one = t.stride()
@@ -139,9 +143,8 @@ def _rows(t, name, pool, shape, heads=None):
     return t.data_ptr(), ts, hs
 
 
-def _bytes(t, name):
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+def _bytes(t, name, device):
+    _on_device(t, name, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr(), t.numel() * t.element_size()
@@ -149,7 +152,11 @@ def _bytes(t, name):
 
 def _stream(stream, pool):
     """The stream's handle; the current one of the pool's device by default (asked for
-    without building a Stream object, which takes as long as the launches)."""
+    without building a Stream object, which takes as long as the launches). Launches go to
+    the current device, which has to be the pool's."""
+    if torch._C._cuda_getDevice() != pool.device_index:
+        raise ValueError("the pool is on cuda:%d, the current device is cuda:%d" %
+                         (pool.device_index, torch._C._cuda_getDevice()))
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(pool.device_index)
     return _lib._stream(stream)
@@ -187,14 +194,15 @@ class KvPool:
 def ds_cache_append(pool, layer, k_new, v_new, q_start, block_table, kv_len, status, stream=None):
     """New keys and values [T, n_kv_heads, head_dim] into their pages."""
     B, M = block_table.shape
+    dev = pool.device_index
     shape = k_new.shape
     k, kt, kh = _rows(k_new, "k_new", pool, shape, pool.n_kv_heads)
     v, vt, vh = _rows(v_new, "v_new", pool, v_new.shape, pool.n_kv_heads)
     if v_new.shape != shape:
         raise ValueError("k_new and v_new must have one shape")
     a = pool.packed + _pack_append(layer, B, shape[0], M, k, v, kt, kh, vt, vh,
-                   _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
-                   _words(kv_len, "kv_len", B), _words(status, "status"))
+                   _words(q_start, "q_start", dev, B + 1), _words(block_table, "block_table", dev),
+                   _words(kv_len, "kv_len", dev, B), _words(status, "status", dev))
     return _entry("ds_cache_append")(a, _stream(stream, pool))
 
 
@@ -210,6 +218,7 @@ def ds_paged_attention(pool, layer, q, q_start, max_q, block_table, kv_len, out,
     """Attention of ragged rows q [T, n_heads, head_dim] over the cache; `scale`
     defaults to 1 / sqrt(head_dim). Writes out and, if given, lse [T, n_heads] float32."""
     B, M = block_table.shape
+    dev = pool.device_index
     shape = q.shape
     qp, qt, qh = _rows(q, "q", pool, shape)
     T, H = shape[0], shape[1]
@@ -218,14 +227,14 @@ def ds_paged_attention(pool, layer, q, q_start, max_q, block_table, kv_len, out,
         raise ValueError("out must have q's shape")
     lp = 0
     if lse is not None:
-        if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.numel() != T * H:
-            raise ValueError("lse must be a contiguous float32 CUDA tensor [T, n_heads]")
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.numel() != T * H:
+            raise ValueError("lse must be a contiguous float32 tensor [T, n_heads] on the pool's device")
         lp = lse.data_ptr()
-    wp, wn = _bytes(workspace, "workspace")
+    wp, wn = _bytes(workspace, "workspace", dev)
     a = pool.packed + _pack_attention(layer, B, T, M, max_q, H, 1 if causal else 0, window,
                       1.0 / math.sqrt(pool.head_dim) if scale is None else scale, qp, qt, qh,
-                      _words(q_start, "q_start", B + 1), _words(block_table, "block_table"),
-                      _words(kv_len, "kv_len", B), op, ot, oh, lp, wp, wn, _words(status, "status"))
+                      _words(q_start, "q_start", dev, B + 1), _words(block_table, "block_table", dev),
+                      _words(kv_len, "kv_len", dev, B), op, ot, oh, lp, wp, wn, _words(status, "status", dev))
     return _entry("ds_paged_attention")(a, _stream(stream, pool))
 
 
@@ -237,13 +246,14 @@ def ds_cache_update(pool, block_table, kv_len, ref, new_len, table_out, len_out,
                     parent=None, stream=None):
     """Every request's next state (out of place): see include/ds_cache.h."""
     B, M = block_table.shape
+    dev = pool.device_index
     N = pool.n_pages
-    wp, wn = _bytes(workspace, "workspace")
-    a = pool.packed + _pack_update(B, M, _words(block_table, "block_table"), _words(kv_len, "kv_len", B),
-                   _words(ref, "ref", N), 0 if parent is None else _words(parent, "parent", B),
-                   _words(new_len, "new_len", B), _words(table_out, "table_out", B * M),
-                   _words(len_out, "len_out", B), _words(ref_out, "ref_out", N), wp, wn,
-                   _words(status, "status"))
+    wp, wn = _bytes(workspace, "workspace", dev)
+    a = pool.packed + _pack_update(B, M, _words(block_table, "block_table", dev), _words(kv_len, "kv_len", dev, B),
+                   _words(ref, "ref", dev, N), 0 if parent is None else _words(parent, "parent", dev, B),
+                   _words(new_len, "new_len", dev, B), _words(table_out, "table_out", dev, B * M),
+                   _words(len_out, "len_out", dev, B), _words(ref_out, "ref_out", dev, N), wp, wn,
+                   _words(status, "status", dev))
     return _entry("ds_cache_update")(a, _stream(stream, pool))
 
 
@@ -254,11 +264,12 @@ def ds_cache_compact_workspace_bytes(n_pages):
 def ds_cache_compact(pool, block_table, ref, table_out, ref_out, page_map, n_used, workspace, status, stream=None):
     """Held pages to the front of the pool (state out of place, pages in place)."""
     B, M = block_table.shape
+    dev = pool.device_index
     N = pool.n_pages
-    wp, wn = _bytes(workspace, "workspace")
-    a = pool.packed + _pack_compact(B, M, _words(block_table, "block_table"), _words(ref, "ref", N),
-                    _words(table_out, "table_out", B * M), _words(ref_out, "ref_out", N),
-                    _words(page_map, "page_map", N), _words(n_used, "n_used", 1), wp, wn, _words(status, "status"))
+    wp, wn = _bytes(workspace, "workspace", dev)
+    a = pool.packed + _pack_compact(B, M, _words(block_table, "block_table", dev), _words(ref, "ref", dev, N),
+                    _words(table_out, "table_out", dev, B * M), _words(ref_out, "ref_out", dev, N),
+                    _words(page_map, "page_map", dev, N), _words(n_used, "n_used", dev, 1), wp, wn, _words(status, "status", dev))
     return _entry("ds_cache_compact")(a, _stream(stream, pool))
 
 

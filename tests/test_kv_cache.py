@@ -159,6 +159,67 @@ def test_binding_refuses_what_is_no_device_tensor(kv):
         kv._words(torch.zeros(3), "lengths")                  # not int32
 
 
+class _Tensor:
+    """What the binding asks of a tensor, on a device of choice (its address is never read)."""
+    is_cuda = True
+
+    def __init__(self, torch, shape, dtype, device):
+        self.meta, self.dtype, self.shape, self.device_index = torch.empty(shape, device="meta"), dtype, torch.Size(shape), device
+
+    def __getattr__(self, name):
+        return getattr(self.meta, name)
+
+    def get_device(self):
+        return self.device_index
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_binding_refuses_other_devices(kv, monkeypatch):
+    """A pool beside the current device, or an argument beside the pool's device, is refused before anything is called."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    B, M, N, T, H, Hk, D = 2, 3, 8, 5, 4, 2, 64
+
+    def calls(pool_device, odd=None):
+        def t(name, shape, dtype=torch.int32):
+            return _Tensor(torch, shape, dtype, 1 - pool_device if name == odd else pool_device)
+
+        pool = SimpleNamespace(packed=bytes(kv.ctypes.sizeof(kv.PoolDesc)), device_index=pool_device, dtype=torch.bfloat16, n_pages=N,
+                               n_kv_heads=Hk, head_dim=D)
+        bf = torch.bfloat16
+        w = dict(q_start=t("q_start", (B + 1,)), block_table=t("block_table", (B, M)), kv_len=t("kv_len", (B,)))
+        status, ws = t("status", (4,)), t("workspace", (64,), torch.uint8)
+        table_out, ref = t("table_out", (B, M)), t("ref", (N,))
+        return {"append": lambda: kv.ds_cache_append(pool, 0, t("k_new", (T, Hk, D), bf), t("v_new", (T, Hk, D), bf), status=status, **w),
+                "attention": lambda: kv.ds_paged_attention(pool, 0, t("q", (T, H, D), bf), max_q=3, out=t("out", (T, H, D), bf), status=status,
+                                                           workspace=ws, lse=t("lse", (T, H), torch.float32), **w),
+                "update": lambda: kv.ds_cache_update(pool, w["block_table"], w["kv_len"], ref, t("new_len", (B,)), table_out,
+                                                     t("len_out", (B,)), t("ref_out", (N,)), ws, status, parent=t("parent", (B,))),
+                "compact": lambda: kv.ds_cache_compact(pool, w["block_table"], ref, table_out, t("ref_out", (N,)), t("page_map", (N,)),
+                                                       t("n_used", (1,)), ws, status)}
+
+    called = []
+    monkeypatch.setattr(kv, "_entry", lambda name: lambda args, stream: called.append(name) or 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    for f in calls(0).values():
+        assert f() == 0
+    assert len(called) == 4
+    for f in calls(1).values():                                # the pool is on another device than the current one
+        with pytest.raises(ValueError, match="current device"):
+            f()
+    odd = {"append": ("k_new", "v_new"), "attention": ("q", "out", "lse", "workspace"),
+           "update": ("new_len", "parent", "table_out", "len_out", "ref", "ref_out", "workspace"),
+           "compact": ("ref", "table_out", "ref_out", "page_map", "n_used", "workspace")}
+    for call, names in odd.items():
+        for name in names + ("block_table", "status") + (("q_start", "kv_len") if call in ("append", "attention") else ()):
+            with pytest.raises(ValueError, match=name):
+                calls(0, name)[call]()
+    assert len(called) == 4
+
+
 def test_plain_forms_agree_with_hand_made_states():
     """The tests' own reference on states small enough to check by hand."""
     import _kv_ref as ref
