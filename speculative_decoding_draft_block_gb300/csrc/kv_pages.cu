@@ -232,16 +232,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
   cl.sync();
 
-  // holders afterwards: a warp a request, only the entries that change
+  // holders afterwards: a warp a request. Of the pages that a request keeps from itself no
+  // count changes, but they have to be pages.
   for (int b = b0 + (tid >> 5); b < b1; b += kPlanWarps) {
     const Move m = move_of(b);
     if (!m.ok) continue;
     const int32_t* now = p.table + (int64_t)b * p.max_pages;
     const int32_t* past = p.table + (int64_t)max(m.parent, 0) * p.max_pages;
-    const int from = m.parent == b ? m.kept : 0;
-    const int to = max(m.old, m.kept);
-    constexpr int kAhead = 8;  // entries in flight a lane: a long row is one or two round trips
-    for (int j0 = from + lane; j0 < to; j0 += 32 * kAhead) {
+    const bool same = m.parent == b;
+    constexpr int kAlone = 16;  // entries in flight a lane: a long row is one or two round trips
+    for (int j0 = lane; same && j0 < m.old; j0 += 32 * kAlone) {
+      int o[kAlone];
+#pragma unroll
+      for (int i = 0; i < kAlone; ++i) o[i] = j0 + 32 * i < m.old ? __ldcg(now + j0 + 32 * i) : 0;
+#pragma unroll
+      for (int i = 0; i < kAlone; ++i) {
+        const int j = j0 + 32 * i;
+        if (o[i] < 0 || o[i] >= N)
+          bad = 1;
+        else if (j >= m.kept && j < m.old)
+          atomicSub(w.count + o[i], 1);
+      }
+    }
+    const int to = same ? 0 : max(m.old, m.kept);
+    constexpr int kAhead = 8;
+    for (int j0 = lane; j0 < to; j0 += 32 * kAhead) {
       int o[kAhead], h[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {

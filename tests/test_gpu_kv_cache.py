@@ -565,6 +565,45 @@ def test_update_refuses_bad_state_and_changes_nothing(kv):
             assert all(torch.equal(a, b) for a, b in zip(state, out)), change
 
 
+@pytest.mark.parametrize("B,own", [(1, False), (16, True), (40, False), (300, True), (300, False)])
+def test_update_refuses_bad_pages_that_stay(kv, B, own):
+    """A table entry that is no page, anywhere in what a request keeps from itself, whether it grows, stays, falls back or
+    (its pages being given back) ends: the state out is the state in."""
+    S, M = 16, 40
+    N = B * M
+    rng = np.random.RandomState(B)
+    k = torch.zeros((1, N, S, 1, 8), device="cuda")
+    pool = kv.KvPool(k, k.clone())
+    ws = torch.empty(kv.ds_cache_update_workspace_bytes(B, N), dtype=torch.uint8, device="cuda")
+    full = rng.permutation(N).reshape(B, M)
+    lens = rng.randint(1, M * S, size=B)
+    held = np.zeros(N, dtype=np.int32)
+    for b in range(B):
+        full[b, ref.ceil_div(int(lens[b]), S):] = -1
+    held[full[full >= 0]] = 1
+    parent = _i32(np.arange(B)) if own else None
+
+    def update(table, new):
+        state = _i32(table), _i32(lens), _i32(held)
+        out = tuple(torch.full_like(x, -77) for x in state)
+        status = torch.zeros(4, dtype=torch.int32, device="cuda")
+        kv.check(kv.ds_cache_update(pool, *state, _i32(new), *out, ws, status, parent=parent))
+        return state, out, int(status[0])
+
+    for i in range(12):
+        b = int(rng.choice([0, B - 1, rng.randint(B)]))
+        new = np.minimum(M * S, lens + rng.randint(0, 3, size=B))
+        new[b] = [new[b], lens[b], max(0, lens[b] - 20), 0][i % 4]
+        _, out, code = update(full, new)
+        assert code == 0 and out[1].tolist() == new.tolist()
+        last = ref.ceil_div(int(lens[b]), S) - 1
+        table = full.copy()
+        table[b, int(rng.choice([0, last, rng.randint(last + 1)]))] = [N, -1, 1 << 30][i % 3]
+        state, out, code = update(table, new)
+        assert code == 6, (i, b)
+        assert all(torch.equal(x, y) for x, y in zip(state, out)), (i, b)
+
+
 @pytest.mark.parametrize("N,B,held", [(1, 1, 1.0), (5, 2, 0.0), (64, 3, 0.5), (1000, 9, 0.9), (20000, 40, 0.3), (4099, 7, 1.0)])
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])
 def test_compact_against_the_plain_form(kv, N, B, held, layout):
