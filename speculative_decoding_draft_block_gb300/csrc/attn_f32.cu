@@ -20,7 +20,7 @@ namespace ds {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeyTile = 64;
+constexpr int kKeyTile = kAttnTileF32;
 
 template <int kBM>
 struct Form32 : WorkForm<kKeyTile, kMaxShares, kBM> {};

@@ -69,7 +69,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384;
-constexpr int kTile = 128;         // keys a tile, rows a tile
+constexpr int kTile = kAttnTileTc;  // keys a tile, rows a tile
 constexpr int kFewRows = 16;       // rows of a unit in the form for few rows
 constexpr float kSlack = 8.f;      // growth of the exponents that is left in the sums
 constexpr uint32_t kCtrlRegs = 88, kSoftRegs = 208, kLaunchRegs = 168;

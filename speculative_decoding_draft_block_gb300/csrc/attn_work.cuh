@@ -19,9 +19,7 @@
 namespace ds {
 namespace {
 
-// Set-up of a unit, in key tiles (0, 2 and 3 are slower where units of a few tiles stand
-// beside longer ones).
-constexpr int kUnitCost = 1;
+constexpr int kUnitCost = kAttnUnitCost;  // of a unit's set-up, in key tiles
 
 template <int kTileKeys, int kShareCount, int kPartialRows>
 struct WorkForm {
@@ -151,7 +149,7 @@ struct Walk {
         continue;
       }
       const Unit y = make_unit<F>(p, r, u, unit_rows);
-      // (at most 2^23 + 1 tiles and 256 heads: 32 bits)
+      // (fits: work_fits)
       const uint32_t w = y.n + kUnitCost, all = w * p.pool.n_kv_heads;
       if (at >= base + all) {
         base += all;

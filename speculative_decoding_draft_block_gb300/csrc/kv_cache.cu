@@ -221,6 +221,7 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   if (a->max_q < 1 || a->n_heads < 1 || a->n_heads % a->pool.n_kv_heads != 0 ||
       a->n_heads / a->pool.n_kv_heads > 128)
     return DS_ERR_INVALID_ARG;
+  if (!work_fits(a->pool.dtype, (int64_t)a->max_pages * a->pool.page_size, a->pool.n_kv_heads)) return DS_ERR_UNSUPPORTED;
   if ((a->causal != 0 && a->causal != 1) || a->window < 0 || !isfinite(a->scale) ||
       !(a->scale > 0.f))
     return DS_ERR_INVALID_ARG;

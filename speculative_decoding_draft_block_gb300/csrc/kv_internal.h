@@ -153,6 +153,18 @@ struct Readiness {
   }
 };
 
+// The attention's key tiles, and the set-up of a unit of its work in tiles (0, 2 and 3
+// are slower where units of a few tiles stand beside longer ones).
+constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1;
+
+// Whether the work of one block of rows, over all KV heads, can be counted in 32 bits: with
+// tiles of 128 keys always (2^23 + 1 tiles, 256 heads), with tiles of 64 except for 256
+// heads over 2^30 tokens.
+inline bool work_fits(int32_t dtype, int64_t tokens, int32_t n_kv_heads) {
+  const int64_t tile = dtype == DS_BF16 ? kAttnTileTc : kAttnTileF32;
+  return ((tokens + tile - 1) / tile + kAttnUnitCost) * n_kv_heads <= (int64_t)UINT32_MAX;
+}
+
 constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are built for
 
 size_t update_ws_bytes(int32_t B, int32_t n_pages);

@@ -106,6 +106,17 @@ def test_attention_head_dims(kv):
     assert lib.ds_paged_attention(ctypes.byref(_attend(kv, T=0, q=None, out=None)), None) == 0
 
 
+def test_attention_work_that_passes_32_bits(kv):
+    """Tiles of a block of rows times KV heads: 2^24 + 1 tiles of 64 keys and 256 heads are 2^32 + 256. (No rows: what
+    is not refused launches nothing.)"""
+    call = kv.load().ds_paged_attention
+    for dtype, heads, tokens, code in ((0, 256, 1 << 30, UNSUPPORTED), (0, 255, 1 << 30, 0), (0, 256, (1 << 30) - 128, 0),
+                                       (0, 256, (1 << 30) - 16, UNSUPPORTED), (1, 256, 1 << 30, 0)):
+        pool = _pool(kv, dtype=dtype, n_kv_heads=heads, head_dim=64)
+        args = _attend(kv, pool, n_heads=heads, max_pages=tokens // 16, T=0, q=None, out=None)
+        assert call(ctypes.byref(args), None) == code, (dtype, heads, tokens)
+
+
 @pytest.mark.parametrize("bad", [dict(layer=2), dict(B=0), dict(T=-1), dict(max_pages=0), dict(k_new=None), dict(v_new=FAKE + 4),
                                  dict(k_token_stride=129), dict(v_head_stride=0), dict(q_start=None), dict(block_table=None),
                                  dict(kv_len=FAKE + 8), dict(status=None)], ids=str)
