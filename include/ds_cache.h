@@ -40,7 +40,7 @@ extern "C" {
  * strides (the same for K and V), so tokens or heads may be outermost in a
  * page and K and V may be interleaved.
  *   page_size   16, 32, 64, 128 or 256 tokens
- *   n_pages     1..2^28, n_layers >= 1
+ *   n_pages     1..2^28, n_layers 1..2^28
  *   head_dim    a multiple of 8, at most 256 (ds_paged_attention: 64 or 128)
  *   n_kv_heads  1..256
  *   strides     multiples of 16 bytes, >= head_dim (layer_stride is not read

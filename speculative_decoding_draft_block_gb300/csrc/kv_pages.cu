@@ -401,7 +401,7 @@ __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int s
 }
 
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
-  const int b = blockIdx.x, part = blockIdx.y;  // part: 2 * layer + (0: K, 1: V)
+  const int b = blockIdx.x;
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -410,15 +410,14 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
   const int4 row = __ldcg(w.row + b);
   const int parent = row.x, shared = row.y, want = row.z, start = row.w;
   if (fail) {
-    if (part == 0) {
+    if (blockIdx.y == 0) {
       for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
         p.table_out[(int64_t)b * p.max_pages + j] = __ldcg(p.table + (int64_t)b * p.max_pages + j);
       if (threadIdx.x == 0) p.len_out[b] = __ldcg(p.kv_len + b);
     }
     return;
   }
-  if (part > 0 && copy.x < 0) return;
-  if (part == 0) {
+  if (blockIdx.y == 0) {
     const int32_t* past = p.table + (int64_t)max(parent, 0) * p.max_pages;
     for (int j = threadIdx.x; j < p.max_pages; j += blockDim.x)
       p.table_out[(int64_t)b * p.max_pages + j] =
@@ -427,11 +426,13 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
       p.len_out[b] = __ldcg(p.new_len + b);
       if (copy.x >= 0) atomicSub(p.ref_out + copy.x, 1);
     }
-    if (copy.x < 0) return;
   }
+  if (copy.x < 0) return;
   const int dst = __ldcg(w.free_list + start);
-  char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
-  copy_tokens(p.pool, base, copy.x, dst, copy.y, threadIdx.x, blockDim.x);
+  for (int part = blockIdx.y; part < 2 * p.pool.n_layers; part += gridDim.y) {  // 2 * layer + (0: K, 1: V)
+    char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
+    copy_tokens(p.pool, base, copy.x, dst, copy.y, threadIdx.x, blockDim.x);
+  }
 }
 
 // ---- compact -------------------------------------------------------------------------------
@@ -586,7 +587,8 @@ cudaError_t launch_update(const UpdateParams& p, cudaStream_t s) {
                             ? launch_early(update_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, s, p)
                             : launch_early(update_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, s, p);
   if (e != cudaSuccess) return e;
-  return launch_early(update_apply_kernel, dim3(p.B, 2 * p.pool.n_layers), dim3(256), 0, s, p);
+  const int parts = 2 * p.pool.n_layers;  // (a grid's limit in y: 65535)
+  return launch_early(update_apply_kernel, dim3(p.B, parts < 65535 ? parts : 65535), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {

@@ -541,6 +541,31 @@ def test_update_copies_every_layout(kv):
         assert torch.equal(k, want_k) and torch.equal(v, want_v)
 
 
+@pytest.mark.parametrize("L", [1, 32767, 32768, 40000])
+def test_update_and_compact_of_many_layers(kv, L):
+    """More layers than a grid has rows of blocks: the copied page and the moved ones in every layer."""
+    N, S = 4, 16
+    k = torch.randn((L, N, S, 1, 8), device="cuda")
+    v = torch.randn((L, N, S, 1, 8), device="cuda")
+    want = [k.clone(), v.clone()]
+    pool, status = kv.KvPool(k, v), torch.zeros(4, dtype=torch.int32, device="cuda")
+    state = _i32([[2, -1], [2, -1]]), _i32([9, 9]), _i32([0, 0, 2, 1])
+    out = tuple(torch.empty_like(x) for x in state)
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    kv.check(kv.ds_cache_update(pool, *state, _i32([10, 11]), *out, ws, status))
+    assert int(status[0]) == 0 and out[0].tolist() == [[2, -1], [0, -1]] and out[2].tolist() == [1, 0, 1, 1]
+    for x, y in zip((k, v), want):
+        y[:, 0, :9] = y[:, 2, :9]
+        assert torch.equal(x, y)
+    page_map, n_used = _i32([0] * N), _i32([0])
+    moved = tuple(torch.empty_like(x) for x in (out[0], out[2]))
+    kv.check(kv.ds_cache_compact(pool, out[0], out[2], *moved, page_map, n_used, ws, status))
+    assert int(status[0]) == 0 and n_used.tolist() == [3] and page_map.tolist() == [0, -1, 2, 1]
+    for x, y in zip((k, v), want):
+        y[:, 1] = y[:, 3]
+        assert torch.equal(x, y)
+
+
 def test_update_refuses_bad_state_and_changes_nothing(kv):
     S, N, M, B = 16, 8, 3, 3
     k = torch.zeros((1, N, S, 1, 8), device="cuda")

@@ -106,6 +106,18 @@ def test_attention_head_dims(kv):
     assert lib.ds_paged_attention(ctypes.byref(_attend(kv, T=0, q=None, out=None)), None) == 0
 
 
+def test_layers_of_a_pool(kv):
+    """2^28 layers at most (twice their number is counted in 32 bits)."""
+    lib = kv.load()
+    for L, code in ((1 << 28, 0), ((1 << 28) + 1, INVALID), (2 ** 31 - 1, INVALID)):
+        pool = _pool(kv, n_layers=L)
+        assert lib.ds_cache_append(ctypes.byref(_append(kv, pool, T=0)), None) == code
+        assert lib.ds_paged_attention(ctypes.byref(_attend(kv, pool, T=0)), None) == code
+        if code:
+            assert lib.ds_cache_update(ctypes.byref(_update(kv, pool)), None) == code
+            assert lib.ds_cache_compact(ctypes.byref(_compact(kv, pool)), None) == code
+
+
 def test_attention_work_that_passes_32_bits(kv):
     """Tiles of a block of rows times KV heads: 2^24 + 1 tiles of 64 keys and 256 heads are 2^32 + 256. (No rows: what
     is not refused launches nothing.)"""
