@@ -278,7 +278,8 @@ class PagedCache:
 
     The state (block table, lengths, holders' counts) has two copies; `update`
     and `compact` write the one and make it current. Nothing synchronises; errors
-    the device finds are in `status` (`check_status` reads it)."""
+    the device finds are in `status` (`check_status` reads it). The calls share the
+    state and a workspace: what is issued on several streams the caller orders."""
 
     def __init__(self, n_layers, n_pages, page_size, n_kv_heads, head_dim, max_requests, max_len,
                  dtype=torch.bfloat16, device="cuda", heads_outside=False):
@@ -329,7 +330,12 @@ class PagedCache:
 
     def attend(self, layer, q, q_start, max_q, out=None, lse=None, causal=True, window=0, scale=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            if stream is None:
+                out = torch.empty_like(q)
+            else:   # of that stream's memory: blocks freed on the current one may still be in use there
+                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), q.device)
+                with torch.cuda.stream(s):
+                    out = torch.empty_like(q)
         check(ds_paged_attention(self.pool, layer, q, q_start, max_q, self.block_table, self.kv_len, out,
                                  self.workspace, self.status, lse=lse, causal=causal, window=window, scale=scale,
                                  stream=stream), "ds_paged_attention")

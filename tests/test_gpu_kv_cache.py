@@ -717,6 +717,31 @@ def test_cycles_of_a_paged_cache(kv, dtype):
     c.check_status()
 
 
+def test_attend_on_another_stream_has_that_streams_memory(kv):
+    """Without `out`, a call on another stream does not write into a block that the current stream has freed and may still read."""
+    H, Hk, D, n = 4, 2, 64, 50
+    g = torch.Generator(device="cuda").manual_seed(21)
+    c = kv.PagedCache(1, 16, 16, Hk, D, 2, 100)
+    start = _i32([0, n, 2 * n])
+    q, k, v = (torch.randn((2 * n, h, D), device="cuda", generator=g).to(torch.bfloat16) for h in (H, Hk, Hk))
+    c.update(_i32([n, n]))
+    c.append(0, k, v, start)
+    want = c.attend(0, q, start, n)
+    torch.cuda.synchronize()
+    for how in (lambda s: s, lambda s: s.cuda_stream):
+        s = torch.cuda.Stream()
+        block = torch.ones_like(q)
+        at = block.data_ptr()
+        torch.cuda._sleep(20_000_000)
+        total = block.sum()
+        del block
+        out = c.attend(0, q, start, n, stream=how(s))
+        assert out.data_ptr() != at
+        torch.cuda.synchronize()
+        assert total.item() == q.numel() and torch.equal(out, want)
+    c.check_status()
+
+
 @pytest.mark.parametrize("dtype,outside", [("bf16", False), ("bf16", True), ("f32", False)])
 def test_places_past_32_bits(kv, dtype, outside):
     """Pages more than 2^32 bytes (and 2^31 elements) into a layer: written, read, copied on write and moved."""
