@@ -405,6 +405,43 @@ def test_append_places_rows(kv):
         assert int(status[0]) == (6 if lost else 0)
 
 
+@pytest.mark.parametrize("dtype,D,S,Hk", [("bf16", 128, 16, 2), ("f32", 64, 32, 3), ("bf16", 8, 256, 1), ("f32", 200, 64, 5),
+                                          ("bf16", 72, 128, 4)])
+@pytest.mark.parametrize("which", ["first", "last"])
+def test_append_reports_a_bad_page_and_writes_the_rest(kv, dtype, D, S, Hk, which):
+    """The page of a request's first (last) new token is none: reported, that page's rows are lost, every other row is
+    written, nothing else is touched, in this layer or another."""
+    lens, bad, layer = [(3, 3), (0, 20), (40, 300), (S, S + 1), (1, 7)], 2, 1
+    n_new, n = lens[bad]
+    rng = np.random.RandomState(S + D)
+    M, N = max(ref.ceil_div(x, S) for _, x in lens), sum(ref.ceil_div(x, S) for _, x in lens) + 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v = (torch.randn((3, N, S, Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    table, at, order = np.full((len(lens), M), -1, np.int32), 0, rng.permutation(N)
+    for b, (_, x) in enumerate(lens):
+        table[b, :ref.ceil_div(x, S)] = order[at:at + ref.ceil_div(x, S)]
+        at += ref.ceil_div(x, S)
+    gone = (n - n_new if which == "first" else n - 1) // S
+    table[bad, gone] = N if which == "first" else -3
+    q_start = np.concatenate([[0], np.cumsum([a for a, _ in lens])])
+    kn, vn = (torch.randn((int(q_start[-1]), Hk, D), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    want_k, want_v = k.clone(), v.clone()
+    lost = 0
+    for b, (a, x) in enumerate(lens):
+        for i in range(a):
+            p = x - a + i
+            if b == bad and p // S == gone:
+                lost += 1
+                continue
+            want_k[layer, int(table[b, p // S]), p % S] = kn[q_start[b] + i]
+            want_v[layer, int(table[b, p // S]), p % S] = vn[q_start[b] + i]
+    assert lost > 0
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    kv.check(kv.ds_cache_append(kv.KvPool(k, v), layer, kn, vn, _i32(q_start), _i32(table), _i32([x for _, x in lens]), status))
+    assert int(status[0]) == 6
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
 @pytest.mark.parametrize("dtype,Hk", [("bf16", 8), ("f32", 1)])
 @pytest.mark.parametrize("q_start,kv_len", [([0, 20, 3, 4], [30, 32, 32]), ([0, 100, 1, 2], [30, 32, 32]),
                                             ([0, 4, 8, 25], [30, 31, 32]), ([-1, 4, 8, 20], [32, 9, 32]),
