@@ -442,6 +442,103 @@ def test_append_reports_a_bad_page_and_writes_the_rest(kv, dtype, D, S, Hk, whic
     assert torch.equal(k, want_k) and torch.equal(v, want_v)
 
 
+def _interleaved(kind, L, N, S, Hk, D, dtype):
+    """K and V as views of one tensor: (buffer, k, v) of shape [L, N, S, Hk, D]."""
+    if kind == "token":          # K and V of a token side by side
+        buf = torch.zeros((L, N, S, 2, Hk, D), dtype=dtype, device="cuda")
+        return buf, buf[:, :, :, 0], buf[:, :, :, 1]
+    if kind == "head":           # of a head, with a gap behind them
+        buf = torch.zeros((L, N, S, Hk, 2 * D + 8), dtype=dtype, device="cuda")
+        return buf, buf[..., :D], buf[..., D:2 * D]
+    if kind == "page":           # of a page, heads outside its tokens
+        buf = torch.zeros((L, N, 2, Hk, S, D), dtype=dtype, device="cuda")
+        return buf, buf[:, :, 0].transpose(2, 3), buf[:, :, 1].transpose(2, 3)
+    # layers inside pages, tokens of several layers side by side, more heads than are used
+    buf = torch.zeros((N, S, L, 2, Hk + 1, D), dtype=dtype, device="cuda")
+    k, v = (buf[:, :, :, i, :Hk].permute(2, 0, 1, 3, 4) for i in range(2))
+    return buf, k, v
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["token", "head", "page", "layers"])
+@pytest.mark.parametrize("S,Hk,D,G,n", [(16, 2, 128, 4, 5), (64, 3, 64, 1, 2), (128, 1, 128, 5, 40), (16, 4, 64, 2, 90)])
+def test_interleaved_pools(kv, dtype, kind, S, Hk, D, G, n):
+    """K and V in one tensor, with strides that are not dense: append, attention, copy on write and compaction through
+    the calls, against dense arrays; what lies between the rows stays as it was."""
+    L, B, N, lens = 2, 3, 64, [3 * S + 7, n, 5]
+    g = torch.Generator(device="cuda").manual_seed(S + D + n)
+    buf, k, v = _interleaved(kind, L, N, S, Hk, D, DT[dtype])
+    mine = torch.zeros_like(buf)
+    for x in _views(kind, mine, Hk, D):
+        x.fill_(1)
+    pool, status = kv.KvPool(k, v), torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(kv.ds_cache_update_workspace_bytes(B, N), kv.ds_cache_compact_workspace_bytes(N),
+                         kv.ds_paged_attention_workspace_bytes(pool, G * Hk)), dtype=torch.uint8, device="cuda")
+    M = 10
+    held = torch.zeros(N, dtype=torch.int32, device="cuda")
+    held[::3] = 1                                       # somebody else's, so that pages lie apart
+    state = [_i32(np.full((B, M), -1)), _i32([0] * B), held]
+
+    def update(new, parent=None):
+        out = [torch.empty_like(x) for x in state]
+        kv.check(kv.ds_cache_update(pool, *state, _i32(new), *out, ws, status, parent=None if parent is None else _i32(parent)))
+        state[:] = out
+
+    past = [[torch.zeros((2, 0, Hk, D), dtype=DT[dtype], device="cuda") for _ in range(B)] for _ in range(L)]
+
+    def add(rows):
+        start = _i32(np.concatenate([[0], np.cumsum(rows)]))
+        for layer in range(L):
+            new = torch.randn((2, sum(rows), Hk, D), device="cuda", generator=g).to(DT[dtype])
+            kv.check(kv.ds_cache_append(pool, layer, new[0], new[1], start, state[0], state[1], status))
+            past[layer] = [torch.cat([x, y], 1) for x, y in zip(past[layer], new.split(rows, 1))]
+
+    def check(rows):
+        start = np.concatenate([[0], np.cumsum(rows)])
+        held_len = [x.shape[1] for x in past[0]]
+        assert state[1].tolist() == held_len
+        for layer in range(L):
+            q = torch.randn((sum(rows), G * Hk, D), device="cuda", generator=g).to(DT[dtype])
+            out = torch.empty_like(q)
+            kv.check(kv.ds_paged_attention(pool, layer, q, _i32(start), max(rows), state[0], state[1], out, ws, status))
+            dense = np.zeros((2, B, max(held_len), Hk, D))
+            for b in range(B):
+                dense[:, b, :held_len[b]] = _host(past[layer][b])
+            want, _, tol, _ = ref.attend(_host(q), dense[0], dense[1], np.arange(B)[:, None], held_len, start, True, 0,
+                                         ref.default_scale(D), dtype == "bf16")
+            assert (np.abs(_host(out) - want) <= tol).all()
+        assert int(status[0]) == 0
+        assert (buf[mine == 0] == 0).all()
+
+    update(lens)
+    add(lens)
+    check([n, n, 5])
+    update([lens[0], lens[0], 5], [0, 0, 2])            # request 1 becomes a copy of request 0
+    for layer in range(L):
+        past[layer][1] = past[layer][0]
+    update([lens[0] + 3, lens[0] + n, 6])               # both write into the shared last page
+    add([3, n, 1])
+    check([3, n, 1])
+    state[2] -= (torch.arange(N, device="cuda") % 3 == 0).int()
+    out = torch.empty_like(state[0]), torch.empty_like(state[2])
+    page_map, used = torch.empty_like(state[2]), _i32([0])
+    kv.check(kv.ds_cache_compact(pool, state[0], state[2], *out, page_map, used, ws, status))
+    state[0], state[2] = out
+    assert int(used[0]) == int((state[2] > 0).sum()) and int(state[0].max()) < int(used[0])
+    check([4, n, 2])
+
+
+def _views(kind, buf, Hk, D):
+    """K's and V's parts of a buffer of _interleaved."""
+    if kind == "token":
+        return buf[:, :, :, 0], buf[:, :, :, 1]
+    if kind == "head":
+        return buf[..., :D], buf[..., D:2 * D]
+    if kind == "page":
+        return buf[:, :, 0], buf[:, :, 1]
+    return buf[:, :, :, 0, :Hk], buf[:, :, :, 1, :Hk]
+
+
 @pytest.mark.parametrize("dtype,Hk", [("bf16", 8), ("f32", 1)])
 @pytest.mark.parametrize("q_start,kv_len", [([0, 20, 3, 4], [30, 32, 32]), ([0, 100, 1, 2], [30, 32, 32]),
                                             ([0, 4, 8, 25], [30, 31, 32]), ([-1, 4, 8, 20], [32, 9, 32]),
