@@ -574,8 +574,7 @@ cudaError_t launch_rows(const AttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t attention_ws_bytes(int32_t dtype, int32_t D) {
-  (void)dtype;
+size_t attention_ws_bytes(int32_t D) {
   // a record a share, and rows of partial results: D sums, reference and sum
   return (size_t)kMaxShares * 64 + (size_t)kRows * (D + 2) * sizeof(float);
 }

@@ -30,7 +30,7 @@ struct WorkForm {
   static __host__ __device__ __forceinline__ int64_t begin(int64_t total, int v) {
     return (int64_t)((uint64_t)(total * v) / (uint64_t)kShares);
   }
-  // whether no row of a unit that sees keys [lo, hi) sees some of a tile's
+  // whether some of a tile's keys are seen by no row of a unit that sees keys [lo, hi)
   static __device__ __forceinline__ bool partly_seen(int tile, int lo, int hi) {
     return tile * kKeys < lo || (tile + 1) * kKeys > hi;
   }

@@ -207,7 +207,7 @@ ds_status ds_cache_append(const ds_append_args* a, ds_stream_t stream) {
 
 size_t ds_paged_attention_workspace_bytes(int32_t dtype, int32_t head_dim) {
   if ((dtype != DS_F32 && dtype != DS_BF16) || (head_dim != 64 && head_dim != 128)) return 0;
-  return attention_ws_bytes(dtype, head_dim);
+  return attention_ws_bytes(head_dim);
 }
 
 ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
@@ -229,7 +229,7 @@ ds_status ds_paged_attention(const ds_attention_args* a, ds_stream_t stream) {
   for (const void* q : ptrs)
     if (!aligned(q, 16)) return DS_ERR_INVALID_ARG;
   if (a->lse != nullptr && !aligned(a->lse, 4)) return DS_ERR_INVALID_ARG;
-  if (!aligned(a->workspace, 16) || a->workspace_bytes < attention_ws_bytes(a->pool.dtype, a->pool.head_dim))
+  if (!aligned(a->workspace, 16) || a->workspace_bytes < attention_ws_bytes(a->pool.head_dim))
     return DS_ERR_WORKSPACE;
   if (a->T == 0) return DS_OK;
   if (!aligned(a->q, 16) || !aligned(a->out, 16)) return DS_ERR_INVALID_ARG;

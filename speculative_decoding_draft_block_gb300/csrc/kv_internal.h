@@ -169,7 +169,7 @@ constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are b
 
 size_t update_ws_bytes(int32_t B, int32_t n_pages);
 size_t compact_ws_bytes(int32_t n_pages);
-size_t attention_ws_bytes(int32_t dtype, int32_t D);
+size_t attention_ws_bytes(int32_t D);
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s);
