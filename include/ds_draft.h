@@ -62,7 +62,7 @@ typedef enum {
   DS_ERR_WORKSPACE = 3,   /* workspace pointer missing or smaller than *_workspace_bytes */
   DS_ERR_CUDA = 4,        /* a CUDA runtime call failed (launch or query) */
   DS_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up */
-  DS_ERR_BOUNDS = 6,      /* a token id read from device memory is outside [0, V) */
+  DS_ERR_BOUNDS = 6,      /* read from device memory: a token id outside [0, V), or (ds_cache.h) a row, length or page */
   DS_ERR_NONFINITE = 7,   /* a NaN or +inf logit, or a row with no finite logit */
   DS_ERR_PAGES = 8        /* the cache has too few free pages (ds_cache.h) */
 } ds_status;

@@ -651,7 +651,7 @@ const char* ds_status_string(ds_status s) {
     case DS_ERR_WORKSPACE: return "workspace missing or too small";
     case DS_ERR_CUDA: return "CUDA runtime error";
     case DS_ERR_TIMEOUT: return "device wait timed out";
-    case DS_ERR_BOUNDS: return "token id out of range";
+    case DS_ERR_BOUNDS: return "token id (cache: row, length or page) out of range";
     case DS_ERR_NONFINITE: return "non-finite logit or empty distribution";
     case DS_ERR_PAGES: return "too few free cache pages";
   }

@@ -161,6 +161,11 @@ def test_bad_compactions_are_refused(kv, bad, code):
     assert kv.load().ds_cache_compact(ctypes.byref(_compact(kv, **bad)), None) == code
 
 
+def test_status_texts_name_the_cache(kv):
+    text = kv._lib.ds_status_string
+    assert "page" in text(6) and "token" in text(6) and "page" in text(8)
+
+
 def test_workspace_sizes(kv):
     lib = kv.load()
     assert lib.ds_cache_update_workspace_bytes(128, 1000) >= 4 * (4 * 1000 + 2 * 128)
