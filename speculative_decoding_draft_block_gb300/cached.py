@@ -166,8 +166,12 @@ def main(argv=None):
     ap.add_argument("--cycles", type=int, default=16)
     ap.add_argument("--temperature", type=float, default=0.0)
     a = ap.parse_args(argv)
-    c = CachedCycle(small_inputs(a.requests, temperature=a.temperature))
-    c.prompt([[(7 * b + i) % c.cyc.V for i in range(3 + 9 * b)] for b in range(a.requests)])
+    inp, page = small_inputs(a.requests, temperature=a.temperature), 16
+    prompts = [range(7 * b, 7 * b + 3 + 9 * b) for b in range(a.requests)]
+    # room for the longest request to grow by K + 1 tokens every cycle, in pages of its own
+    longest = len(prompts[-1]) + a.cycles * (inp["base_logits"].shape[1] + 1)
+    c = CachedCycle(inp, page_size=page, n_pages=a.requests * -(-longest // page), max_len=longest)
+    c.prompt([[i % c.cyc.V for i in p] for p in prompts])
     emitted = torch.zeros(a.requests, dtype=torch.int32, device=c.anchor.device)
     for i in range(a.cycles):
         if i == a.cycles // 2:   # the first request ends, a copy of the last takes its place

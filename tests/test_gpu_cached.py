@@ -82,6 +82,13 @@ def test_the_command(cached, capsys):
     assert "6 cycles of 3 requests" in capsys.readouterr().out
 
 
+@pytest.mark.parametrize("requests,cycles", [(1, 1), (48, 4), (2, 400)])
+def test_the_command_has_room_for_what_it_is_asked(cached, capsys, requests, cycles):
+    """Many requests, or many cycles, pass a fixed pool or a fixed length."""
+    cached.main(["--requests", str(requests), "--cycles", str(cycles)])
+    assert "%d cycles of %d requests" % (cycles, requests) in capsys.readouterr().out
+
+
 def test_attention_writes_the_cycles_states(cached):
     """The attention's output is the draft's hidden states as they stand (heads * head_dim = d): the confidence kernel,
     which reads the states before it waits for the draft, sees all of them."""
