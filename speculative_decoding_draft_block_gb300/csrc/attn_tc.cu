@@ -103,7 +103,7 @@ enum : uint32_t {
 // What the waits look at beside their barrier.
 struct Watch {
   int abort;  // a wait has given up
-  int beat;   // counts up while rows are computed again (see `anew`), which may take long
+  int anew;   // warps that compute rows again (see `anew`), which may take long
 };
 
 struct Header {
@@ -159,27 +159,21 @@ struct Form : WorkForm<kTile, kForm == kPairs ? kMaxAttnCtas : 2 * kMaxAttnCtas,
 
 // Bounded waits. One that gives up sets the abort flag, which ends every role's
 // loop; the status is reported once, at the kernel's end (the waits are many and
-// inlined, and the warps' loops share one instruction cache). A wait gives up once
-// the beat has stood still for its limit; the beat comes every 32 keys of a
-// recomputation, so that one of any length is waited for.
-__device__ __forceinline__ bool given_up(volatile Watch* watch, int& beat, uint32_t& polled, uint32_t limit) {
-  if (polled >= limit) {
-    const int now = watch->beat;
-    if (now == beat) watch->abort = 1;
-    beat = now;
-    polled = 0;
-  }
+// inlined, and the warps' loops share one instruction cache). While a warp computes
+// rows again, which ends by itself, the others' waits do not count.
+__device__ __forceinline__ bool given_up(volatile Watch* watch, uint32_t& polled, uint32_t limit) {
+  if (watch->anew != 0) polled = 0;
+  if (polled >= limit) watch->abort = 1;
   return watch->abort != 0;
 }
 
 // Waits until the entry of that number stands in a slot.
 __device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t number, volatile Watch* watch) {
   const volatile uint32_t* at = entry;
-  int beat = 0;
 #pragma unroll 1
   for (uint32_t i = 1; *at != number; ++i) {
     __nanosleep(40);
-    if ((i & 255) == 0 && given_up(watch, beat, i, kWaitPolls << 8)) return false;
+    if ((i & 255) == 0 && given_up(watch, i, kWaitPolls << 8)) return false;
   }
   return true;
 }
@@ -188,10 +182,9 @@ __device__ __forceinline__ bool wait_number(const uint32_t* entry, uint32_t numb
 // roles that may have nothing to do for as long as a unit lasts.
 constexpr uint32_t kIdlePolls = 1u << 22;
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile Watch* watch, uint32_t polls) {
-  int beat = 0;
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait_sleep(bar, parity, 20000u); ++i)
-    if ((i & 15) == 0 && given_up(watch, beat, i, polls)) return false;
+    if ((i & 15) == 0 && given_up(watch, i, polls)) return false;
   return true;
 }
 
@@ -284,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.entry[i] = 0;
     }
     sh.watch.abort = 0;
-    sh.watch.beat = 0;
+    sh.watch.anew = 0;
     fence_barrier_init();
   }
 
@@ -826,12 +819,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what they see, in float32, four at a time over the same keys: each lane has D / 32
       // columns; of eight keys' 32 products every lane ends up with one sum, its weight
       // (-1: unseen), and hands it to all. A piece may be as long as the cache, so
-      // the other roles' waits follow the beat.
+      // the other roles' waits do not count meanwhile.
       // 58 to 217 rows x keys a us and SM: 210 rows over 100,000 keys (D = 64) 95 ms.
       auto anew = [&](uint32_t again, int t_row, int h_row, char* dst, int a, int z, float r_ref, float r_f) {
         constexpr int N = D / 32, kR = 4, kK = 8;  // columns, rows, keys
         static_assert(kR * kK == 32, "a lane a row and key");
         const int shift = p.pool.page_shift;
+        if (lane == 0) atomicAdd(&sh.watch.anew, 1);
         __syncwarp();  // the rows as they were first stored
 #pragma unroll 1
         while (again != 0) {
@@ -865,7 +859,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int z_all = __reduce_max_sync(0xffffffffu, my_a < my_z ? my_z : 0);
 #pragma unroll 1
           for (int k0 = a_all; k0 < z_all; k0 += 32) {
-            if (lane == 0) atomicAdd(&sh.watch.beat, 1);
             // where this lane's key of 32 stands, -1: nowhere (a page out of range has been reported)
             int64_t place = -1;
             if (k0 + lane < z_all) {
@@ -935,6 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (lane == 0) atomicSub(&sh.watch.anew, 1);
       };
       const uint32_t last_tile = list_tiles - 1;
       const uint32_t stage_at = (kPair ? 2 * last_tile + s : 4 * last_tile + (s == 0 ? 2 : 4)) % kSlots;
