@@ -144,10 +144,11 @@ def _rows(t, name, pool, shape, heads=None):
 
 
 def _bytes(t, name, device):
-    _on_device(t, name, device)
+    if t.get_device() != device:
+        _on_device(t, name, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _stream(stream, pool):
