@@ -103,8 +103,9 @@ ds_status ds_cache_append(const ds_append_args* args, ds_stream_t stream);
  * us and SM, float32 2 to 4. In bfloat16 calls of up to 16 rows a KV head it is done
  * for the rows that see the value, too.)
  * bfloat16: products and sums in float32, the weights exp(s_j - r) of the
- * value product rounded to bfloat16. float32: all in float32; 256 KV heads over a table
- * of more than 2^30 - 128 tokens are not supported (DS_ERR_UNSUPPORTED).
+ * value product rounded to bfloat16. float32: all in float32; 256 KV heads over a
+ * table of more than 2^30 - 128 tokens are DS_ERR_UNSUPPORTED.
+ * `out` must not overlap q or the pool.
  */
 typedef struct {
   ds_kv_pool pool;              /* head_dim 64 or 128 */

@@ -35,7 +35,7 @@
 //        stream, and both read each key tile from shared memory. Bound by the
 //        tensor core and, between its products, by the softmax that feeds it. Units
 //        with one row tile run on stream 0. Prompt chunks of 2 x 2048 tokens over
-//        9000 to 16384 cached: 465 to 520 us, 1.55 to 1.38 PFLOP/s by the clock.
+//        9000 to 16384 cached: 465 to 528 us, 1.55 to 1.36 PFLOP/s by the clock.
 //
 //   warps 0, 1  producers: walk over the share (solo: one a stream, with its K and
 //               V; pair: one for Q and K, one for V), hand its pieces to the softmax

@@ -7,8 +7,8 @@
 // without a grid-wide wait. The second launch spreads what is left (tables and
 // page contents) over the whole GPU, reading the plan from the workspace (past the
 // first-level cache: it is set up, and may be resident, while the plan runs).
-// Update of 128 requests and 16384 pages: 12.0 us (the plan alone 10.6). Compaction of
-// 4 GB, half of it held (2.06 GB read and written): 323 us, 6.4 TB/s.
+// Update of 128 requests and 16384 pages: 11.0 us (the plan alone 9.9). Compaction of
+// 4 GB, half of it held (2.06 GB read and written): 320 to 328 us, 6.3 to 6.4 TB/s.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -591,8 +591,8 @@ size_t compact_ws_bytes(int32_t n_pages) {
 
 // Whether one CTA plans: its barriers are cheaper than a cluster's (8 is the
 // portable size), its reads fewer at a time. Update of 16 requests and 1024 pages:
-// 9.7 us, by a cluster 10.5; of 64 and 1024: 12.0 and 9.9; of 128 and 4096: 15.4 and
-// 10.6. Compaction of 512 pages: 10.0 and 10.4 us; of 2048: 14.4 and 14.2; of 8192:
+// 8.7 us, by a cluster 8.8; of 8 and 512: 8.5 and 8.7; of 64 and 1024: 12.6 and 9.6; of
+// 128 and 4096: 17.5 and 10.1. Compaction of 512 pages: 10.0 and 10.4 us; of 2048: 14.4 and 14.2; of 8192:
 // 35.1 and 31.8.
 bool one_cta(int32_t B, int32_t n_pages) { return n_pages <= 1024 && B <= 16; }
 
