@@ -118,7 +118,9 @@ bool strides16(std::initializer_list<int64_t> strides, int32_t dtype) {
 // The pool's fields, and its view with `layer` as base (all layers: layer 0).
 ds_status check_pool(const ds_kv_pool& a, int32_t layer, PoolView* v) {
   if (a.dtype != DS_F32 && a.dtype != DS_BF16) return DS_ERR_INVALID_ARG;
-  if (a.n_layers < 1 || a.n_layers > (1 << 28) || a.n_pages < 1 || a.n_pages > (1 << 28) || layer < 0 || layer >= a.n_layers) return DS_ERR_INVALID_ARG;
+  if (a.n_layers < 1 || a.n_layers > (1 << 28) || a.n_pages < 1 || a.n_pages > (1 << 28) || layer < 0 ||
+      layer >= a.n_layers)
+    return DS_ERR_INVALID_ARG;
   if (a.page_size < 16 || a.page_size > 256 || (a.page_size & (a.page_size - 1)) != 0) return DS_ERR_INVALID_ARG;
   if (a.n_kv_heads < 1 || a.n_kv_heads > 256) return DS_ERR_INVALID_ARG;
   if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8 != 0) return DS_ERR_INVALID_ARG;

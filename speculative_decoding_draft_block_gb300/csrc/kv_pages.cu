@@ -592,8 +592,8 @@ size_t compact_ws_bytes(int32_t n_pages) {
 // Whether one CTA plans: its barriers are cheaper than a cluster's (8 is the
 // portable size), its reads fewer at a time. Update of 16 requests and 1024 pages:
 // 8.7 us, by a cluster 8.8; of 8 and 512: 8.5 and 8.7; of 64 and 1024: 12.6 and 9.6; of
-// 128 and 4096: 17.5 and 10.1. Compaction of 512 pages: 10.0 and 10.4 us; of 2048: 14.4 and 14.2; of 8192:
-// 35.1 and 31.8.
+// 128 and 4096: 17.5 and 10.1. Compaction of 512 pages: 10.0 and 10.4 us; of 2048: 14.4
+// and 14.2; of 8192: 35.1 and 31.8.
 bool one_cta(int32_t B, int32_t n_pages) { return n_pages <= 1024 && B <= 16; }
 
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s) {

@@ -334,8 +334,7 @@ class PagedCache:
             if stream is None:
                 out = torch.empty_like(q)
             else:   # of that stream's memory: blocks freed on the current one may still be in use there
-                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), q.device)
-                with torch.cuda.stream(s):
+                with torch.cuda.stream(torch.cuda.ExternalStream(_lib._stream(stream).value or 0, q.device)):
                     out = torch.empty_like(q)
         check(ds_paged_attention(self.pool, layer, q, q_start, max_q, self.block_table, self.kv_len, out,
                                  self.workspace, self.status, lse=lse, causal=causal, window=window, scale=scale,
