@@ -24,6 +24,10 @@
  *   ds_cache_append, ds_paged_attention          per layer
  *   ... logits ..., ds_verify
  *   ds_cache_update  (new_len = accepted prefix) back to what was accepted
+ * With a tree of drafted tokens a request (below), ds_tree_masks once a cycle,
+ * ds_paged_attention_tree in place of ds_paged_attention, and ds_cache_keep, which
+ * gives the lengths for the last ds_cache_update. A quantised pool (below) takes the
+ * calls that have `scales`.
  */
 #ifndef DS_CACHE_H
 #define DS_CACHE_H
@@ -200,6 +204,104 @@ typedef struct {
 
 size_t ds_cache_compact_workspace_bytes(int32_t n_pages);
 ds_status ds_cache_compact(const ds_compact_args* args, ds_stream_t stream);
+
+/* ---- quantised pools ----------------------------------------------------------- */
+
+/*
+ * dtype DS_E4M3: K and V hold 8-bit floats (OCP FP8 E4M3, no infinities), and every
+ * token's row of a head has a power of two for all of its head_dim values:
+ *     x = code * 2^(scale - 127),
+ * scale a byte (OCP E8M0) of `scales` [n_layers][n_pages][2][n_kv_heads][page_size],
+ * contiguous, K's of a page first, then V's; 255 (not a number): the row is NaN. Such
+ * a row of a pool has head_dim a multiple of 16 (strides count 8-bit elements); rows
+ * outside the cache (k_new, v_new, q, out) are bfloat16.
+ *   ds_cache_append_scaled   a row gets the smallest 2^e, e >= -100, with
+ *       max |x| <= 448 * 2^e, and its values x / 2^e rounded to the nearest (ties to
+ *       even): off by at most 2^-4 |x| or 2^(e - 10), whichever is more. A row with a
+ *       value that is not finite gets scale 255 and zeros for codes.
+ *   ds_paged_attention_tree  reads code * 2^(scale - 127), which bfloat16 holds exactly
+ *       for scales from 27 (what append writes) to 246, and to its smallest subnormal
+ *       below that; a code of 0x7F or 0xFF, which append does not write, reads as 480 in size.
+ *       All else is as for bfloat16 pools.
+ *   ds_cache_update_scaled, ds_cache_compact_scaled   move the scales with the pages.
+ * With scales = NULL the calls are those without the suffix.
+ */
+enum { DS_E4M3 = 2 };
+
+ds_status ds_cache_append_scaled(const ds_append_args* args, uint8_t* scales, ds_stream_t stream);
+ds_status ds_cache_update_scaled(const ds_update_args* args, uint8_t* scales, ds_stream_t stream);
+ds_status ds_cache_compact_scaled(const ds_compact_args* args, uint8_t* scales, ds_stream_t stream);
+
+/* ---- trees of drafted tokens ------------------------------------------------------ */
+
+/*
+ * The new tokens of a request may be the nodes of a tree (or several trees) that
+ * hang on its cached context: its first kv_len - n_b tokens. Bit j % 32 of word
+ * j / 32 of a row's mask: the row sees new token j of its request. So row i sees
+ *   the context's tokens (window > 0: those at p - window + 1 and after,
+ *                          p = kv_len - n_b + depth[i], depth 0 without `depth`),
+ *   the new tokens of its mask, itself among them only if its bit is set.
+ * Bits of tokens past n_b count for nothing. A negative depth counts as 0. `causal` of
+ * the arguments has to be 1. A request with rows but kv_len < n_b has no context, and
+ * its first n_b - kv_len tokens have no place: their bits count for nothing. Table
+ * entries are needed for all pages from the first that a row of depth 0 would see.
+ */
+typedef struct {
+  const uint32_t* mask;     /* [T][mask_words] */
+  int32_t mask_words;       /* >= ceil(min(max_q, T) / 32), <= 2^18 */
+  const int32_t* depth;     /* [T] or NULL; looked at only if window > 0 */
+} ds_tree;
+
+/* ds_paged_attention over a pool with or without `scales`, of a tree or (NULL) not. */
+ds_status ds_paged_attention_tree(const ds_attention_args* args, const uint8_t* scales, const ds_tree* tree,
+                                  ds_stream_t stream);
+
+/*
+ * Masks and depths of trees given by their nodes' parents: rows as in ds_append_args,
+ * parent[t] the place within the request of row t's parent, -1 for a root. A
+ * parent comes before its children; any other value: DS_ERR_BOUNDS, and the node
+ * counts as a root. depth = number of ancestors; mask: the node and its ancestors
+ * (window > 0: those less than `window` above it). A request outside the limits
+ * (longer than max_q, rows outside [0, T)): DS_ERR_BOUNDS, its rows are left alone.
+ */
+typedef struct {
+  int32_t B, T;                 /* 1 <= B <= 65535, 0 <= T <= 2^23 */
+  int32_t max_q;                /* upper bound of n_b, 1..4096 */
+  int32_t mask_words;           /* >= ceil(min(max_q, T) / 32), <= 2^18 */
+  int32_t window;               /* 0: none */
+  const int32_t* parent;        /* [T] */
+  const int32_t* q_start;       /* [B+1] */
+  uint32_t* mask;               /* out [T][mask_words] */
+  int32_t* depth;               /* out [T], or NULL */
+  int32_t* status;
+} ds_tree_args;
+
+ds_status ds_tree_masks(const ds_tree_args* args, ds_stream_t stream);
+
+/*
+ * Keeps a path of each request's new tokens: for i < m_b, the number of entries of
+ * path[b] before its first negative one, the row at position first + path[b][i]
+ * goes to position first + i, first = kv_len[b] - n_b, K and V of all layers; and
+ * new_len[b] = first + m_b, the length to go on with (ds_cache_update). The path's
+ * entries ascend, below n_b. Rows move in place: what stood at the places that are
+ * written and is not of the path is lost. Pages that other requests hold must not be written
+ * (as by ds_cache_append). A request whose rows, length (below n_b, too) or path is out of these
+ * limits, or which needs a page outside [0, n_pages): DS_ERR_BOUNDS, its rows stay, new_len[b] = kv_len[b].
+ */
+typedef struct {
+  ds_kv_pool pool;
+  int32_t B, T, max_pages;
+  int32_t path_len;             /* 1..4096 */
+  const int32_t* path;          /* [B][path_len] */
+  const int32_t* q_start;       /* [B+1] */
+  const int32_t* block_table;   /* [B][max_pages] */
+  const int32_t* kv_len;        /* [B], the new tokens counted */
+  int32_t* new_len;             /* out [B], not overlapping the inputs */
+  uint8_t* scales;              /* of a quantised pool, else NULL */
+  int32_t* status;
+} ds_keep_args;
+
+ds_status ds_cache_keep(const ds_keep_args* args, ds_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,8 +22,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeyTile = kAttnTileF32;
 
-template <int kBM>
-struct Form32 : WorkForm<kKeyTile, kMaxShares, kBM> {};
+template <int kBM, bool kTree>
+struct Form32 : WorkForm<kKeyTile, kMaxShares, kBM, kTree> {};
 
 template <int D, int kBM>
 struct Tiles {
@@ -47,9 +47,9 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D, int kBM>
+template <int D, int kBM, bool kTree>
 __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) {
-  using F = Form32<kBM>;
+  using F = Form32<kBM, kTree>;
   constexpr int kRM = kBM / 16;      // rows of a thread
   constexpr int kC = D / 64;         // float4 output columns of a thread
   extern __shared__ __align__(16) uint8_t smem[];
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
     char* out[kRM];
     float* lse[kRM];
     bool valid[kRM];
+    const uint32_t* words[kRM];  // (a tree's rows: hi is the context's end)
 #pragma unroll
     for (int i = 0; i < kRM; ++i) {
       const int row = ty * kRM + i, at = x.off + row, tok = p.by_group.quotient(at);
@@ -83,6 +84,12 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       hi[i] = !valid[i] ? 0 : p.causal ? min(pos + 1, x.kv) : x.kv;
       lo[i] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       const int64_t t = x.token + tok;
+      words[i] = nullptr;
+      if (kTree && valid[i]) {
+        words[i] = p.mask + t * p.mask_words;
+        hi[i] = x.ctx;
+        lo[i] = tree_low(p, x.ctx, t);
+      }
       out[i] = p.out + t * p.o_token + head * p.o_head;
       lse[i] = p.lse != nullptr ? p.lse + t * p.n_heads + head : nullptr;
     }
@@ -96,6 +103,10 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       continue;
     }
     const int32_t* table = p.block_table + (int64_t)x.b * p.max_pages;
+    auto sees = [&](int i, int key) {
+      if (key >= lo[i] && key < hi[i]) return true;
+      return kTree && valid[i] && key >= x.ctx && key >= 0 && key < x.kv && tree_sees(words[i], key, x.ctx);
+    };
     // places of a tile's keys (by the first 64 threads)
     auto find = [&](int j) {
       if (tid < kKeyTile) {
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int key = key0 + 16 * k;
-          s[i][k] = key >= lo[i] && key < hi[i] ? s[i][k] * c : kNegInf;
+          s[i][k] = sees(i, key) ? s[i][k] * c : kNegInf;
           top = fmaxf(top, s[i][k]);
         }
 #pragma unroll
@@ -245,7 +256,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
         for (int k = 0; k < kC; ++k) o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float ref = m[i] == kNegInf ? 0.f : m[i];
 #pragma unroll 1
-        for (int key = max(key0, lo[i]); key < min(key1, hi[i]); ++key) {
+        for (int key = max(key0, lo[i]); key < min(key1, kTree ? x.kv : hi[i]); ++key) {
+          if (kTree && !sees(i, key)) continue;
           const int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) break;  // (reported above)
           const int64_t at = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride + (int64_t)(key & mask) * p.pool.token_stride;
@@ -309,9 +321,9 @@ struct FewTiles {
   ShareStart<kThreads, 1> work;
 };
 
-template <int D, int kR>
+template <int D, int kR, bool kTree>
 __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnParams p) {
-  using F = Form32<kR>;
+  using F = Form32<kR, kTree>;
   constexpr int kCols = D / 4;                // threads across a row of values
   constexpr int kGroups = kThreads / kCols;   // groups of keys in the value product
   constexpr int kGroupKeys = kKeyTile / kGroups;
@@ -376,11 +388,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
       }
       copies_commit();
     };
+    // (a tree's rows: hi is the context's end)
+    auto sees = [&](int row, int key) {
+      if (key >= sh.lo[row] && key < sh.hi[row]) return true;
+      if (!kTree || row >= x.rows || key < x.ctx || key < 0 || key >= x.kv) return false;
+      const int64_t t = x.token + p.by_group.quotient(x.off + row);
+      return tree_sees(p.mask + t * p.mask_words, key, x.ctx);
+    };
     find(0);
     if (tid < kR) {
       const int tok = p.by_group.quotient(x.off + tid), pos = x.pos + tok;
-      sh.hi[tid] = tid >= x.rows ? 0 : p.causal ? min(pos + 1, x.kv) : x.kv;
-      sh.lo[tid] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      sh.hi[tid] = tid >= x.rows ? 0 : kTree ? x.ctx : p.causal ? min(pos + 1, x.kv) : x.kv;
+      sh.lo[tid] = kTree ? (tid < x.rows ? tree_low(p, x.ctx, x.token + tok) : 0) : p.window > 0 ? max(0, pos - p.window + 1) : 0;
     }
     for (int i = tid; i < kR * kCols; i += kThreads) {
       int64_t t;
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
         for (int r = 0; r < kR; ++r) {
           s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
           s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-          if ((r & 3) == part4) sh.s[r][my_key] = key >= sh.lo[r] && key < sh.hi[r] ? s[r] * c : kNegInf;
+          if ((r & 3) == part4) sh.s[r][my_key] = sees(r, key) ? s[r] * c : kNegInf;
         }
       }
       __syncthreads();  // scores are there, K is read
@@ -501,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
         y = make_float4(0.f, 0.f, 0.f, 0.f);
         const float ref = st.x == kNegInf ? 0.f : st.x;
 #pragma unroll 1
-        for (int key = max(key0, sh.lo[row]); key < min(key1, sh.hi[row]); ++key) {
+        for (int key = max(key0, sh.lo[row]); key < min(key1, kTree ? x.kv : sh.hi[row]); ++key) {
+          if (kTree && !sees(row, key)) continue;
           const int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) break;
           const int64_t at = (int64_t)page * p.pool.page_stride + x.h * p.pool.head_stride + (int64_t)(key & mask) * p.pool.token_stride;
@@ -533,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
 }
 
 // A form of the kernel with its shared memory, and the join of its cut units.
-template <int D, int kBM>
+template <int D, int kBM, bool kTree>
 cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParams), size_t smem, Readiness& readiness) {
-  using F = Form32<kBM>;
+  using F = Form32<kBM, kTree>;
   cudaError_t e = readiness.get(
       [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
   if (e != cudaSuccess) return e;
@@ -545,16 +565,16 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s, void (*kernel)(AttnParam
   return launch_join<F, D, float>(p, s, (int)(most < kBM ? most : kBM), kBM, kBM);
 }
 
-template <int D, int kR>
+template <int D, int kR, bool kTree>
 cudaError_t launch_few(const AttnParams& p, cudaStream_t s) {
   static Readiness readiness;
-  return launch<D, kR>(p, s, attn_f32_few_kernel<D, kR>, sizeof(FewTiles<D, kR>), readiness);
+  return launch<D, kR, kTree>(p, s, attn_f32_few_kernel<D, kR, kTree>, sizeof(FewTiles<D, kR>), readiness);
 }
 
-template <int D, int kBM>
+template <int D, int kBM, bool kTree>
 cudaError_t launch_tiles(const AttnParams& p, cudaStream_t s) {
   static Readiness readiness;
-  return launch<D, kBM>(p, s, attn_f32_kernel<D, kBM>, sizeof(Tiles<D, kBM>), readiness);
+  return launch<D, kBM, kTree>(p, s, attn_f32_kernel<D, kBM, kTree>, sizeof(Tiles<D, kBM>), readiness);
 }
 
 // Measured on 64 requests of one token over 500 to 4000 cached, 8 KV heads (D = 128:
@@ -563,13 +583,13 @@ cudaError_t launch_tiles(const AttnParams& p, cudaStream_t s) {
 // 16 rows 432 against 482, but D = 64 278 against 269 and 10 rows over 33 to 1000
 // cached 15.7 against 14.2: the sums of 16 rows do not leave two blocks an SM enough
 // registers. Tiles of 64 rows take the rest: prompt chunks of 512 tokens 36 TFLOP/s.
-template <int D>
+template <int D, bool kTree>
 cudaError_t launch_rows(const AttnParams& p, cudaStream_t s) {
   const int64_t rows = (int64_t)p.max_q * p.group;  // of the longest request, per KV head
-  return rows <= 4    ? launch_few<D, 4>(p, s)
-         : rows <= 8  ? launch_few<D, 8>(p, s)
-         : rows <= 16 ? launch_tiles<D, 16>(p, s)
-                      : launch_tiles<D, 64>(p, s);
+  return rows <= 4    ? launch_few<D, 4, kTree>(p, s)
+         : rows <= 8  ? launch_few<D, 8, kTree>(p, s)
+         : rows <= 16 ? launch_tiles<D, 16, kTree>(p, s)
+                      : launch_tiles<D, 64, kTree>(p, s);
 }
 
 }  // namespace
@@ -580,7 +600,8 @@ size_t attention_ws_bytes(int32_t D) {
 }
 
 cudaError_t launch_attention_f32(const AttnParams& p, cudaStream_t s) {
-  return p.D == 128 ? launch_rows<128>(p, s) : launch_rows<64>(p, s);
+  if (p.mask != nullptr) return p.D == 128 ? launch_rows<128, true>(p, s) : launch_rows<64, true>(p, s);
+  return p.D == 128 ? launch_rows<128, false>(p, s) : launch_rows<64, false>(p, s);
 }
 
 }  // namespace ds

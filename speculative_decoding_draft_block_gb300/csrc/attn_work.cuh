@@ -21,8 +21,9 @@ namespace {
 
 constexpr int kUnitCost = kAttnUnitCost;  // of a unit's set-up, in key tiles
 
-template <int kTileKeys, int kShareCount, int kPartialRows>
+template <int kTileKeys, int kShareCount, int kPartialRows, bool kTrees = false>
 struct WorkForm {
+  static constexpr bool kTree = kTrees;            // whether the rows may be a tree's nodes
   static constexpr int kKeys = kTileKeys;          // keys of a tile
   static constexpr int kShares = kShareCount;
   static constexpr int kPartRows = kPartialRows;   // rows of a slot of partial results
@@ -43,7 +44,8 @@ struct Piece {
   int token, off, rows;   // the unit's rows begin at head `off` of the KV head's, of row `token` of q
   int pos, kv;            // position of that token, cached tokens
   int whole, slot;        // the piece is the unit; else its slot of partial results
-  int pad[3];
+  int ctx;                // tokens cached before the request's rows
+  int pad[2];
 };
 static_assert(sizeof(Piece) == 64, "four 16-byte words");
 
@@ -92,6 +94,10 @@ __device__ __forceinline__ Unit make_unit(const AttnParams& p, const Request& r,
   x.pos = r.kv - r.n + x.token;
   x.hi = p.causal ? min(r.kv - r.n + last + 1, r.kv) : r.kv;
   x.lo = p.window > 0 ? max(0, x.pos - p.window + 1) : 0;
+  if (F::kTree && p.mask != nullptr) {  // (a row's depth is at least 0)
+    x.hi = r.kv;
+    x.lo = p.window > 0 ? max(0, r.kv - r.n - p.window + 1) : 0;
+  }
   x.n = 0;
   x.tile0 = 0;
   if (x.hi > x.lo) {
@@ -173,6 +179,7 @@ struct Walk {
       x.rows = y.rows;
       x.pos = y.pos;
       x.kv = r.kv;
+      x.ctx = r.kv - r.n;
       x.whole = x.n == y.n;
       x.slot = t0 > 0 ? 0 : 1;
       if (cut != nullptr && !x.whole && x.slot == 1) {
@@ -252,6 +259,41 @@ __device__ __forceinline__ int64_t locate_shares(const AttnParams& p, int unit_r
     }
   }
   return total;
+}
+
+// ---- rows of trees ---------------------------------------------------------------------
+
+// The first key of the context that a tree's row t sees.
+__device__ __forceinline__ int tree_low(const AttnParams& p, int ctx, int64_t t) {
+  if (p.window <= 0) return 0;
+  const int depth = p.depth != nullptr ? min(max(__ldcg(p.depth + t), 0), 1 << 29) : 0;
+  return max(0, ctx + depth - p.window + 1);
+}
+
+// Bits a .. z - 1 of a word, whatever the bounds.
+__device__ __forceinline__ uint32_t bits_between(int a, int z) {
+  a = min(max(a, 0), 32);
+  z = min(max(z, 0), 32);
+  return (uint32_t)((1ull << z) - 1) & ~(uint32_t)((1ull << a) - 1);
+}
+
+// Which of keys key0 .. key0 + 31 a tree's row sees: of its context from lo on, and
+// the new tokens of its mask, which begin at key ctx (two words hold the 32 bits).
+__device__ __forceinline__ uint32_t tree_seen(const uint32_t* words, int n_words, int key0, int lo, int ctx, int kv) {
+  uint32_t seen = bits_between(lo - key0, ctx - key0);
+  const int j = key0 - ctx;
+  if (j > -32 && key0 < kv) {
+    const int w = j >> 5;
+    const uint32_t a = w >= 0 && w < n_words ? __ldcg(words + w) : 0u;
+    const uint32_t b = w + 1 < n_words ? __ldcg(words + w + 1) : 0u;
+    seen |= __funnelshift_r(a, b, j & 31) & bits_between(0, kv - key0);
+  }
+  return seen;
+}
+
+// The same for one key of [lo, kv).
+__device__ __forceinline__ bool tree_sees(const uint32_t* words, int key, int ctx) {
+  return key < ctx || (__ldcg(words + ((key - ctx) >> 5)) >> ((key - ctx) & 31) & 1u) != 0;
 }
 
 __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {

@@ -16,6 +16,10 @@ struct PoolView {
   char* v;
   int64_t layer_stride, page_stride, token_stride, head_stride;  // bytes
   int32_t n_layers, n_pages, page_shift, n_kv_heads, row_bytes;  // row: head_dim elements
+  // of a quantised pool (else null): a byte a row, [layer][page][K, V][head][token]
+  uint8_t* scales;
+  __host__ __device__ __forceinline__ int64_t scale_part() const { return (int64_t)n_kv_heads << page_shift; }
+  __host__ __device__ __forceinline__ int64_t scale_layer() const { return 2 * scale_part() * n_pages; }
 };
 
 struct AppendParams {
@@ -59,6 +63,30 @@ struct AttnParams {
   const int32_t* kv_len;
   float* lse;
   char* workspace;
+  int32_t* status;
+  // trees (mask null: none)
+  const uint32_t* mask;
+  const int32_t* depth;
+  int32_t mask_words;
+};
+
+struct KeepParams {
+  PoolView pool;
+  int32_t B, T, max_pages, path_len;
+  const int32_t* path;
+  const int32_t* q_start;
+  const int32_t* table;
+  const int32_t* kv_len;
+  int32_t* new_len;
+  int32_t* status;
+};
+
+struct TreeParams {
+  int32_t B, T, max_q, mask_words, window;
+  const int32_t* parent;
+  const int32_t* q_start;
+  uint32_t* mask;
+  int32_t* depth;
   int32_t* status;
 };
 
@@ -161,9 +189,11 @@ constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1;
 // tiles of 128 keys always (2^23 + 1 tiles, 256 heads), with tiles of 64 except for 256
 // heads over 2^30 tokens.
 inline bool work_fits(int32_t dtype, int64_t tokens, int32_t n_kv_heads) {
-  const int64_t tile = dtype == DS_BF16 ? kAttnTileTc : kAttnTileF32;
+  const int64_t tile = dtype == DS_F32 ? kAttnTileF32 : kAttnTileTc;
   return ((tokens + tile - 1) / tile + kAttnUnitCost) * n_kv_heads <= (int64_t)UINT32_MAX;
 }
+
+constexpr int kMaxTree = 4096;     // nodes of a tree whose masks are made, entries of a path
 
 constexpr int kMaxAttnCtas = 152;  // one per SM of the device the kernels are built for
 
@@ -174,7 +204,11 @@ size_t attention_ws_bytes(int32_t D);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_update(const UpdateParams& p, cudaStream_t s);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s);
+cudaError_t launch_keep(const KeepParams& p, cudaStream_t s);
+cudaError_t launch_tree_masks(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_attention_f32(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_tc_tree(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_tc_e4m3(const AttnParams& p, cudaStream_t s);
 
 }  // namespace ds

@@ -414,6 +414,27 @@ __device__ __forceinline__ void copy_tokens(const PoolView& v, char* base, int s
   }
 }
 
+// The same for the scales of a quantised pool: a head's tokens are contiguous, 16
+// at a time; of the last ones of a copied page only those that are copied change.
+__device__ __forceinline__ void copy_scales(const PoolView& v, int layer, int kv, int src, int dst, int tokens, int tid,
+                                            int threads) {
+  uint8_t* base = v.scales + layer * v.scale_layer() + kv * v.scale_part();
+  const uint4* from = reinterpret_cast<const uint4*>(base + 2 * v.scale_part() * src);
+  uint4* to = reinterpret_cast<uint4*>(base + 2 * v.scale_part() * dst);
+  const int n = (int)(v.scale_part() >> 4), in_head = (1 << v.page_shift >> 4) - 1;
+  for (int x = tid; x < n; x += threads) {
+    const int left = tokens - 16 * (x & in_head);
+    if (left <= 0) continue;
+    uint4 y = __ldcg(from + x);
+    if (left < 16) {
+      const uint4 old = __ldcg(to + x);
+      auto mix = [&](uint32_t a, uint32_t b, int m) { return m >= 4 ? a : m <= 0 ? b : (a & ((1u << 8 * m) - 1)) | (b & ~((1u << 8 * m) - 1)); };
+      y = make_uint4(mix(y.x, old.x, left), mix(y.y, old.y, left - 4), mix(y.z, old.z, left - 8), mix(y.w, old.w, left - 12));
+    }
+    to[x] = y;
+  }
+}
+
 __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p) {
   const int b = blockIdx.x;
   const UpdateWs w = update_ws(p.ws, p.B, p.pool.n_pages);
@@ -446,6 +467,7 @@ __global__ void __launch_bounds__(256) update_apply_kernel(const UpdateParams p)
   for (int part = blockIdx.y; part < 2 * p.pool.n_layers; part += gridDim.y) {  // 2 * layer + (0: K, 1: V)
     char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
     copy_tokens(p.pool, base, copy.x, dst, copy.y, threadIdx.x, blockDim.x);
+    if (p.pool.scales != nullptr) copy_scales(p.pool, part >> 1, part & 1, copy.x, dst, copy.y, threadIdx.x, blockDim.x);
   }
 }
 
@@ -568,7 +590,9 @@ __global__ void __launch_bounds__(256, 3) compact_apply_kernel(const CompactPara
   }
   while (i < n) {
     char* base = (part & 1 ? p.pool.v : p.pool.k) + (int64_t)(part >> 1) * p.pool.layer_stride;
-    copy_tokens(p.pool, base, __ldcg(w.src + i), __ldcg(w.dst + i), tokens, threadIdx.x & (threads - 1), threads);
+    const int src = __ldcg(w.src + i), dst = __ldcg(w.dst + i);
+    copy_tokens(p.pool, base, src, dst, tokens, threadIdx.x & (threads - 1), threads);
+    if (p.pool.scales != nullptr) copy_scales(p.pool, part >> 1, part & 1, src, dst, tokens, threadIdx.x & (threads - 1), threads);
     i += step / parts;
     part += step % parts;
     if (part >= parts) {
