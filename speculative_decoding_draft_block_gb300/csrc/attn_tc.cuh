@@ -1346,8 +1346,10 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)p.pool.n_kv_heads, (cuuint64_t)p.pool.n_pages};
     const cuuint64_t str[3] = {(cuuint64_t)p.pool.token_stride, (cuuint64_t)p.pool.head_stride, (cuuint64_t)p.pool.page_stride};
     const cuuint32_t box[4] = {kQuant ? D : 64, (cuuint32_t)(page < kTile ? page : kTile), 1, 1};
-    const auto encode = kQuant ? encode_tmap_bytes : encode_tmap_bf16;
-    if (!encode(&mk, p.pool.k, 4, dims, str, box) || !encode(&mv, p.pool.v, 4, dims, str, box)) return cudaErrorInvalidValue;
+    auto encode = [&](CUtensorMap* m, const char* from) {
+      return kQuant ? encode_tmap_bytes(m, from, 4, dims, str, box, false) : encode_tmap_bf16(m, from, 4, dims, str, box);
+    };
+    if (!encode(&mk, p.pool.k) || !encode(&mv, p.pool.v)) return cudaErrorInvalidValue;
   }
   cudaError_t e = launch_early(attn_tc_kernel<D, kForm, kTree, kQuant>, dim3(kMaxAttnCtas), dim3(Split<kQuant>::kThreads),
                                Layout<D, kQuant>::kBytes, s, p, mq, mk, mv);
@@ -1366,7 +1368,11 @@ cudaError_t launch_form(const AttnParams& p, cudaStream_t s) {
   // 111 and 113. (The quarters' sums of 16 rows fill the staging slot.)
   const int per_tile = kTile / p.group;
   const bool pair = p.max_q > per_tile && p.T > (int64_t)p.B * per_tile;
-  const bool few = (int64_t)p.max_q * p.group <= kFewRows;
+  const bool few = !kQuant && (int64_t)p.max_q * p.group <= kFewRows;  // (quantised: attn_e4m3_few.cu)
+  if constexpr (kQuant) {
+    if (p.D == 128) return pair ? launch<128, kPairs, kTree, true>(p, s) : launch<128, kSolo, kTree, true>(p, s);
+    return pair ? launch<64, kPairs, kTree, true>(p, s) : launch<64, kSolo, kTree, true>(p, s);
+  } else {
   if (p.D == 128)
     return few    ? launch<128, kFew, kTree, kQuant>(p, s)
            : pair ? launch<128, kPairs, kTree, kQuant>(p, s)
@@ -1374,6 +1380,7 @@ cudaError_t launch_form(const AttnParams& p, cudaStream_t s) {
   return few    ? launch<64, kFew, kTree, kQuant>(p, s)
          : pair ? launch<64, kPairs, kTree, kQuant>(p, s)
                 : launch<64, kSolo, kTree, kQuant>(p, s);
+  }
 }
 
 }  // namespace

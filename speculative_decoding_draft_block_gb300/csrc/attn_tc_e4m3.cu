@@ -3,6 +3,9 @@
 
 namespace ds {
 
-cudaError_t launch_attention_tc_e4m3(const AttnParams& p, cudaStream_t s) { return launch_form<true, true>(p, s); }
+cudaError_t launch_attention_tc_e4m3(const AttnParams& p, cudaStream_t s) {
+  if ((int64_t)p.max_q * p.group <= kFewRows) return launch_attention_e4m3_few(p, s);
+  return launch_form<true, true>(p, s);
+}
 
 }  // namespace ds

@@ -185,9 +185,9 @@ cudaError_t launch_rnn_pack(const void* W_ih, const void* W_hh, int32_t r, int32
 // 2-D or 3-D bfloat16 tensor map with 128-byte swizzle (draft_tc.cu).
 bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
                       const cuuint64_t* strides, const cuuint32_t* box);
-// The same for bytes, box[0] of them in a row, left in that order.
+// The same for rows of box[0] = 64 or 128 bytes, as they are or swizzled over those.
 bool encode_tmap_bytes(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
-                       const cuuint64_t* strides, const cuuint32_t* box);
+                       const cuuint64_t* strides, const cuuint32_t* box, bool swizzled);
 
 // DS_OK on a device the kernels are built for (api.cu).
 ds_status device_supported();
