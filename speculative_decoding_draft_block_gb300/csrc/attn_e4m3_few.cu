@@ -19,12 +19,17 @@
 //   - q in float16 has a row's largest value in [2^14, 2^15): its values keep
 //     bfloat16's 8 bits down to 2^-31 of that.
 //
-// Units, shares and the join are those of attn_work.cuh, with tiles of 128 keys. Two
-// blocks an SM. A producer warp walks over the share and loads tiles (codes
-// swizzled, one box a page, scales beside them) into a ring; each of eight warps takes
-// 16 keys of every tile, with references, sums and outputs of its own, which are put
-// together at the end of a piece in the ring's last stage. References are raised when a lane
-// finds that one has to be (a vote a tile), so no maxima go over lanes otherwise.
+// Units, shares and the join are those of attn_work.cuh, for groups of KH KV heads (the query
+// heads of a group count as those of one KV head; a tile has 128 / KH keys of each): with
+// tokens outside heads, a head's row of codes is 128 bytes, and memory gives those at 5.1
+// TB/s one head at a time (128 requests of 4000 cached), neighbours together at MEASURED.
+// Two blocks an SM. A producer warp walks over the share and loads tiles (codes
+// swizzled, a box a page and head, scales beside them) into a ring. Each of the other
+// warps takes 16 keys of every tile of one head (32 where there are four), with references, sums
+// and outputs of its own. References are raised when a lane finds that one has to be (a vote
+// a tile), so no maxima go over lanes otherwise. At a piece's end a warp puts its outputs where
+// its last keys' codes were, and a head's warps add them up; the next piece's q
+// is on its way meanwhile.
 //
 // Products of a warp (m16n8k16), keys or dimensions down, rows of q across:
 //   S^T[16 keys][8 rows] = K[16][D] Q^T: lane 4 g + t holds D / 4 consecutive codes of keys g and
@@ -45,7 +50,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = kAttnTileTc;               // keys of a tile
+constexpr int kTile = kAttnTileTc;               // keys of a tile, over the heads of a group
 constexpr int kAhead = 4;                        // pieces handed out ahead
 constexpr float kTop = 15.5f, kRaised = 12.f;    // largest exponent of a weight, and after a raise
 constexpr float kSlack = 20.f;                   // growth of the sum's exponents
@@ -58,28 +63,28 @@ struct Stage {
   static constexpr int kCount = D == 128 ? 3 : 6;
 };
 
-template <int D, int NT, int kWarps>
+template <int D, int NT, int KH, int kWarps>
 struct Shared {
   Piece piece[kAhead];
   uint64_t piece_full[kAhead], piece_empty[kAhead];
-  uint64_t full[Stage<D>::kCount], empty[Stage<D>::kCount], met;
-  float2 stat[kWarps][8 * NT];  // a piece's references and sums
+  uint64_t full[Stage<D>::kCount], empty[Stage<D>::kCount], met[KH];
+  float2 stat[2][kWarps][8 * NT];  // references and sums of a piece, and of the one before
   int abort;
   ShareStart<32 * (kWarps + 1), 1> work;
   alignas(16) uint8_t scale[Stage<D>::kCount][2][kTile];
 };
 
-template <int D, int NT, int kWarps>
+template <int D, int NT, int KH, int kWarps>
 constexpr uint32_t header_bytes() {
-  return (uint32_t)(sizeof(Shared<D, NT, kWarps>) + 1023) / 1024 * 1024;
+  return (uint32_t)(sizeof(Shared<D, NT, KH, kWarps>) + 1023) / 1024 * 1024;
 }
-template <int D, int NT, int kWarps>
+template <int D, int NT, int KH, int kWarps>
 constexpr uint32_t smem_bytes() {
-  return header_bytes<D, NT, kWarps>() + Stage<D>::kCount * Stage<D>::kBytes;
+  return header_bytes<D, NT, KH, kWarps>() + Stage<D>::kCount * Stage<D>::kBytes;
 }
 
-template <int NT>
-struct FormFew : WorkForm<kTile, kMaxShares, 8 * NT, true> {};
+template <int NT, int KH>
+struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true> {};
 
 // By all lanes of a warp; false once a wait has given up (after about a second, a minute
 // with more polls).
@@ -121,19 +126,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A meeting of the warps with keys: a barrier with a limit, since one that has given up
-// elsewhere does not come.
-struct Meeting {
-  uint32_t parity = 0;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, volatile int* abort) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    const bool ok = wait_warp(bar, parity, abort);
-    parity ^= 1;
-    return ok;
-  }
-};
-
 // A scale's power of two, and its exponent.
 __device__ __forceinline__ float power_of(uint32_t s) {
   return __uint_as_float(s == 255 ? 0x7fc00000u : s == 0 ? 0x00400000u : s << 23);
@@ -142,20 +134,28 @@ __device__ __forceinline__ float exponent_of(uint32_t s) {
   return s == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(0x4b000000u | s) - 8388735.f;  // 2^23 + 127
 }
 
-// NT times 8 rows, kWarps warps with keys and the producer.
-template <int D, int NT, int kWarps>
+// The query heads of one KV head: in the parameters a group of KH heads counts as one.
+struct Heads {
+  int32_t group, n_kv_heads;
+  Divisor by_group;
+};
+
+// NT times 8 rows a KV head, kWarps warps with keys and the producer.
+template <int D, int NT, int KH, int kWarps>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
-    attn_e4m3_few_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
-  using F = FormFew<NT>;
+    attn_e4m3_few_kernel(const AttnParams p, const Heads hd, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV) {
+  using F = FormFew<NT, KH>;
   using St = Stage<D>;
-  using S = Shared<D, NT, kWarps>;
-  constexpr int kThreads = 32 * (kWarps + 1);
-  static_assert(kTile % (16 * kWarps) == 0 && kWarps * 8 * D * 4 <= (int)St::kBytes, "keys of a warp, sums in a stage");
+  using S = Shared<D, NT, KH, kWarps>;
+  constexpr int kThreads = 32 * (kWarps + 1), kHeadWarps = kWarps / KH;
+  constexpr int kKeys = kTile / KH, kWarpKeys = kTile / kWarps;  // keys of a tile, of a warp of it
+  static_assert(kWarpKeys % 16 == 0 && 4 * NT * D * 4 <= kWarpKeys * D, "a warp's outputs in its keys' places");
   constexpr int kStages = St::kCount;
-  constexpr int kRows = 8 * NT;
+  constexpr int kRows = 8 * NT * KH;
   extern __shared__ __align__(1024) uint8_t smem[];
   S& sh = *reinterpret_cast<S*>(smem);
-  uint8_t* ring = smem + header_bytes<D, NT, kWarps>();
+  uint8_t* ring = smem + header_bytes<D, NT, KH, kWarps>();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool misplaced = (smem_u32(smem) & 1023u) != 0;  // (the swizzle is taken from address bits)
   if (tid == 0) {
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], kWarps);
     }
-    mbar_init(&sh.met, kWarps);
+    for (int i = 0; i < KH; ++i) mbar_init(&sh.met[i], kHeadWarps);
     sh.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tmK);
@@ -192,7 +192,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer
     const int shift = p.pool.page_shift, page_size = 1 << shift;
-    const int rows = min(page_size, kTile), boxes = kTile / rows;  // keys of a box, pages of a tile
+    const int rows = min(page_size, kKeys), boxes = kKeys / rows;  // keys of a box, pages of a tile
+    const int box = lane % boxes, sub = lane / boxes;              // a lane's page and head of a tile
+    const int64_t scale_part = (int64_t)hd.n_kv_heads << shift;
     Walk<F> wk;
     wk.start(begin, end, sh.work, 0);
     bool ok = true;
@@ -208,11 +210,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
       }
       if (x.n < 0) break;
       const int32_t* table = p.block_table + (int64_t)x.b * p.max_pages;
-      // Table entry of this lane's box of a tile, kNoPage: no row sees it.
+      const int head = x.h * KH + sub;
+      // Table entry of this lane's page of a tile, kNoPage: no row sees it.
       constexpr int kNoPage = INT32_MIN;
       auto page_of = [&](int tile) {
-        const int key = tile * kTile + lane * rows;
-        if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return kNoPage;
+        const int key = tile * kKeys + box * rows;
+        if (sub >= KH || key >= x.hi || key + rows <= x.lo) return kNoPage;
         return __ldcg(table + (key >> shift));
       };
       int page = x.n > 0 ? page_of(x.tile0) : kNoPage;
@@ -225,19 +228,19 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
           now = 0;
         }
         const uint32_t some = __ballot_sync(0xffffffffu, now != kNoPage);
-        const int token = (tile * kTile) & (page_size - 1);
+        const int token = (tile * kKeys) & (page_size - 1);
         ok = wait_warp(&sh.empty[stage], parity ^ 1, abort);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * rows * (D + 1));
         __syncwarp();
-        // a lane a box
         if (now != kNoPage) {
-          uint8_t* to = ring + stage * St::kBytes + lane * rows * D;
-          const uint8_t* from = p.pool.scales + 2 * (int64_t)now * p.pool.scale_part() + ((int64_t)x.h << shift) + token;
-          tma_load_4d_plain(to, &tmK, &sh.full[stage], 0, token, x.h, now);
-          tma_load_4d_plain(to + St::kCodes, &tmV, &sh.full[stage], 0, token, x.h, now);
-          bulk_load(&sh.scale[stage][0][lane * rows], from, rows, &sh.full[stage]);
-          bulk_load(&sh.scale[stage][1][lane * rows], from + p.pool.scale_part(), rows, &sh.full[stage]);
+          const int at = sub * kKeys + box * rows;
+          uint8_t* to = ring + stage * St::kBytes + at * D;
+          const uint8_t* from = p.pool.scales + 2 * (int64_t)now * scale_part + ((int64_t)head << shift) + token;
+          tma_load_4d_plain(to, &tmK, &sh.full[stage], 0, token, head, now);
+          tma_load_4d_plain(to + St::kCodes, &tmV, &sh.full[stage], 0, token, head, now);
+          bulk_load(&sh.scale[stage][0][at], from, rows, &sh.full[stage]);
+          bulk_load(&sh.scale[stage][1][at], from + scale_part, rows, &sh.full[stage]);
         }
         __syncwarp();
         if (++stage == kStages) {
@@ -249,339 +252,354 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
   } else {
     // ------------------------------------------------------------------ keys
     const int g = lane >> 2, t = lane & 3;
+    const int sub = warp / kHeadWarps, of_head = warp % kHeadWarps;  // its head of the group, its place there
     const float c = p.scale * kLog2eHi;
     const bool tree = p.mask != nullptr;
-    Meeting meet;
-    for (uint32_t np = 0;; ++np) {
-      const uint32_t at = np % kAhead;
-      if (!wait_warp(&sh.piece_full[at], (np / kAhead) & 1, abort, kPolls << 6)) break;
-      // (read where it is used, to keep the loop's registers few; released at the piece's end)
-      const volatile Piece& x = sh.piece[at];
-      const int n_tiles = x.n, tile0 = x.tile0;
-      if (n_tiles < 0) break;
-      auto head_of = [&](int row, int64_t& tok_row) {  // query head of a row, and its row of q
-        const int tok = p.by_group.quotient(x.off + row);
-        tok_row = x.token + tok;
-        return x.h * p.group + x.off + row - tok * p.group;
-      };
-      if (n_tiles == 0) {
-        for (int i = tid; i < x.rows * (D / 8); i += 32 * kWarps) {
-          int64_t tr;
-          const int row = i / (D / 8), head = head_of(row, tr);
-          reinterpret_cast<uint4*>(p.out + tr * p.o_token + head * p.o_head)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
-          if (i % (D / 8) == 0 && p.lse != nullptr) p.lse[tr * p.n_heads + head] = kNegInf;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.piece_empty[at]);
-        continue;
-      }
-      // q as the products take it: row g of each eight, D / 4 columns from (D / 4) t
-      uint32_t q[NT][D / 8];
-      float c_row[NT][2];       // of rows 2 t, 2 t + 1 of each eight: factor of their scores
-      int lo_all = x.lo, hi_all = x.hi;  // keys that all rows see
-      // keys that a row sees (of a tree's row: of the context), and its row of q
-      auto range_of = [&](int row, int& lo, int& hi) -> int64_t {
-        const int tok = p.by_group.quotient(x.off + row), pos = x.pos + tok;
-        const int64_t tr = x.token + tok;
-        hi = tree ? x.ctx : p.causal ? min(pos + 1, x.kv) : x.kv;
-        lo = tree ? tree_low(p, x.ctx, tr) : p.window > 0 ? max(0, pos - p.window + 1) : 0;
-        return tr;
-      };
+    uint4 w_q[NT][D / 32];  // a piece's q as it is loaded: row g of each eight, D / 4 columns from (D / 4) t
+    // Row of q and head of a row of this warp's head; its place among the unit's rows.
+    auto place_of = [&](const volatile Piece& x, int row, int64_t& tr, int& head) {
+      const int tok = hd.by_group.quotient(row), in = sub * hd.group + row - tok * hd.group;
+      tr = x.token + tok;
+      head = x.h * p.group + in;
+      return tok * p.group + in;
+    };
+    auto load_q = [&](const volatile Piece& x) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint4 w[D / 32];
         int64_t tr;
-        const int row = 8 * n + g, head = head_of(row, tr);
-        const bool there = row < x.rows;
+        int head;
+        const bool there = place_of(x, 8 * n + g, tr, head) < x.rows;
         const uint4* from = reinterpret_cast<const uint4*>(p.q + tr * p.q_token + head * p.q_head) + t * (D / 32);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) w[i] = there ? __ldcg(from + i) : make_uint4(0, 0, 0, 0);
-        uint32_t top = 0;
-        constexpr uint32_t kAbs = 0x7fff7fffu;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & kAbs, w[i].y & kAbs), __vmaxu2(w[i].z & kAbs, w[i].w & kAbs)));
-        top = max(top & 0xffffu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t up = min(268u - (top >> 7), 253u);  // exponent field of 2^(14 - E), largest value 2^E and more
-        const float f = __uint_as_float(up << 23), down = __uint_as_float((254u - up) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            q[n][4 * i + k] = to_f16x2(__uint_as_float(y[k] << 16) * f, __uint_as_float(y[k] & 0xffff0000u) * f);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          c_row[n][i] = c * __shfl_sync(0xffffffffu, down, 4 * (2 * t + i));
-          const int r = 8 * n + 2 * t + i;
-          int lo, hi;
-          if (r < x.rows) {
-            range_of(r, lo, hi);
-            lo_all = max(lo_all, lo);
-            hi_all = min(hi_all, hi);
-          }
-        }
+        for (int i = 0; i < D / 32; ++i) w_q[n][i] = there ? __ldcg(from + i) : make_uint4(0, 0, 0, 0);
       }
-      lo_all = __reduce_max_sync(0xffffffffu, lo_all);
-      hi_all = __reduce_min_sync(0xffffffffu, hi_all);
-      const int lo_any = x.lo, hi_any = x.hi;
-      float r[NT][2], rv[NT][2], l[NT][2];  // references of the sum and of the weights, sum
-      float o[NT][D / 16][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          r[n][i] = rv[n][i] = -FLT_MAX;
-          l[n][i] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
-      }
-      bool ok = true;
-      for (int it = 0; it < n_tiles; ++it) {
-        ok = wait_warp(&sh.full[stage], parity, abort);
-        if (!ok) break;
-#pragma unroll 1
-        for (int sub = warp; sub < kTile / 16; sub += kWarps) {
-          const int key0 = (tile0 + it) * kTile + 16 * sub;
-          if (key0 + 16 <= lo_any || key0 >= hi_any) continue;
-          const uint8_t* kc = ring + stage * St::kBytes;
-          const uint8_t* vc = kc + St::kCodes;
-          const uint8_t* sc = &sh.scale[stage][0][16 * sub];
-          float ks[2], ev[2];  // of keys g, g + 8
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ks[i] = power_of(sc[g + 8 * i]);
-            ev[i] = exponent_of(sc[kTile + g + 8 * i]);
-          }
-          float s[NT][4];  // key g: rows 2 t, 2 t + 1; key g + 8
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-          {
-            uint4 w[2][D / 64];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = 16 * sub + g + 8 * i;
-#pragma unroll
-              for (int k = 0; k < D / 64; ++k) {
-                const int chunk = D == 128 ? (2 * t + k) ^ (row & 7) : t ^ ((row >> 1) & 3);
-                w[i][k] = *reinterpret_cast<const uint4*>(kc + row * D + chunk * 16);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint4 &y = w[0][k / 4], &z = w[1][k / 4];
-              const uint32_t a = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
-              const uint32_t b = k % 4 == 0 ? z.x : k % 4 == 1 ? z.y : k % 4 == 2 ? z.z : z.w;
-              const uint32_t f[4] = {halves_lo(a), halves_lo(b), halves_hi(a), halves_hi(b)};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma_f16(s[n], f, q[n][2 * k], q[n][2 * k + 1]);
-            }
-          }
-          // the values' codes: 4 keys
-          constexpr int kVW = D / 32;  // words of a key
-          uint32_t w[4][kVW];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 16 * sub + 2 * t + (i & 1) + 8 * (i >> 1);
-            if constexpr (D == 128) {
-              const uint4 y = *reinterpret_cast<const uint4*>(vc + row * D + ((g ^ (row & 7)) << 4));
-              w[i][0] = y.x;
-              w[i][1] = y.y;
-              w[i][kVW - 2] = y.z;
-              w[i][kVW - 1] = y.w;
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(vc + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-              w[i][0] = y.x;
-              w[i][1] = y.y;
-            }
-          }
-          float e[NT][4];  // exponents of the weights in the sum
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= ks[i >> 1];
-          if (key0 < lo_all || key0 + 16 > hi_all) {
-            uint32_t any = 0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t seen = 0;
-                const int row = 8 * n + 2 * t + i;
-                if (row < x.rows) {
-                  int lo, hi;
-                  const int64_t tr = range_of(row, lo, hi);
-                  seen = tree ? tree_seen(p.mask + tr * p.mask_words, p.mask_words, key0, lo, hi, x.kv)
-                              : bits_between(lo - key0, hi - key0);
-                }
-                any |= seen;
-                if (!(seen >> g & 1)) s[n][i] = kNegInf;
-                if (!(seen >> (g + 8) & 1)) s[n][2 + i] = kNegInf;
-              }
-            // keys that no row sees may hold anything: their values become zeros
-            any |= __shfl_xor_sync(0xffffffffu, any, 1);
-            any |= __shfl_xor_sync(0xffffffffu, any, 2);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (!(any >> (g + 8 * i) & 1)) ev[i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(any >> (2 * t + (i & 1) + 8 * (i >> 1)) & 1))
-#pragma unroll
-                for (int k = 0; k < kVW; ++k) w[i][k] = 0;
-          }
-          bool raise = false;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[n][i] = s[n][i] * c_row[n][i & 1];
-              raise |= e[n][i] - r[n][i & 1] > kSlack || e[n][i] + ev[i >> 1] - rv[n][i & 1] > kTop;
-            }
-          if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float a = fmaxf(e[n][i], e[n][2 + i]), b = fmaxf(e[n][i] + ev[0], e[n][2 + i] + ev[1]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                  b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-                }
-                if (a - r[n][i] > kSlack) {
-                  l[n][i] *= ex2_approx(r[n][i] - a);
-                  r[n][i] = a;
-                }
-                if (b - rv[n][i] > kTop) {
-                  const float f = ex2_approx(rv[n][i] - (b - kRaised));
-                  rv[n][i] = b - kRaised;
-#pragma unroll
-                  for (int j = 0; j < D / 16; ++j) {
-                    o[n][j][i] *= f;
-                    o[n][j][2 + i] *= f;
-                  }
-                }
-              }
-          }
-          uint32_t b0[NT], b1[NT];
+    };
+    uint32_t met = 0;
+    if (wait_warp(&sh.piece_full[0], 0, abort, kPolls << 6)) {
+      if (sh.piece[0].n > 0) load_q(sh.piece[0]);
+      for (uint32_t np = 0;; ++np) {
+        // (read where it is used, to keep the loop's registers few; released at the piece's end)
+        const volatile Piece& x = sh.piece[np % kAhead];
+        const int n_tiles = x.n, tile0 = x.tile0;
+        if (n_tiles < 0) break;
+        // keys that a row sees (of a tree's row: of the context), and its row of q
+        auto range_of = [&](int row, int& lo, int& hi) -> int64_t {
+          const int tok = hd.by_group.quotient(row), pos = x.pos + tok;
+          const int64_t tr = x.token + tok;
+          hi = tree ? x.ctx : p.causal ? min(pos + 1, x.kv) : x.kv;
+          lo = tree ? tree_low(p, x.ctx, tr) : p.window > 0 ? max(0, pos - p.window + 1) : 0;
+          return tr;
+        };
+        const int n_rows = x.rows / KH;  // of this warp's head
+        uint32_t q[NT][D / 8];
+        float c_row[NT][2];                // of rows 2 t, 2 t + 1 of each eight: factor of their scores
+        int lo_all = x.lo, hi_all = x.hi;  // keys that all rows see
+        const int lo_any = x.lo, hi_any = x.hi;
+        float r[NT][2], dv[NT][2], l[NT][2];  // reference of the sum, and less that of the weights; sum
+        float o[NT][D / 16][4];
+        if (n_tiles > 0) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float v[4];
+            uint32_t top = 0;
+            constexpr uint32_t kAbs = 0x7fff7fffu;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint4 y = w_q[n][i];
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & kAbs, y.y & kAbs), __vmaxu2(y.z & kAbs, y.w & kAbs)));
+            }
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t up = min(268u - (top >> 7), 253u);  // exponent field of 2^(14 - E), largest value 2^E and more
+            const float f = __uint_as_float(up << 23), down = __uint_as_float((254u - up) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint32_t y[4] = {w_q[n][i].x, w_q[n][i].y, w_q[n][i].z, w_q[n][i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                q[n][4 * i + k] = to_f16x2(__uint_as_float(y[k] << 16) * f, __uint_as_float(y[k] & 0xffff0000u) * f);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              c_row[n][i] = fmaxf(c * __shfl_sync(0xffffffffu, down, 4 * (2 * t + i)), __int_as_float(1));  // (never 0)
+              const int row = 8 * n + 2 * t + i;
+              int lo, hi;
+              if (row < n_rows) {
+                range_of(row, lo, hi);
+                lo_all = max(lo_all, lo);
+                hi_all = min(hi_all, hi);
+              }
+              r[n][i] = -FLT_MAX;
+              dv[n][i] = 0.f;
+              l[n][i] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
+          }
+          lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+          hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+        }
+        bool ok = true;
+        for (int it = 0; it < n_tiles; ++it) {
+          ok = wait_warp(&sh.full[stage], parity, abort);
+          if (!ok) break;
+#pragma unroll 1
+          for (int k0 = 0; k0 < kWarpKeys; k0 += 16) {
+            const int row0 = of_head * kWarpKeys + k0;  // of the tile's keys of this head
+            const int key0 = (tile0 + it) * kKeys + row0;
+            if (key0 + 16 <= lo_any || key0 >= hi_any) continue;
+            const uint8_t* kc = ring + stage * St::kBytes + (sub * kKeys + row0) * D;
+            const uint8_t* vc = kc + St::kCodes;
+            const uint8_t* sc = &sh.scale[stage][0][sub * kKeys + row0];
+            float ks[2], ev[2];  // of keys g, g + 8
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              ks[i] = power_of(sc[g + 8 * i]);
+              ev[i] = exponent_of(sc[kTile + g + 8 * i]);
+            }
+            float s[NT][4], s2[NT][4];  // key g: rows 2 t, 2 t + 1; key g + 8 (two chains of products)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.f;
+            {
+              uint4 w[2][D / 64];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = g + 8 * i;
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k) {
+                  const int chunk = D == 128 ? (2 * t + k) ^ (row & 7) : t ^ ((row >> 1) & 3);
+                  w[i][k] = *reinterpret_cast<const uint4*>(kc + row * D + chunk * 16);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint4 &y = w[0][k / 4], &z = w[1][k / 4];
+                const uint32_t a = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
+                const uint32_t b = k % 4 == 0 ? z.x : k % 4 == 1 ? z.y : k % 4 == 2 ? z.z : z.w;
+                const uint32_t f[4] = {halves_lo(a), halves_lo(b), halves_hi(a), halves_hi(b)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(k & 1 ? s2[n] : s[n], f, q[n][2 * k], q[n][2 * k + 1]);
+              }
+            }
+            // the values' codes: 4 keys
+            constexpr int kVW = D / 32;  // words of a key
+            uint32_t w[4][kVW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              l[n][i & 1] += ex2_approx(e[n][i] - r[n][i & 1]);
-              // (where a key is not seen, its value's scale may be NaN)
-              v[i] = e[n][i] == kNegInf ? 0.f : ex2_approx(e[n][i] + (ev[i >> 1] - rv[n][i & 1]));
+              const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+              if constexpr (D == 128) {
+                const uint4 y = *reinterpret_cast<const uint4*>(vc + row * D + ((g ^ (row & 7)) << 4));
+                w[i][0] = y.x;
+                w[i][1] = y.y;
+                w[i][kVW - 2] = y.z;
+                w[i][kVW - 1] = y.w;
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2*>(vc + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                w[i][0] = y.x;
+                w[i][1] = y.y;
+              }
             }
-            b0[n] = transpose8(to_f16x2(v[0], v[1]));
-            b1[n] = transpose8(to_f16x2(v[2], v[3]));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[n][i] = (s[n][i] + s2[n][i]) * ks[i >> 1];
+            if (key0 < lo_all || key0 + 16 > hi_all) {
+              uint32_t any = 0;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t seen = 0;
+                  const int row = 8 * n + 2 * t + i;
+                  if (row < n_rows) {
+                    int lo, hi;
+                    const int64_t tr = range_of(row, lo, hi);
+                    seen = tree ? tree_seen(p.mask + tr * p.mask_words, p.mask_words, key0, lo, hi, x.kv)
+                                : bits_between(lo - key0, hi - key0);
+                  }
+                  any |= seen;
+                  if (!(seen >> g & 1)) s[n][i] = kNegInf;
+                  if (!(seen >> (g + 8) & 1)) s[n][2 + i] = kNegInf;
+                }
+              // keys that no row sees may hold anything: their values become zeros
+              any |= __shfl_xor_sync(0xffffffffu, any, 1);
+              any |= __shfl_xor_sync(0xffffffffu, any, 2);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (!(any >> (g + 8 * i) & 1)) ev[i] = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(any >> (2 * t + (i & 1) + 8 * (i >> 1)) & 1))
+#pragma unroll
+                  for (int k = 0; k < kVW; ++k) w[i][k] = 0;
+            }
+            // exponents over the references: of the sum's terms, of the weights
+            float e[NT][4], ew[NT][4], top_e = kNegInf, top_w = kNegInf;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e[n][i] = fmaf(s[n][i], c_row[n][i & 1], -r[n][i & 1]);
+                ew[n][i] = e[n][i] + (ev[i >> 1] + dv[n][i & 1]);
+                top_e = fmaxf(top_e, e[n][i]);
+                top_w = fmaxf(top_w, ew[n][i]);
+              }
+            if (__any_sync(0xffffffffu, top_e > kSlack || top_w > kTop)) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float y0 = s[n][i] * c_row[n][i], y1 = s[n][2 + i] * c_row[n][i];
+                  float a = fmaxf(y0, y1), b = fmaxf(y0 + ev[0], y1 + ev[1]);
+#pragma unroll
+                  for (int d = 4; d < 32; d <<= 1) {
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                    b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+                  }
+                  float rv = r[n][i] - dv[n][i];
+                  if (a - r[n][i] > kSlack) {
+                    l[n][i] *= ex2_approx(r[n][i] - a);
+                    r[n][i] = a;
+                  }
+                  if (b - rv > kTop) {
+                    const float f = ex2_approx(rv - (b - kRaised));
+                    rv = b - kRaised;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                      o[n][j][i] *= f;
+                      o[n][j][2 + i] *= f;
+                    }
+                  }
+                  dv[n][i] = r[n][i] - rv;
+                  e[n][i] = y0 - r[n][i];
+                  e[n][2 + i] = y1 - r[n][i];
+                  ew[n][i] = e[n][i] + (ev[0] + dv[n][i]);
+                  ew[n][2 + i] = e[n][2 + i] + (ev[1] + dv[n][i]);
+                }
+            }
+            uint32_t b0[NT], b1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                l[n][i & 1] += ex2_approx(e[n][i]);
+                // (where a key is not seen, its value's scale may be NaN)
+                v[i] = e[n][i] == kNegInf ? 0.f : ex2_approx(ew[n][i]);
+              }
+              b0[n] = transpose8(to_f16x2(v[0], v[1]));
+              b1[n] = transpose8(to_f16x2(v[2], v[3]));
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+              const uint32_t a = __byte_perm(w[0][j / 2], w[1][j / 2], sel), b = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
+              const uint32_t f[4] = {halves_lo(a), halves_hi(a), halves_lo(b), halves_hi(b)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(o[n][j], f, b0[n], b1[n]);
+            }
           }
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
-            const uint32_t a = __byte_perm(w[0][j / 2], w[1][j / 2], sel), b = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-            const uint32_t f[4] = {halves_lo(a), halves_hi(a), halves_lo(b), halves_hi(b)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[n][j], f, b0[n], b1[n]);
+          __syncwarp();
+          if (it + 1 < n_tiles) {
+            if (lane == 0) mbar_arrive(&sh.empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              parity ^= 1;
+            }
           }
         }
-        __syncwarp();
-        if (it + 1 < n_tiles) {
+        if (!ok) break;
+        // the next piece, which the producer has handed out by now as a rule, and its q
+        const uint32_t nx = (np + 1) % kAhead;
+        ok = wait_warp(&sh.piece_full[nx], ((np + 1) / kAhead) & 1, abort, kPolls << 6);
+        if (!ok) break;
+        if (sh.piece[nx].n > 0) load_q(sh.piece[nx]);
+        if (n_tiles > 0) {
+          // The outputs on the warp's own reference, four rows of each eight in the places of its
+          // keys and four in those of its values (16-byte pieces so that accesses do not collide).
+          float2(&stat)[kWarps][8 * NT] = sh.stat[np & 1];
+          constexpr int kChunks = D / 4;
+          auto place = [&](int w, int n, int row) {
+            return reinterpret_cast<float4*>(ring + stage * St::kBytes + (row >> 2) * St::kCodes +
+                                             (sub * kKeys + w * kWarpKeys) * D + (n * 4 + (row & 3)) * (D * 4));
+          };
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+              if (g == 0) stat[warp][8 * n + 2 * t + i] = make_float2(r[n][i], l[n][i]);
+              // (in two halves: values at the ends of bfloat16's range have factors past float32's)
+              const float f = ex2_approx(-0.5f * dv[n][i]);
+              float4* to = place(of_head, n, 2 * t + i);
+              // a lane's D / 8 columns from (D / 8) g: two a product
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                to[(g * (D / 32) + k) ^ t] = make_float4(o[n][2 * k][i] * f * f, o[n][2 * k][2 + i] * f * f,
+                                                         o[n][2 * k + 1][i] * f * f, o[n][2 * k + 1][2 + i] * f * f);
+            }
+          // a head's warps meet (with a limit: one that has given up elsewhere does not come)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.met[sub]);
+          ok = wait_warp(&sh.met[sub], met & 1, abort);
+          ++met;
+          if (!ok) break;
+          for (int i = of_head * 32 + lane; i < n_rows * kChunks; i += 32 * kHeadWarps) {
+            const int row = i / kChunks, chunk = i % kChunks;
+            float top = -FLT_MAX, sum = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kHeadWarps; ++w) top = fmaxf(top, stat[sub * kHeadWarps + w][row].x);
+#pragma unroll
+            for (int w = 0; w < kHeadWarps; ++w) {
+              const float2 st = stat[sub * kHeadWarps + w][row];
+              const float4 z = place(w, row >> 3, row & 7)[chunk ^ ((row & 7) >> 1)];
+              const float f = ex2_approx(st.x - top);
+              if (st.y == 0.f) continue;  // saw nothing
+              sum = fmaf(st.y, f, sum);
+              y = make_float4(fmaf(z.x, f, y.x), fmaf(z.y, f, y.y), fmaf(z.z, f, y.z), fmaf(z.w, f, y.w));
+            }
+            const bool some = sum > 0.f || sum != sum;
+            const float f = !x.whole ? 1.f : some ? 1.f / sum : 0.f;
+            int64_t tr;
+            int head;
+            const size_t prow = (size_t)(share * 2 + x.slot) * F::kPartRows + place_of(x, row, tr, head);
+            if (x.whole)
+              reinterpret_cast<uint2*>(p.out + tr * p.o_token + head * p.o_head)[chunk] =
+                  make_uint2(to_bf16x2(y.x * f, y.y * f), to_bf16x2(y.z * f, y.w * f));
+            else
+              reinterpret_cast<float4*>(part.out + prow * D)[chunk] = y;
+            if (chunk == 0) {
+              if (!x.whole)
+                part.stat[prow] = make_float2(some ? top : kNegInf, sum);
+              else if (p.lse != nullptr)
+                p.lse[tr * p.n_heads + head] = some ? (top + log2f(sum)) * kLn2 : kNegInf;
+            }
+          }
+          fence_proxy_async_smem();  // the stage's next filling comes by TMA
+          __syncwarp();
           if (lane == 0) mbar_arrive(&sh.empty[stage]);
           if (++stage == kStages) {
             stage = 0;
             parity ^= 1;
           }
-        }
-      }
-      if (!ok) break;
-      // The warps' sums on one reference, eight rows at a time through the last tile's stage
-      // (16-byte pieces placed so that neither side's accesses collide).
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
-          if (g == 0) sh.stat[warp][8 * n + 2 * t + i] = make_float2(r[n][i], l[n][i]);
-        }
-      if (!meet(&sh.met, abort)) break;
-      float4* sums = reinterpret_cast<float4*>(ring + stage * St::kBytes);
-      constexpr int kChunks = D / 4;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = 2 * t + i;
-          float top = -FLT_MAX;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.stat[w][8 * n + row].x);
-          // (in two halves: values at the ends of bfloat16's range have factors past float32's)
-          const float f = rv[n][i] == -FLT_MAX ? 0.f : ex2_approx(0.5f * (rv[n][i] - top));
-          // a lane's D / 8 columns from (D / 8) g: two a product
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            const int chunk = g * (D / 32) + k;
-            sums[(warp * 8 + row) * kChunks + (chunk ^ t)] =
-                make_float4(o[n][2 * k][i] * f * f, o[n][2 * k][2 + i] * f * f, o[n][2 * k + 1][i] * f * f,
-                            o[n][2 * k + 1][2 + i] * f * f);
+        } else {
+          // nothing to see
+          for (int i = of_head * 32 + lane; i < n_rows * (D / 8); i += 32 * kHeadWarps) {
+            int64_t tr;
+            int head;
+            place_of(x, i / (D / 8), tr, head);
+            reinterpret_cast<uint4*>(p.out + tr * p.o_token + head * p.o_head)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+            if (i % (D / 8) == 0 && p.lse != nullptr) p.lse[tr * p.n_heads + head] = kNegInf;
           }
+          __syncwarp();
         }
-        ok = meet(&sh.met, abort);
-        if (!ok) break;
-        for (int i = tid; i < 8 * kChunks; i += 32 * kWarps) {
-          const int row = i / kChunks, chunk = i % kChunks, urow = 8 * n + row;
-          if (urow >= x.rows) continue;
-          float top = -FLT_MAX, sum = 0.f;
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.stat[w][urow].x);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 st = sh.stat[w][urow];
-            const float4 z = sums[(w * 8 + row) * kChunks + (chunk ^ (row >> 1))];
-            sum += st.y * ex2_approx(st.x - top);
-            y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
-          }
-          const bool some = sum > 0.f || sum != sum;
-          const float f = !x.whole ? 1.f : some ? 1.f / sum : 0.f;
-          int64_t tr;
-          const int head = head_of(urow, tr);
-          const size_t prow = (size_t)(share * 2 + x.slot) * F::kPartRows + urow;
-          if (x.whole)
-            reinterpret_cast<uint2*>(p.out + tr * p.o_token + head * p.o_head)[chunk] =
-                make_uint2(to_bf16x2(y.x * f, y.y * f), to_bf16x2(y.z * f, y.w * f));
-          else
-            reinterpret_cast<float4*>(part.out + prow * D)[chunk] = y;
-          if (chunk == 0) {
-            if (!x.whole)
-              part.stat[prow] = make_float2(some ? top : kNegInf, sum);
-            else if (p.lse != nullptr)
-              p.lse[tr * p.n_heads + head] = some ? (top + log2f(sum)) * kLn2 : kNegInf;
-          }
-        }
-        ok = meet(&sh.met, abort);
-        if (!ok) break;
-      }
-      if (!ok) break;
-      fence_proxy_async_smem();  // the stage's next filling comes by TMA
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh.empty[stage]);
-        mbar_arrive(&sh.piece_empty[at]);
-      }
-      if (++stage == kStages) {
-        stage = 0;
-        parity ^= 1;
+        if (lane == 0) mbar_arrive(&sh.piece_empty[np % kAhead]);
       }
     }
   }
@@ -592,32 +610,47 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
   }
 }
 
-template <int D, int NT, int kWarps>
-cudaError_t launch(const AttnParams& p, cudaStream_t s) {
+template <int D, int NT, int KH>
+cudaError_t launch(const AttnParams& given, cudaStream_t s) {
   static Readiness readiness;
-  constexpr uint32_t kSmem = smem_bytes<D, NT, kWarps>();
+  constexpr int kWarps = NT == 1 ? 8 : 4;  // (registers: 16 rows' outputs take twice those of 8)
+  constexpr uint32_t kSmem = smem_bytes<D, NT, KH, kWarps>();
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
-  const cudaError_t ready = readiness.get(
-      [] { return cudaFuncSetAttribute(attn_e4m3_few_kernel<D, NT, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+  const auto kernel = attn_e4m3_few_kernel<D, NT, KH, kWarps>;
+  const cudaError_t ready =
+      readiness.get([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (ready != cudaSuccess) return ready;
   CUtensorMap mk, mv;
-  const int page = 1 << p.pool.page_shift;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)p.pool.n_kv_heads, (cuuint64_t)p.pool.n_pages};
-  const cuuint64_t str[3] = {(cuuint64_t)p.pool.token_stride, (cuuint64_t)p.pool.head_stride, (cuuint64_t)p.pool.page_stride};
-  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(page < kTile ? page : kTile), 1, 1};
-  if (!encode_tmap_bytes(&mk, p.pool.k, 4, dims, str, box, true) || !encode_tmap_bytes(&mv, p.pool.v, 4, dims, str, box, true))
+  const int page = 1 << given.pool.page_shift, keys = kTile / KH;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)given.pool.n_kv_heads, (cuuint64_t)given.pool.n_pages};
+  const cuuint64_t str[3] = {(cuuint64_t)given.pool.token_stride, (cuuint64_t)given.pool.head_stride,
+                             (cuuint64_t)given.pool.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(page < keys ? page : keys), 1, 1};
+  if (!encode_tmap_bytes(&mk, given.pool.k, 4, dims, str, box, true) || !encode_tmap_bytes(&mv, given.pool.v, 4, dims, str, box, true))
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch_early(attn_e4m3_few_kernel<D, NT, kWarps>, dim3(kMaxShares), dim3(32 * (kWarps + 1)), kSmem, s, p, mk, mv);
+  const Heads heads = {given.group, given.pool.n_kv_heads, given.by_group};
+  AttnParams p = given;
+  p.group *= KH;
+  p.by_group.set((uint32_t)p.group);
+  p.pool.n_kv_heads /= KH;
+  const cudaError_t e = launch_early(kernel, dim3(kMaxShares), dim3(32 * (kWarps + 1)), kSmem, s, p, heads, mk, mv);
   if (e != cudaSuccess) return e;
-  return launch_join<FormFew<NT>, D, __nv_bfloat16>(p, s, p.max_q * p.group, 8 * NT, 8 * NT);
+  return launch_join<FormFew<NT, KH>, D, __nv_bfloat16>(p, s, p.max_q * p.group, 8 * NT * KH, 8 * NT * KH);
+}
+
+template <int D, int NT>
+cudaError_t launch_heads(const AttnParams& p, cudaStream_t s) {
+  if constexpr (D == 64 && NT == 1)
+    if (p.pool.n_kv_heads % 4 == 0) return launch<D, NT, 4>(p, s);
+  return p.pool.n_kv_heads % 2 == 0 ? launch<D, NT, 2>(p, s) : launch<D, NT, 1>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_e4m3_few(const AttnParams& p, cudaStream_t s) {
   const bool eight = p.max_q * p.group <= 8;
-  if (p.D == 128) return eight ? launch<128, 1, 8>(p, s) : launch<128, 2, 4>(p, s);
-  return eight ? launch<64, 1, 8>(p, s) : launch<64, 2, 4>(p, s);
+  if (p.D == 128) return eight ? launch_heads<128, 1>(p, s) : launch_heads<128, 2>(p, s);
+  return eight ? launch_heads<64, 1>(p, s) : launch_heads<64, 2>(p, s);
 }
 
 }  // namespace ds
