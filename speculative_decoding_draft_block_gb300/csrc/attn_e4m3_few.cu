@@ -70,7 +70,7 @@ struct Shared {
   uint64_t full[Stage<D>::kCount], empty[Stage<D>::kCount], met[KH];
   float2 stat[2][kWarps][8 * NT];  // references and sums of a piece, and of the one before
   int abort;
-  ShareStart<32 * (kWarps + 1), 1> work;
+  ShareStart<32 * (kWarps + 2), 1> work;
   alignas(16) uint8_t scale[Stage<D>::kCount][2][kTile];
 };
 
@@ -83,8 +83,9 @@ constexpr uint32_t smem_bytes() {
   return header_bytes<D, NT, KH, kWarps>() + Stage<D>::kCount * Stage<D>::kBytes;
 }
 
+// (A piece's beginning and end cost a block as much as three tiles: see launch_heads.)
 template <int NT, int KH>
-struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true> {};
+struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true, 3> {};
 
 // By all lanes of a warp; false once a wait has given up (after about a second, a minute
 // with more polls).
@@ -140,15 +141,15 @@ struct Heads {
   Divisor by_group;
 };
 
-// NT times 8 rows a KV head, kWarps warps with keys and the producer.
+// NT times 8 rows a KV head; kWarps warps with keys, one that walks over the share, one that loads.
 template <int D, int NT, int KH, int kWarps>
-__global__ void __launch_bounds__(32 * (kWarps + 1), 2)
+__global__ void __launch_bounds__(32 * (kWarps + 2), 2)
     attn_e4m3_few_kernel(const AttnParams p, const Heads hd, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
   using F = FormFew<NT, KH>;
   using St = Stage<D>;
   using S = Shared<D, NT, KH, kWarps>;
-  constexpr int kThreads = 32 * (kWarps + 1), kHeadWarps = kWarps / KH;
+  constexpr int kThreads = 32 * (kWarps + 2), kHeadWarps = kWarps / KH;
   constexpr int kKeys = kTile / KH, kWarpKeys = kTile / kWarps;  // keys of a tile, of a warp of it
   static_assert(kWarpKeys % 16 == 0 && 4 * NT * D * 4 <= kWarpKeys * D, "a warp's outputs in its keys' places");
   constexpr int kStages = St::kCount;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
   if (tid == 0) {
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&sh.piece_full[i], 1);
-      mbar_init(&sh.piece_empty[i], kWarps);
+      mbar_init(&sh.piece_empty[i], kWarps + 1);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -190,64 +191,87 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2)
   uint32_t stage = 0, parity = 0;
 
   if (warp == kWarps) {
-    // ------------------------------------------------------------------ producer
-    const int shift = p.pool.page_shift, page_size = 1 << shift;
-    const int rows = min(page_size, kKeys), boxes = kKeys / rows;  // keys of a box, pages of a tile
-    const int box = lane % boxes, sub = lane / boxes;              // a lane's page and head of a tile
-    const int64_t scale_part = (int64_t)hd.n_kv_heads << shift;
+    // ------------------------------------------------------------------ walk
     Walk<F> wk;
     wk.start(begin, end, sh.work, 0);
-    bool ok = true;
-    for (uint32_t np = 0; ok; ++np) {
+    for (uint32_t np = 0;; ++np) {
       const Piece x = wk.next(p, kRows, lane == 0 ? part.cut + share : nullptr, total);
       const uint32_t i = np % kAhead;
       // (a piece may be as long as the cache)
-      ok = wait_warp(&sh.piece_empty[i], ((np / kAhead) & 1) ^ 1, abort, kPolls << 6);
-      if (!ok) break;
+      if (!wait_warp(&sh.piece_empty[i], ((np / kAhead) & 1) ^ 1, abort, kPolls << 6)) break;
       if (lane == 0) {
         sh.piece[i] = x;
         mbar_arrive(&sh.piece_full[i]);
       }
       if (x.n < 0) break;
-      const int32_t* table = p.block_table + (int64_t)x.b * p.max_pages;
-      const int head = x.h * KH + sub;
-      // Table entry of this lane's page of a tile, kNoPage: no row sees it.
-      constexpr int kNoPage = INT32_MIN;
-      auto page_of = [&](int tile) {
-        const int key = tile * kKeys + box * rows;
-        if (sub >= KH || key >= x.hi || key + rows <= x.lo) return kNoPage;
-        return __ldcg(table + (key >> shift));
-      };
-      int page = x.n > 0 ? page_of(x.tile0) : kNoPage;
-      for (int j = 0; j < x.n; ++j) {
-        const int tile = x.tile0 + j;
-        int now = page;
-        if (j + 1 < x.n) page = page_of(tile + 1);
-        if (now != kNoPage && (now < 0 || now >= p.pool.n_pages)) {
-          report(p.status, kErrBounds);
-          now = 0;
-        }
-        const uint32_t some = __ballot_sync(0xffffffffu, now != kNoPage);
-        const int token = (tile * kKeys) & (page_size - 1);
-        ok = wait_warp(&sh.empty[stage], parity ^ 1, abort);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * rows * (D + 1));
+    }
+  } else if (warp == kWarps + 1) {
+    // ------------------------------------------------------------------ loads
+    const int shift = p.pool.page_shift, page_size = 1 << shift;
+    const int rows = min(page_size, kKeys), boxes = kKeys / rows;  // keys of a box, pages of a tile
+    const int box = lane % boxes, sub = lane / boxes;              // a lane's page and head of a tile
+    const int64_t scale_part = (int64_t)hd.n_kv_heads << shift;
+    constexpr int kNoPage = INT32_MIN;
+    const int32_t* table = nullptr;
+    int n = 0, tile0 = 0, lo = 0, hi = 0, head = 0, page = kNoPage, j = 0;
+    uint32_t np = 0;
+    // Table entry of this lane's page of a tile, kNoPage: no row sees it.
+    auto page_of = [&](int tile) {
+      const int key = tile * kKeys + box * rows;
+      if (sub >= KH || key >= hi || key + rows <= lo) return kNoPage;
+      return __ldcg(table + (key >> shift));
+    };
+    // the next piece with tiles (n < 0: there is none), and its first page
+    auto next_piece = [&] {
+      do {
+        const uint32_t i = np % kAhead;
+        if (!wait_warp(&sh.piece_full[i], (np / kAhead) & 1, abort, kPolls << 6)) return false;
+        const volatile Piece& x = sh.piece[i];
+        n = x.n;
+        tile0 = x.tile0;
+        lo = x.lo;
+        hi = x.hi;
+        head = x.h * KH + sub;
+        table = p.block_table + (int64_t)x.b * p.max_pages;
         __syncwarp();
-        if (now != kNoPage) {
-          const int at = sub * kKeys + box * rows;
-          uint8_t* to = ring + stage * St::kBytes + at * D;
-          const uint8_t* from = p.pool.scales + 2 * (int64_t)now * scale_part + ((int64_t)head << shift) + token;
-          tma_load_4d_plain(to, &tmK, &sh.full[stage], 0, token, head, now);
-          tma_load_4d_plain(to + St::kCodes, &tmV, &sh.full[stage], 0, token, head, now);
-          bulk_load(&sh.scale[stage][0][at], from, rows, &sh.full[stage]);
-          bulk_load(&sh.scale[stage][1][at], from + scale_part, rows, &sh.full[stage]);
-        }
-        __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
-        }
+        if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
+        ++np;
+      } while (n == 0);
+      j = 0;
+      if (n > 0) page = page_of(tile0);
+      return true;
+    };
+    bool ok = next_piece();
+    while (ok && n > 0) {
+      int now = page;
+      const int token = ((tile0 + j) * kKeys) & (page_size - 1), now_head = head;
+      if (now != kNoPage && (now < 0 || now >= p.pool.n_pages)) {
+        report(p.status, kErrBounds);
+        now = 0;
       }
+      const uint32_t some = __ballot_sync(0xffffffffu, now != kNoPage);
+      // (the next tile's page is on its way before the wait for a place for this one)
+      const bool last = ++j == n;
+      if (!last) page = page_of(tile0 + j);
+      ok = wait_warp(&sh.empty[stage], parity ^ 1, abort);
+      if (!ok) break;
+      if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * rows * (D + 1));
+      __syncwarp();
+      if (now != kNoPage) {
+        const int at = sub * kKeys + box * rows;
+        uint8_t* to = ring + stage * St::kBytes + at * D;
+        const uint8_t* from = p.pool.scales + 2 * (int64_t)now * scale_part + ((int64_t)now_head << shift) + token;
+        tma_load_4d_plain(to, &tmK, &sh.full[stage], 0, token, now_head, now);
+        tma_load_4d_plain(to + St::kCodes, &tmV, &sh.full[stage], 0, token, now_head, now);
+        bulk_load(&sh.scale[stage][0][at], from, rows, &sh.full[stage]);
+        bulk_load(&sh.scale[stage][1][at], from + scale_part, rows, &sh.full[stage]);
+      }
+      __syncwarp();
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+      if (last) ok = next_piece();
     }
   } else {
     // ------------------------------------------------------------------ keys
@@ -633,9 +657,9 @@ cudaError_t launch(const AttnParams& given, cudaStream_t s) {
   p.group *= KH;
   p.by_group.set((uint32_t)p.group);
   p.pool.n_kv_heads /= KH;
-  const cudaError_t e = launch_early(kernel, dim3(kMaxShares), dim3(32 * (kWarps + 1)), kSmem, s, p, heads, mk, mv);
+  const cudaError_t e = launch_early(kernel, dim3(kMaxShares), dim3(32 * (kWarps + 2)), kSmem, s, p, heads, mk, mv);
   if (e != cudaSuccess) return e;
-  return launch_join<FormFew<NT, KH>, D, __nv_bfloat16>(p, s, p.max_q * p.group, 8 * NT * KH, 8 * NT * KH);
+  return launch_join<FormFew<NT, KH>, D, __nv_bfloat16, 4>(p, s, p.max_q * p.group, 8 * NT * KH, 8 * NT * KH);
 }
 
 template <int D, int NT>

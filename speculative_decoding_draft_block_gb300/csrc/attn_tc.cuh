@@ -11,7 +11,7 @@
 // Work. A unit is (request, KV head, block of query rows): the G query heads of
 // a KV head times its tokens are packed as rows of 128-row tiles (a tile holds
 // 128 / G whole tokens). All units' key tiles (128 keys each), one after the
-// other with kUnitCost tiles' worth of set-up before each unit, are the work
+// other with kCost tiles' worth of set-up before each unit, are the work
 // list, and it is cut into equal contiguous shares. Lengths are read on the
 // device only, shares are equal to within a tile whatever the batch looks like,
 // and a unit that is cut is joined by the second kernel from float32 partial results.

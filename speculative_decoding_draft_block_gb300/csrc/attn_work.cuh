@@ -3,7 +3,7 @@
 //
 // A unit is (request, KV head, block of query rows), where a request's rows are
 // its tokens times the G query heads of a KV head: row = token * G + head. All
-// units' key tiles, one unit after the other with kUnitCost tiles' worth of
+// units' key tiles, one unit after the other with kCost tiles' worth of
 // set-up before each, are the work list; it is cut into kShares contiguous
 // shares of equal length. Lengths are read on the device only. A unit that is
 // cut leaves float32 partial results (sums, reference exponent, sum of weights),
@@ -19,10 +19,10 @@
 namespace ds {
 namespace {
 
-constexpr int kUnitCost = kAttnUnitCost;  // of a unit's set-up, in key tiles
-
-template <int kTileKeys, int kShareCount, int kPartialRows, bool kTrees = false>
+template <int kTileKeys, int kShareCount, int kPartialRows, bool kTrees = false, int kUnitCost = kAttnUnitCost>
 struct WorkForm {
+  static constexpr int kCost = kUnitCost;          // of a unit's set-up, in key tiles
+  static_assert(kUnitCost <= kAttnUnitCostMost, "work_fits");
   static constexpr bool kTree = kTrees;            // whether the rows may be a tree's nodes
   static constexpr int kKeys = kTileKeys;          // keys of a tile
   static constexpr int kShares = kShareCount;
@@ -115,13 +115,14 @@ template <class F>
 __device__ __forceinline__ int64_t request_work(const AttnParams& p, const Request& r, int unit_rows) {
   int64_t w = 0;
 #pragma unroll 1
-  for (int u = 0; u * unit_rows < r.n * p.group; ++u) w += make_unit<F>(p, r, u, unit_rows).n + kUnitCost;
+  for (int u = 0; u * unit_rows < r.n * p.group; ++u) w += make_unit<F>(p, r, u, unit_rows).n + F::kCost;
   return w * p.pool.n_kv_heads;
 }
 
 // Tiles of a unit (first work tile `first`, n key tiles) that lie before work tile x.
+template <class F>
 __host__ __device__ __forceinline__ int tiles_before(int64_t x, int64_t first, int n) {
-  const int64_t t = x - first - kUnitCost;
+  const int64_t t = x - first - F::kCost;
   return t <= 0 ? 0 : t >= n ? n : (int)t;
 }
 
@@ -156,7 +157,7 @@ struct Walk {
       }
       const Unit y = make_unit<F>(p, r, u, unit_rows);
       // (fits: work_fits)
-      const uint32_t w = y.n + kUnitCost, all = w * p.pool.n_kv_heads;
+      const uint32_t w = y.n + F::kCost, all = w * p.pool.n_kv_heads;
       if (at >= base + all) {
         base += all;
         ++u;
@@ -164,7 +165,7 @@ struct Walk {
       }
       const int h = (int)((uint32_t)(at - base) / w);
       const int64_t first = base + (int64_t)((uint32_t)h * w);
-      const int t0 = tiles_before(at, first, y.n), t1 = tiles_before(end, first, y.n);
+      const int t0 = tiles_before<F>(at, first, y.n), t1 = tiles_before<F>(end, first, y.n);
       const bool here = y.n == 0 ? at == first : t1 > t0;
       at = first + w;
       if (!here) continue;
@@ -370,8 +371,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
   // have nothing and have written nothing), and whether there are more shares
   auto has_part = [&](int i, bool& more) {
     const int k = share + 32 * i + lane;
-    const int a = k < F::kShares ? tiles_before(F::begin(cu.total, k), cu.first, cu.n) : cu.n;
-    const int z = k < F::kShares ? tiles_before(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
+    const int a = k < F::kShares ? tiles_before<F>(F::begin(cu.total, k), cu.first, cu.n) : cu.n;
+    const int z = k < F::kShares ? tiles_before<F>(F::begin(cu.total, k + 1), cu.first, cu.n) : cu.n;
     more = __shfl_sync(0xffffffffu, z, 31) < cu.n;
     return a < z;
   };
@@ -504,11 +505,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
 // Launch of the join for units of at most `rows` rows of a slot. With few rows two a
 // block, so that the parts in flight are more: 10 rows of float32 12.7 us, with eight
 // a block 15.9; with many rows blocks of two are too many.
-template <class F, int D, typename T>
+template <class F, int D, typename T, int kFew = 2>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s, int rows, int tile, int used) {
   if (rows <= 16)
-    return launch_early(attn_join_kernel<F, D, T, 2>, dim3(F::kShares, (rows + 1) / 2), dim3(kJoinThreads), 0, s, p, tile,
-                        used);
+    return launch_early(attn_join_kernel<F, D, T, kFew>, dim3(F::kShares, (rows + kFew - 1) / kFew), dim3(kJoinThreads), 0, s,
+                        p, tile, used);
   return launch_early(attn_join_kernel<F, D, T, 8>, dim3(F::kShares, (rows + 7) / 8), dim3(kJoinThreads), 0, s, p, tile,
                       used);
 }

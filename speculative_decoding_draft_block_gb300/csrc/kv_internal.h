@@ -182,8 +182,8 @@ struct Readiness {
 };
 
 // The attention's key tiles, and the set-up of a unit of its work in tiles (0, 2 and 3
-// are slower where units of a few tiles stand beside longer ones).
-constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1;
+// are slower where units of a few tiles stand beside longer ones), the most of any form.
+constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1, kAttnUnitCostMost = 4;
 
 // Whether the work of one block of rows, over all KV heads, can be counted in 32 bits: with
 // tiles of 128 keys always (2^23 + 1 tiles, 256 heads), with tiles of 64 except for 256
