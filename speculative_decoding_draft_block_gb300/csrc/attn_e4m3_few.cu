@@ -22,10 +22,11 @@
 // Units, shares and the join are those of attn_work.cuh, for groups of KH KV heads (the query
 // heads of a group count as those of one KV head; a tile has 128 / KH keys of each): with
 // tokens outside heads, a head's row of codes is 128 bytes, and memory gives those at 5.1
-// TB/s one head at a time (128 requests of 4000 cached), neighbours together at MEASURED.
-// Two blocks an SM. A producer warp walks over the share and loads tiles (codes
+// TB/s one head at a time (128 requests of 4000 cached), neighbours together at 6.0, as heads
+// outside tokens.
+// Two blocks an SM. One warp walks over the share, one loads tiles (codes
 // swizzled, a box a page and head, scales beside them) into a ring. Each of the other
-// warps takes 16 keys of every tile of one head (32 where there are four), with references, sums
+// four takes 32 keys of every tile of one head, with references, sums
 // and outputs of its own. References are raised when a lane finds that one has to be (a vote
 // a tile), so no maxima go over lanes otherwise. At a piece's end a warp puts its outputs where
 // its last keys' codes were, and a head's warps add them up; the next piece's q
@@ -63,6 +64,10 @@ struct Stage {
   static constexpr int kCount = D == 128 ? 3 : 6;
 };
 
+// Whether q is kept in shared memory: beside the outputs of 16 rows registers do not hold it.
+template <int D, int NT>
+constexpr bool kSharedQ = D == 128 && NT == 2;
+
 template <int D, int NT, int KH, int kWarps>
 struct Shared {
   Piece piece[kAhead];
@@ -72,6 +77,7 @@ struct Shared {
   int abort;
   ShareStart<32 * (kWarps + 2), 1> work;
   alignas(16) uint8_t scale[Stage<D>::kCount][2][kTile];
+  uint4 q[kSharedQ<D, NT> ? KH : 1][D / 16][32];  // as the products take it, two eights of rows a lane
 };
 
 template <int D, int NT, int KH, int kWarps>
@@ -83,7 +89,8 @@ constexpr uint32_t smem_bytes() {
   return header_bytes<D, NT, KH, kWarps>() + Stage<D>::kCount * Stage<D>::kBytes;
 }
 
-// (A piece's beginning and end cost a block as much as three tiles: see launch_heads.)
+// (A piece's beginning and end cost a block as much as three tiles: 128 requests of 300 to 8000
+// cached 121.5 us, counted as one tile 138, as two 126, as four 121.5.)
 template <int NT, int KH>
 struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true, 3> {};
 
@@ -141,8 +148,9 @@ struct Heads {
   Divisor by_group;
 };
 
-// NT times 8 rows a KV head; kWarps warps with keys, one that walks over the share, one that loads.
-template <int D, int NT, int KH, int kWarps>
+// NT times 8 rows a KV head; kWarps warps with keys, kG times 16 at a time, one that walks over
+// the share, one that loads.
+template <int D, int NT, int KH, int kWarps, int kG>
 __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
     attn_e4m3_few_kernel(const AttnParams p, const Heads hd, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
@@ -151,9 +159,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
   using S = Shared<D, NT, KH, kWarps>;
   constexpr int kThreads = 32 * (kWarps + 2), kHeadWarps = kWarps / KH;
   constexpr int kKeys = kTile / KH, kWarpKeys = kTile / kWarps;  // keys of a tile, of a warp of it
-  static_assert(kWarpKeys % 16 == 0 && 4 * NT * D * 4 <= kWarpKeys * D, "a warp's outputs in its keys' places");
+  static_assert(kWarpKeys % (16 * kG) == 0 && kG <= 2 && 4 * NT * D * 4 <= kWarpKeys * D, "a warp's outputs in its keys' places");
   constexpr int kStages = St::kCount;
   constexpr int kRows = 8 * NT * KH;
+  constexpr bool kQShared = kSharedQ<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   S& sh = *reinterpret_cast<S*>(smem);
   uint8_t* ring = smem + header_bytes<D, NT, KH, kWarps>();
@@ -364,74 +373,107 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
           }
           lo_all = __reduce_max_sync(0xffffffffu, lo_all);
           hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+          if constexpr (kQShared) {
+            // (a head's warps write the same; all of them have met since q was last read)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              sh.q[sub][k][lane] = make_uint4(q[0][2 * k], q[0][2 * k + 1], q[NT - 1][2 * k], q[NT - 1][2 * k + 1]);
+            __syncwarp();
+          }
         }
         bool ok = true;
         for (int it = 0; it < n_tiles; ++it) {
           ok = wait_warp(&sh.full[stage], parity, abort);
           if (!ok) break;
 #pragma unroll 1
-          for (int k0 = 0; k0 < kWarpKeys; k0 += 16) {
+          for (int k0 = 0; k0 < kWarpKeys; k0 += 16 * kG) {
             const int row0 = of_head * kWarpKeys + k0;  // of the tile's keys of this head
             const int key0 = (tile0 + it) * kKeys + row0;
-            if (key0 + 16 <= lo_any || key0 >= hi_any) continue;
+            if (key0 + 16 * kG <= lo_any || key0 >= hi_any) continue;
             const uint8_t* kc = ring + stage * St::kBytes + (sub * kKeys + row0) * D;
             const uint8_t* vc = kc + St::kCodes;
             const uint8_t* sc = &sh.scale[stage][0][sub * kKeys + row0];
-            float ks[2], ev[2];  // of keys g, g + 8
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              ks[i] = power_of(sc[g + 8 * i]);
-              ev[i] = exponent_of(sc[kTile + g + 8 * i]);
-            }
-            float s[NT][4], s2[NT][4];  // key g: rows 2 t, 2 t + 1; key g + 8 (two chains of products)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.f;
+            float ev[kG][2];      // exponents of the values of keys g, g + 8 (and 16 on)
+            float s[kG][NT][4];   // key g: rows 2 t, 2 t + 1; key g + 8
             {
-              uint4 w[2][D / 64];
+              float s2[kG][NT][4];  // (two chains of products)
+              uint4 w[kG][2][D / 64];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int row = g + 8 * i;
+              for (int u = 0; u < kG; ++u) {
 #pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-                  const int chunk = D == 128 ? (2 * t + k) ^ (row & 7) : t ^ ((row >> 1) & 3);
-                  w[i][k] = *reinterpret_cast<const uint4*>(kc + row * D + chunk * 16);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) s[u][n][i] = s2[u][n][i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int row = g + 8 * i;  // (16 u does not change the swizzle)
+#pragma unroll
+                  for (int k = 0; k < D / 64; ++k) {
+                    const int chunk = D == 128 ? (2 * t + k) ^ (row & 7) : t ^ ((row >> 1) & 3);
+                    w[u][i][k] = *reinterpret_cast<const uint4*>(kc + (16 * u + row) * D + chunk * 16);
+                  }
                 }
               }
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
-                const uint4 &y = w[0][k / 4], &z = w[1][k / 4];
-                const uint32_t a = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
-                const uint32_t b = k % 4 == 0 ? z.x : k % 4 == 1 ? z.y : k % 4 == 2 ? z.z : z.w;
-                const uint32_t f[4] = {halves_lo(a), halves_lo(b), halves_hi(a), halves_hi(b)};
+                uint32_t qk[2 * NT];
+                if constexpr (kQShared) {
+                  const uint4 y = sh.q[sub][k][lane];
+                  qk[0] = y.x;
+                  qk[1] = y.y;
+                  qk[2 * NT - 2] = y.z;
+                  qk[2 * NT - 1] = y.w;
+                } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(k & 1 ? s2[n] : s[n], f, q[n][2 * k], q[n][2 * k + 1]);
+                  for (int n = 0; n < NT; ++n) {
+                    qk[2 * n] = q[n][2 * k];
+                    qk[2 * n + 1] = q[n][2 * k + 1];
+                  }
+                }
+#pragma unroll
+                for (int u = 0; u < kG; ++u) {
+                  const uint4 &y = w[u][0][k / 4], &z = w[u][1][k / 4];
+                  const uint32_t a = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
+                  const uint32_t b = k % 4 == 0 ? z.x : k % 4 == 1 ? z.y : k % 4 == 2 ? z.z : z.w;
+                  const uint32_t f[4] = {halves_lo(a), halves_lo(b), halves_hi(a), halves_hi(b)};
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) mma_f16(k & 1 ? s2[u][n] : s[u][n], f, qk[2 * n], qk[2 * n + 1]);
+                }
               }
+#pragma unroll
+              for (int u = 0; u < kG; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float ks = power_of(sc[16 * u + g + 8 * i]);
+                  ev[u][i] = exponent_of(sc[kTile + 16 * u + g + 8 * i]);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 2 * i; j < 2 * i + 2; ++j) s[u][n][j] = (s[u][n][j] + s2[u][n][j]) * ks;
+                }
             }
             // the values' codes: 4 keys
             constexpr int kVW = D / 32;  // words of a key
-            uint32_t w[4][kVW];
+            uint32_t w[kG][4][kVW];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-              if constexpr (D == 128) {
-                const uint4 y = *reinterpret_cast<const uint4*>(vc + row * D + ((g ^ (row & 7)) << 4));
-                w[i][0] = y.x;
-                w[i][1] = y.y;
-                w[i][kVW - 2] = y.z;
-                w[i][kVW - 1] = y.w;
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(vc + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-                w[i][0] = y.x;
-                w[i][1] = y.y;
+            for (int u = 0; u < kG; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+                const uint8_t* from = vc + (16 * u + row) * D;
+                if constexpr (D == 128) {
+                  const uint4 y = *reinterpret_cast<const uint4*>(from + ((g ^ (row & 7)) << 4));
+                  w[u][i][0] = y.x;
+                  w[u][i][1] = y.y;
+                  w[u][i][kVW - 2] = y.z;
+                  w[u][i][kVW - 1] = y.w;
+                } else {
+                  const uint2 y = *reinterpret_cast<const uint2*>(from + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                  w[u][i][0] = y.x;
+                  w[u][i][1] = y.y;
+                }
               }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[n][i] = (s[n][i] + s2[n][i]) * ks[i >> 1];
-            if (key0 < lo_all || key0 + 16 > hi_all) {
+            if (key0 < lo_all || key0 + 16 * kG > hi_all) {
               uint32_t any = 0;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
@@ -446,39 +488,54 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                                 : bits_between(lo - key0, hi - key0);
                   }
                   any |= seen;
-                  if (!(seen >> g & 1)) s[n][i] = kNegInf;
-                  if (!(seen >> (g + 8) & 1)) s[n][2 + i] = kNegInf;
+#pragma unroll
+                  for (int u = 0; u < kG; ++u) {
+                    if (!(seen >> (16 * u + g) & 1)) s[u][n][i] = kNegInf;
+                    if (!(seen >> (16 * u + g + 8) & 1)) s[u][n][2 + i] = kNegInf;
+                  }
                 }
               // keys that no row sees may hold anything: their values become zeros
               any |= __shfl_xor_sync(0xffffffffu, any, 1);
               any |= __shfl_xor_sync(0xffffffffu, any, 2);
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (!(any >> (g + 8 * i) & 1)) ev[i] = 0.f;
+              for (int u = 0; u < kG; ++u) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!(any >> (2 * t + (i & 1) + 8 * (i >> 1)) & 1))
+                for (int i = 0; i < 2; ++i)
+                  if (!(any >> (16 * u + g + 8 * i) & 1)) ev[u][i] = 0.f;
 #pragma unroll
-                  for (int k = 0; k < kVW; ++k) w[i][k] = 0;
+                for (int i = 0; i < 4; ++i)
+                  if (!(any >> (16 * u + 2 * t + (i & 1) + 8 * (i >> 1)) & 1))
+#pragma unroll
+                    for (int k = 0; k < kVW; ++k) w[u][i][k] = 0;
+              }
             }
             // exponents over the references: of the sum's terms, of the weights
-            float e[NT][4], ew[NT][4], top_e = kNegInf, top_w = kNegInf;
+            float e[kG][NT][4], ew[kG][NT][4], top_e = kNegInf, top_w = kNegInf;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < kG; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                e[n][i] = fmaf(s[n][i], c_row[n][i & 1], -r[n][i & 1]);
-                ew[n][i] = e[n][i] + (ev[i >> 1] + dv[n][i & 1]);
-                top_e = fmaxf(top_e, e[n][i]);
-                top_w = fmaxf(top_w, ew[n][i]);
-              }
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  e[u][n][i] = fmaf(s[u][n][i], c_row[n][i & 1], -r[n][i & 1]);
+                  ew[u][n][i] = e[u][n][i] + (ev[u][i >> 1] + dv[n][i & 1]);
+                  top_e = fmaxf(top_e, e[u][n][i]);
+                  top_w = fmaxf(top_w, ew[u][n][i]);
+                }
             if (__any_sync(0xffffffffu, top_e > kSlack || top_w > kTop)) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const float y0 = s[n][i] * c_row[n][i], y1 = s[n][2 + i] * c_row[n][i];
-                  float a = fmaxf(y0, y1), b = fmaxf(y0 + ev[0], y1 + ev[1]);
+                  float a = kNegInf, b = kNegInf;
+#pragma unroll
+                  for (int u = 0; u < kG; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                      const float y = s[u][n][2 * k + i] * c_row[n][i];
+                      a = fmaxf(a, y);
+                      b = fmaxf(b, y + ev[u][k]);
+                    }
 #pragma unroll
                   for (int d = 4; d < 32; d <<= 1) {
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
@@ -499,32 +556,38 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                     }
                   }
                   dv[n][i] = r[n][i] - rv;
-                  e[n][i] = y0 - r[n][i];
-                  e[n][2 + i] = y1 - r[n][i];
-                  ew[n][i] = e[n][i] + (ev[0] + dv[n][i]);
-                  ew[n][2 + i] = e[n][2 + i] + (ev[1] + dv[n][i]);
+#pragma unroll
+                  for (int u = 0; u < kG; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                      e[u][n][2 * k + i] = s[u][n][2 * k + i] * c_row[n][i] - r[n][i];
+                      ew[u][n][2 * k + i] = e[u][n][2 * k + i] + (ev[u][k] + dv[n][i]);
+                    }
                 }
             }
-            uint32_t b0[NT], b1[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float v[4];
+            for (int u = 0; u < kG; ++u) {
+              uint32_t b0[NT], b1[NT];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                l[n][i & 1] += ex2_approx(e[n][i]);
-                // (where a key is not seen, its value's scale may be NaN)
-                v[i] = e[n][i] == kNegInf ? 0.f : ex2_approx(ew[n][i]);
+              for (int n = 0; n < NT; ++n) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  l[n][i & 1] += ex2_approx(e[u][n][i]);
+                  // (where a key is not seen, its value's scale may be NaN)
+                  v[i] = e[u][n][i] == kNegInf ? 0.f : ex2_approx(ew[u][n][i]);
+                }
+                b0[n] = transpose8(to_f16x2(v[0], v[1]));
+                b1[n] = transpose8(to_f16x2(v[2], v[3]));
               }
-              b0[n] = transpose8(to_f16x2(v[0], v[1]));
-              b1[n] = transpose8(to_f16x2(v[2], v[3]));
-            }
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
-              const uint32_t a = __byte_perm(w[0][j / 2], w[1][j / 2], sel), b = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-              const uint32_t f[4] = {halves_lo(a), halves_hi(a), halves_lo(b), halves_hi(b)};
+              for (int j = 0; j < D / 16; ++j) {
+                const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                const uint32_t a = __byte_perm(w[u][0][j / 2], w[u][1][j / 2], sel), b = __byte_perm(w[u][2][j / 2], w[u][3][j / 2], sel);
+                const uint32_t f[4] = {halves_lo(a), halves_hi(a), halves_lo(b), halves_hi(b)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_f16(o[n][j], f, b0[n], b1[n]);
+                for (int n = 0; n < NT; ++n) mma_f16(o[n][j], f, b0[n], b1[n]);
+              }
             }
           }
           __syncwarp();
@@ -637,10 +700,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
 template <int D, int NT, int KH>
 cudaError_t launch(const AttnParams& given, cudaStream_t s) {
   static Readiness readiness;
-  constexpr int kWarps = NT == 1 ? 8 : 4;  // (registers: 16 rows' outputs take twice those of 8)
+  // Four warps with keys and 168 registers, 32 keys at a time: 128 requests of 4 rows 108 us; eight
+  // warps and 96 registers, 16 keys at a time, 122 (spills), D = 64 80 and 86. 16 rows of D = 128
+  // hold the sums of 16 keys at a time only: 142 us, 152 with 32.
+  constexpr int kWarps = 4, kG = D == 128 && NT == 2 ? 1 : 2;
   constexpr uint32_t kSmem = smem_bytes<D, NT, KH, kWarps>();
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
-  const auto kernel = attn_e4m3_few_kernel<D, NT, KH, kWarps>;
+  const auto kernel = attn_e4m3_few_kernel<D, NT, KH, kWarps, kG>;
   const cudaError_t ready =
       readiness.get([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (ready != cudaSuccess) return ready;
