@@ -25,7 +25,7 @@
 // TB/s one head at a time (128 requests of 4000 cached), neighbours together at 6.0, as heads
 // outside tokens.
 // Two blocks an SM. One warp walks over the share, one loads tiles (codes
-// swizzled, a box a page and head, scales beside them) into a ring. Each of the other
+// swizzled, a box a page, scales beside them) into a ring. Each of the other
 // four takes 32 keys of every tile of one head, with references, sums
 // and outputs of its own. References are raised when a lane finds that one has to be (a vote
 // a tile), so no maxima go over lanes otherwise. At a piece's end a warp puts its outputs where
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
   using S = Shared<D, NT, KH, kWarps>;
   constexpr int kThreads = 32 * (kWarps + 2), kHeadWarps = kWarps / KH;
   constexpr int kKeys = kTile / KH, kWarpKeys = kTile / kWarps;  // keys of a tile, of a warp of it
-  static_assert(kWarpKeys % (16 * kG) == 0 && kG <= 2 && 4 * NT * D * 4 <= kWarpKeys * D, "a warp's outputs in its keys' places");
+  static_assert(kWarpKeys % (16 * kG) == 0 && kG <= 2 && 16 * NT <= kWarpKeys, "a warp's outputs in its keys' places");
   constexpr int kStages = St::kCount;
   constexpr int kRows = 8 * NT * KH;
   constexpr bool kQShared = kSharedQ<D, NT>;
@@ -198,6 +198,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
   }
   volatile int* abort = &sh.abort;
   uint32_t stage = 0, parity = 0;
+  // A tile's boxes (a page's keys of all heads of the group): head by head the keys within a
+  // box. Where 16 keys of head h from key r of the tile on stand, in keys.
+  const int rows = min(1 << p.pool.page_shift, kKeys);
+  auto stand = [&](int h, int r) { return (r & -rows) * KH + h * rows + (r & (rows - 1)); };
 
   if (warp == kWarps) {
     // ------------------------------------------------------------------ walk
@@ -217,8 +221,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ loads
     const int shift = p.pool.page_shift, page_size = 1 << shift;
-    const int rows = min(page_size, kKeys), boxes = kKeys / rows;  // keys of a box, pages of a tile
-    const int box = lane % boxes, sub = lane / boxes;              // a lane's page and head of a tile
+    const int boxes = kKeys / rows;  // pages of a tile: a lane's each
     const int64_t scale_part = (int64_t)hd.n_kv_heads << shift;
     constexpr int kNoPage = INT32_MIN;
     const int32_t* table = nullptr;
@@ -226,8 +229,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
     uint32_t np = 0;
     // Table entry of this lane's page of a tile, kNoPage: no row sees it.
     auto page_of = [&](int tile) {
-      const int key = tile * kKeys + box * rows;
-      if (sub >= KH || key >= hi || key + rows <= lo) return kNoPage;
+      const int key = tile * kKeys + lane * rows;
+      if (lane >= boxes || key >= hi || key + rows <= lo) return kNoPage;
       return __ldcg(table + (key >> shift));
     };
     // the next piece with tiles (n < 0: there is none), and its first page
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
         tile0 = x.tile0;
         lo = x.lo;
         hi = x.hi;
-        head = x.h * KH + sub;
+        head = x.h * KH;
         table = p.block_table + (int64_t)x.b * p.max_pages;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.piece_empty[i]);
@@ -264,16 +267,20 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
       if (!last) page = page_of(tile0 + j);
       ok = wait_warp(&sh.empty[stage], parity ^ 1, abort);
       if (!ok) break;
-      if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * rows * (D + 1));
+      if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * KH * rows * (D + 1));
       __syncwarp();
       if (now != kNoPage) {
-        const int at = sub * kKeys + box * rows;
+        const int at = lane * KH * rows;
         uint8_t* to = ring + stage * St::kBytes + at * D;
         const uint8_t* from = p.pool.scales + 2 * (int64_t)now * scale_part + ((int64_t)now_head << shift) + token;
         tma_load_4d_plain(to, &tmK, &sh.full[stage], 0, token, now_head, now);
         tma_load_4d_plain(to + St::kCodes, &tmV, &sh.full[stage], 0, token, now_head, now);
-        bulk_load(&sh.scale[stage][0][at], from, rows, &sh.full[stage]);
-        bulk_load(&sh.scale[stage][1][at], from + scale_part, rows, &sh.full[stage]);
+        // (heads' scales stand a page apart: one copy if a box is a page)
+        const int copies = rows == page_size ? 1 : KH, bytes = KH * rows / copies;
+        for (int h = 0; h < copies; ++h) {
+          bulk_load(&sh.scale[stage][0][at + h * bytes], from + (h << shift), bytes, &sh.full[stage]);
+          bulk_load(&sh.scale[stage][1][at + h * bytes], from + scale_part + (h << shift), bytes, &sh.full[stage]);
+        }
       }
       __syncwarp();
       if (++stage == kStages) {
@@ -390,9 +397,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
             const int row0 = of_head * kWarpKeys + k0;  // of the tile's keys of this head
             const int key0 = (tile0 + it) * kKeys + row0;
             if (key0 + 16 * kG <= lo_any || key0 >= hi_any) continue;
-            const uint8_t* kc = ring + stage * St::kBytes + (sub * kKeys + row0) * D;
+            int off[kG];  // places of 16 keys each
+#pragma unroll
+            for (int u = 0; u < kG; ++u) off[u] = stand(sub, row0 + 16 * u);
+            const uint8_t* kc = ring + stage * St::kBytes;
             const uint8_t* vc = kc + St::kCodes;
-            const uint8_t* sc = &sh.scale[stage][0][sub * kKeys + row0];
+            const uint8_t* sc = &sh.scale[stage][0][0];
             float ev[kG][2];      // exponents of the values of keys g, g + 8 (and 16 on)
             float s[kG][NT][4];   // key g: rows 2 t, 2 t + 1; key g + 8
             {
@@ -406,11 +416,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                   for (int i = 0; i < 4; ++i) s[u][n][i] = s2[u][n][i] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const int row = g + 8 * i;  // (16 u does not change the swizzle)
+                  const int row = g + 8 * i;  // (16 keys do not change the swizzle)
 #pragma unroll
                   for (int k = 0; k < D / 64; ++k) {
                     const int chunk = D == 128 ? (2 * t + k) ^ (row & 7) : t ^ ((row >> 1) & 3);
-                    w[u][i][k] = *reinterpret_cast<const uint4*>(kc + (16 * u + row) * D + chunk * 16);
+                    w[u][i][k] = *reinterpret_cast<const uint4*>(kc + (off[u] + row) * D + chunk * 16);
                   }
                 }
               }
@@ -444,8 +454,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
               for (int u = 0; u < kG; ++u)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const float ks = power_of(sc[16 * u + g + 8 * i]);
-                  ev[u][i] = exponent_of(sc[kTile + 16 * u + g + 8 * i]);
+                  const float ks = power_of(sc[off[u] + g + 8 * i]);
+                  ev[u][i] = exponent_of(sc[kTile + off[u] + g + 8 * i]);
 #pragma unroll
                   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-                const uint8_t* from = vc + (16 * u + row) * D;
+                const uint8_t* from = vc + (off[u] + row) * D;
                 if constexpr (D == 128) {
                   const uint4 y = *reinterpret_cast<const uint4*>(from + ((g ^ (row & 7)) << 4));
                   w[u][i][0] = y.x;
@@ -612,7 +622,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
           constexpr int kChunks = D / 4;
           auto place = [&](int w, int n, int row) {
             return reinterpret_cast<float4*>(ring + stage * St::kBytes + (row >> 2) * St::kCodes +
-                                             (sub * kKeys + w * kWarpKeys) * D + (n * 4 + (row & 3)) * (D * 4));
+                                             stand(sub, w * kWarpKeys + 16 * n) * D + (row & 3) * (D * 4));
           };
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -715,7 +725,7 @@ cudaError_t launch(const AttnParams& given, cudaStream_t s) {
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)given.pool.n_kv_heads, (cuuint64_t)given.pool.n_pages};
   const cuuint64_t str[3] = {(cuuint64_t)given.pool.token_stride, (cuuint64_t)given.pool.head_stride,
                              (cuuint64_t)given.pool.page_stride};
-  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(page < keys ? page : keys), 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(page < keys ? page : keys), (cuuint32_t)KH, 1};
   if (!encode_tmap_bytes(&mk, given.pool.k, 4, dims, str, box, true) || !encode_tmap_bytes(&mv, given.pool.v, 4, dims, str, box, true))
     return cudaErrorInvalidValue;
   const Heads heads = {given.group, given.pool.n_kv_heads, given.by_group};
