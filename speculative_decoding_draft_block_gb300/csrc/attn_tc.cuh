@@ -77,6 +77,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "attn_work.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -1270,30 +1272,37 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           const bool large = __any_sync(0xffffffffu, factor2 != 0x3f803f80u);
           const uint8_t* from = slot + L::kCodes + row0 * D + piece * 8;
           uint8_t* to = slot + (piece / 8) * (kTile * 128) + row0 * 128;
+          // (no branch among the steps: their instructions interleave)
+          auto restore = [&](auto twice) {
 #pragma unroll 1
-          for (int i0 = 0; i0 < kSteps; i0 += kAtOnce) {
-            uint2 x[kAtOnce];
+            for (int i0 = 0; i0 < kSteps; i0 += kAtOnce) {
+              uint2 x[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) x[i] = *reinterpret_cast<const uint2*>(from + (i0 + i) * kRows * D);
-            __syncwarp();  // (a row's codes are read before its values are written)
+              for (int i = 0; i < kAtOnce; ++i) x[i] = *reinterpret_cast<const uint2*>(from + (i0 + i) * kRows * D);
+              __syncwarp();  // (a row's codes are read before its values are written)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              const int r = (i0 + i) * kRows;
-              const uint32_t f = __shfl_sync(0xffffffffu, factor, r + r0);
-              uint32_t y[4];
-              y[0] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x1404)), f);
-              y[1] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x3424)), f);
-              y[2] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x1404)), f);
-              y[3] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x3424)), f);
-              if (large) {
-                const uint32_t f2 = __shfl_sync(0xffffffffu, factor2, r + r0);
+              for (int i = 0; i < kAtOnce; ++i) {
+                const int r = (i0 + i) * kRows;
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, r + r0);
+                uint32_t y[4];
+                y[0] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x1404)), f);
+                y[1] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x3424)), f);
+                y[2] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x1404)), f);
+                y[3] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x3424)), f);
+                if constexpr (decltype(twice)::value) {
+                  const uint32_t f2 = __shfl_sync(0xffffffffu, factor2, r + r0);
 #pragma unroll
-                for (int w = 0; w < 4; ++w) y[w] = mul_bf16x2(y[w], f2);
+                  for (int w = 0; w < 4; ++w) y[w] = mul_bf16x2(y[w], f2);
+                }
+                *reinterpret_cast<uint4*>(to + r * 128 + (((piece & 7) ^ ((row0 + r) & 7)) << 4)) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
               }
-              *reinterpret_cast<uint4*>(to + r * 128 + (((piece & 7) ^ ((row0 + r) & 7)) << 4)) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
             }
-          }
+          };
+          if (large)
+            restore(std::true_type());
+          else
+            restore(std::false_type());
           fence_proxy_async_smem();  // read by the tensor core, then filled by TMA
         }
         __syncwarp();
