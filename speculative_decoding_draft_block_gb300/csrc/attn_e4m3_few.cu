@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              c_row[n][i] = fmaxf(c * __shfl_sync(0xffffffffu, down, 4 * (2 * t + i)), __int_as_float(1));  // (never 0)
+              c_row[n][i] = c * __shfl_sync(0xffffffffu, down, 4 * (2 * t + i));
               const int row = 8 * n + 2 * t + i;
               int lo, hi;
               if (row < n_rows) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
             const uint8_t* vc = kc + St::kCodes;
             const uint8_t* sc = &sh.scale[stage][0][0];
             float ev[kG][2];      // exponents of the values of keys g, g + 8 (and 16 on)
-            float s[kG][NT][4];   // key g: rows 2 t, 2 t + 1; key g + 8
+            float s[kG][NT][4];   // scores in exponents of 2; key g: rows 2 t, 2 t + 1; key g + 8
             {
               float s2[kG][NT][4];  // (two chains of products)
               uint4 w[kG][2][D / 64];
@@ -456,10 +456,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                 for (int i = 0; i < 2; ++i) {
                   const float ks = power_of(sc[off[u] + g + 8 * i]);
                   ev[u][i] = exponent_of(sc[kTile + off[u] + g + 8 * i]);
+                  // (the factors' product first: with a large scale the score alone passes float32's range)
 #pragma unroll
                   for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int j = 2 * i; j < 2 * i + 2; ++j) s[u][n][j] = (s[u][n][j] + s2[u][n][j]) * ks;
+                    for (int j = 0; j < 2; ++j) s[u][n][2 * i + j] = (s[u][n][2 * i + j] + s2[u][n][2 * i + j]) * (ks * c_row[n][j]);
                 }
             }
             // the values' codes: 4 keys
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  e[u][n][i] = fmaf(s[u][n][i], c_row[n][i & 1], -r[n][i & 1]);
+                  e[u][n][i] = s[u][n][i] - r[n][i & 1];
                   ew[u][n][i] = e[u][n][i] + (ev[u][i >> 1] + dv[n][i & 1]);
                   top_e = fmaxf(top_e, e[u][n][i]);
                   top_w = fmaxf(top_w, ew[u][n][i]);
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                   for (int u = 0; u < kG; ++u)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                      const float y = s[u][n][2 * k + i] * c_row[n][i];
+                      const float y = s[u][n][2 * k + i];
                       a = fmaxf(a, y);
                       b = fmaxf(b, y + ev[u][k]);
                     }
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
                   for (int u = 0; u < kG; ++u)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                      e[u][n][2 * k + i] = s[u][n][2 * k + i] * c_row[n][i] - r[n][i];
+                      e[u][n][2 * k + i] = s[u][n][2 * k + i] - r[n][i];
                       ew[u][n][2 * k + i] = e[u][n][2 * k + i] + (ev[u][k] + dv[n][i]);
                     }
                 }
