@@ -64,7 +64,7 @@
 //
 // Quantised pools (kQuant). Codes times powers of two are bfloat16 numbers, so a tile is
 // restored in shared memory and all else stays as it is. A tile's codes arrive at
-// 16 KB of its slot, a row of head_dim bytes, with their scales in the header. Four more warps take
+// 16 KB of its slot, a row of head_dim bytes, with their scales in the header. Eight more warps take
 // the ring's entries in their order: 8 codes a lane become 16 bytes in the swizzled
 // tile, and the issuers wait for them instead of the copies. With D = 128 a row's
 // codes lie where the second half of its own bfloat16 values goes, and the lanes that
@@ -92,10 +92,10 @@ using namespace sm100;
 // pools) restoring warps.
 template <bool kQuant>
 struct Split {
-  static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr uint32_t kCtrl = kQuant ? 80 : 88, kSoft = kQuant ? 184 : 208, kRestore = 64;
-  static constexpr uint32_t kLaunch = kQuant ? 128 : 168;
-  static_assert(128 * kCtrl + 256 * kSoft + (kQuant ? 128 * kRestore : 0) <= kThreads * kLaunch,
+  static constexpr int kRestorers = kQuant ? 8 : 0, kThreads = 384 + 32 * kRestorers;
+  static constexpr uint32_t kCtrl = kQuant ? 80 : 88, kSoft = kQuant ? 128 : 208, kRestore = 72;
+  static constexpr uint32_t kLaunch = kQuant ? 96 : 168;
+  static_assert(128 * kCtrl + 256 * kSoft + 32 * kRestorers * kRestore <= kThreads * kLaunch,
                 "register split exceeds the launch pool");
 };
 constexpr int kTile = kAttnTileTc;  // keys a tile, rows a tile
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
-      if (kQuant) mbar_init(&sh.ready[i], 4);  // restoring warps
+      if (kQuant) mbar_init(&sh.ready[i], Split<kQuant>::kRestorers);
       sh.entry[i] = 0;
     }
     sh.passed = 0;
@@ -899,6 +899,50 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
             }
             tmem_st_wait();
           }
+          if constexpr (kQuant) {
+            // Half of the row at a time, read twice: the registers go to the restoring warps, and
+            // the code is half as long (the warps share one instruction cache).
+            float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll 1
+            for (int h = 0; h < kTile; h += 64) {
+              uint32_t y[64];
+              tmem_ld32_issue(tS + h, y);
+              tmem_ld32_issue(tS + h + 32, y + 32);
+              tmem_ld_wait(y);
+              reg_dep32(y + 32);
+#pragma unroll
+              for (int q = 0; q < 64; q += 8)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                  mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
+            }
+            raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
+            const float r = m == kNegInf ? 0.f : m * c;
+            const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll 1
+            for (int h = 0; h < kTile; h += 64) {
+              uint32_t y[64];
+              tmem_ld32_issue(tS + h, y);
+              tmem_ld32_issue(tS + h + 32, y + 32);
+              tmem_ld_wait(y);
+              reg_dep32(y + 32);
+#pragma unroll
+              for (int w = 0; w < 32; ++w) {
+                const uint64_t e = fma2(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
+                float2 f = unpack2(e);
+                f.x = ex2_approx(f.x);
+                f.y = ex2_approx(f.y);
+                sum2[w & 1] = add2(sum2[w & 1], pack2(f.x, f.y));
+                y[w] = to_bf16x2(f.x, f.y);
+              }
+              // (over scores that have been read)
+              tmem_st16(tS + h / 2, y);
+              tmem_st16(tS + h / 2 + 16, y + 16);
+            }
+            const float2 sum = unpack2(add2(sum2[0], sum2[1]));
+            l += sum.x + sum.y;
+          } else {
           uint32_t y[128];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32_issue(tS + 32 * q, y + 32 * q);
@@ -933,6 +977,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           }
           const float2 sum = unpack2(add2(sum2[0], sum2[1]));
           l += sum.x + sum.y;
+          }
           tmem_st_wait();
         }
         tc_fence_before();
@@ -1255,9 +1300,9 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
       // ---------------------------------------------------------------- restoring warps
       setmaxnreg_dec<Split<kQuant>::kRestore>();
       constexpr int kPieces = D / 8, kRows = 32 / kPieces;  // of a row; rows of a warp at a time
-      constexpr int kSteps = 32 / kRows, kAtOnce = 8;
+      constexpr int kWarpRows = kTile / Split<kQuant>::kRestorers, kSteps = kWarpRows / kRows, kAtOnce = kSteps < 8 ? kSteps : 8;
       const int r0 = lane / kPieces, piece = lane % kPieces;
-      const int row0 = (warp - 12) * 32 + r0;
+      const int row0 = (warp - 12) * kWarpRows + r0;
       int ends = 0;  // streams that have ended
       RingPos<kSlots> at;
       while (ends < kLists) {
@@ -1267,7 +1312,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           ++ends;
         } else if (!(word & kNull)) {
           uint8_t* slot = sRing + at.slot * L::kSlotBytes;
-          const uint32_t scale = sh.scale[at.slot][(warp - 12) * 32 + lane];
+          const uint32_t scale = sh.scale[at.slot][(warp - 12) * kWarpRows + (lane & (kWarpRows - 1))];
           const uint32_t factor = code_factor(scale), factor2 = code_factor2(scale);
           const bool large = __any_sync(0xffffffffu, factor2 != 0x3f803f80u);
           const uint8_t* from = slot + L::kCodes + row0 * D + piece * 8;
