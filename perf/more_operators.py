@@ -289,6 +289,7 @@ def _prepare_calls(case, s):
     s["pool"] = kv_cache.KvPool(s["k"], s["v"], s["scales"])
     n = kv_cache.ds_paged_attention_workspace_bytes(s["pool"], case["heads"]) if "heads" in case else 0
     s["workspace"] = torch.empty(max(16, n), dtype=torch.uint8, device=_dev())
+    s["held"] = _held(s)   # the same buffers as numbers, for what comes back: no part of a call
 
 
 # ---- one pass ------------------------------------------------------------------------------------
@@ -304,7 +305,7 @@ def _own(c, s):
     from speculative_decoding_draft_block_gb300 import kv_cache as kv
     if c["op"] == "append":
         kv.check(kv.ds_cache_append(s["pool"], 0, s["k_new"], s["v_new"], s["q_start"], s["table"], s["kv_len"], s["status"]))
-        return _held(s)
+        return s["held"]
     if c["op"] == "attend":
         kv.check(kv.ds_paged_attention(s["pool"], 0, s["q"], s["q_start"], s["max_q"], s["table"], s["kv_len"], s["out"],
                                        s["workspace"], s["status"], lse=s["lse"], window=c["window"]))
@@ -315,7 +316,7 @@ def _own(c, s):
         return s["out"], s["lse"]
     if c["op"] == "keep":
         kv.check(kv.ds_cache_keep(s["pool"], s["path"], s["q_start"], s["table"], s["kv_len"], s["new_len"], s["status"]))
-        return s["new_len"], _held(s)
+        return s["new_len"], s["held"]
     kv.check(kv.ds_tree_masks(s["parent"], s["q_start"], s["max_q"], s["mask"], s["depth"], s["status"], window=c["window"]))
     return s["mask"], s["depth"]
 
