@@ -219,10 +219,15 @@ ds_status ds_cache_compact(const ds_compact_args* args, ds_stream_t stream);
  *       max |x| <= 448 * 2^e, and its values x / 2^e rounded to the nearest (ties to
  *       even): off by at most 2^-4 |x| or 2^(e - 10), whichever is more. A row with a
  *       value that is not finite gets scale 255 and zeros for codes.
- *   ds_paged_attention_tree  reads code * 2^(scale - 127), which bfloat16 holds exactly
- *       for scales from 27 (what append writes) to 246, and to its smallest subnormal
- *       below that; a code of 0x7F or 0xFF, which append does not write, reads as 480 in size.
- *       All else is as for bfloat16 pools.
+ *   ds_paged_attention_tree  reads code * 2^(scale - 127). With more than 16 rows a KV head
+ *       these are rounded to bfloat16, which holds them exactly for scales from 27 (what
+ *       append writes) to 246, and to its smallest subnormal below that; all else is as
+ *       for bfloat16 pools. With up to 16 rows the products take codes as they are and q
+ *       as float16 relative to its row's largest value (bfloat16's 8 bits down to 2^-31 of
+ *       that, multiples of 2^-39 of it below), and weights are rounded to float16 (11 bits;
+ *       fewer from 2^-29 of a row's largest weight times its value's power of two on,
+ *       none below 2^-37). The codes 0x7F and 0xFF, which append does not write,
+ *       must not stand in rows that a row of the call sees.
  *   ds_cache_update_scaled, ds_cache_compact_scaled   move the scales with the pages.
  * With scales = NULL the calls are those without the suffix.
  */

@@ -542,38 +542,36 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
 #pragma unroll
                   for (int u = 0; u < kG; ++u)
 #pragma unroll
+                    for (int k = 0; k < 2; ++k) a = fmaxf(a, s[u][n][2 * k + i]);
+#pragma unroll
+                  for (int d = 4; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                  const float was = r[n][i];
+                  if (a - was > kSlack) r[n][i] = a;
+                  // (relative to r, which may be too large for what is added to it to count)
+#pragma unroll
+                  for (int u = 0; u < kG; ++u)
+#pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                      const float y = s[u][n][2 * k + i];
-                      a = fmaxf(a, y);
-                      b = fmaxf(b, y + ev[u][k]);
+                      e[u][n][2 * k + i] = s[u][n][2 * k + i] - r[n][i];
+                      b = fmaxf(b, e[u][n][2 * k + i] + ev[u][k]);
                     }
 #pragma unroll
-                  for (int d = 4; d < 32; d <<= 1) {
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                    b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-                  }
-                  float rv = r[n][i] - dv[n][i];
-                  if (a - r[n][i] > kSlack) {
-                    l[n][i] *= ex2_approx(r[n][i] - a);
-                    r[n][i] = a;
-                  }
-                  if (b - rv > kTop) {
-                    const float f = ex2_approx(rv - (b - kRaised));
-                    rv = b - kRaised;
+                  for (int d = 4; d < 32; d <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+                  if (r[n][i] != was || b + dv[n][i] > kTop) {
+                    const float up = r[n][i] - was, now = fminf(kRaised - b, dv[n][i] + up);  // (r' does not fall)
+                    const float f = ex2_approx(now - dv[n][i] - up);
+                    l[n][i] *= ex2_approx(-up);
+                    dv[n][i] = now;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                       o[n][j][i] *= f;
                       o[n][j][2 + i] *= f;
                     }
                   }
-                  dv[n][i] = r[n][i] - rv;
 #pragma unroll
                   for (int u = 0; u < kG; ++u)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                      e[u][n][2 * k + i] = s[u][n][2 * k + i] - r[n][i];
-                      ew[u][n][2 * k + i] = e[u][n][2 * k + i] + (ev[u][k] + dv[n][i]);
-                    }
+                    for (int k = 0; k < 2; ++k) ew[u][n][2 * k + i] = e[u][n][2 * k + i] + (ev[u][k] + dv[n][i]);
                 }
             }
 #pragma unroll

@@ -273,6 +273,13 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[2], const char* from, 
   to[1] = y.y;
 }
 
+// Exponents of two weights: scores times c, less the reference (exact: the reference's
+// score subtracted first, so that scores of any size have weights of at most 2^kSlack).
+template <bool kExact>
+__device__ __forceinline__ uint64_t weight_exponents(uint64_t s, uint64_t c2, uint64_t r2) {
+  return kExact ? fma2(add2(s, r2), c2, 0) : fma2(s, c2, r2);
+}
+
 // ---- codes and scales ------------------------------------------------------------------
 
 // A scale's factor for codes in place in bfloat16 fields, twice in a word; rows past 57344
@@ -324,6 +331,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
   constexpr int kSlots = L::kSlots;
   constexpr int kHalves = D / 64;
   constexpr int kLists = kPair ? 1 : 2;  // shares of a CTA
+  constexpr bool kExact = kTree || kQuant;
   extern __shared__ __align__(1024) uint8_t smem[];
   H& sh = *reinterpret_cast<H*>(smem);
   uint8_t* sQ = smem + L::kOffQ;
@@ -838,13 +846,13 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 32; ++w) mx[w & 3] = fmaxf(mx[w & 3], __uint_as_float(y[w]));
           raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
-          const float r = m == kNegInf ? 0.f : m * c;
+          const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
           const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
           uint64_t sum2[2] = {0, 0};
           uint32_t pk[16], none[16];
 #pragma unroll
           for (int w = 0; w < 16; ++w) {
-            const uint64_t e = fma2(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
+            const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
             float2 f = unpack2(e);
             f.x = ex2_approx(f.x);
             f.y = ex2_approx(f.y);
@@ -917,7 +925,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
                   mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
             }
             raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
-            const float r = m == kNegInf ? 0.f : m * c;
+            const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
             const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
             uint64_t sum2[2] = {0, 0};
 #pragma unroll 1
@@ -929,7 +937,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
               reg_dep32(y + 32);
 #pragma unroll
               for (int w = 0; w < 32; ++w) {
-                const uint64_t e = fma2(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
+                const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
                 float2 f = unpack2(e);
                 f.x = ex2_approx(f.x);
                 f.y = ex2_approx(f.y);
@@ -958,7 +966,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
               mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
           }
           raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
-          const float r = m == kNegInf ? 0.f : m * c;
+          const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
           const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
           uint64_t sum2[2] = {0, 0};
 #pragma unroll
@@ -966,7 +974,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int w = 0; w < 16; ++w) {
-              const uint64_t e = fma2(pack2(__uint_as_float(y[32 * q + 2 * w]), __uint_as_float(y[32 * q + 2 * w + 1])), c2, r2);
+              const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[32 * q + 2 * w]), __uint_as_float(y[32 * q + 2 * w + 1])), c2, r2);
               float2 f = unpack2(e);
               f.x = ex2_approx(f.x);
               f.y = ex2_approx(f.y);
@@ -1111,7 +1119,8 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
               bool seen = __shfl_sync(0xffffffffu, place >= 0, j0 + lane / kR) && key >= my_a && key < my_z;
               if (kTree && tree) seen = seen && tree_sees(my_words, key, x.ctx);
               if (kQuant) w[0] *= __shfl_sync(0xffffffffu, k_scale, j0 + lane / kR);
-              const float mine = seen ? ex2_approx(fmaf(w[0], c, -my_ref)) : -1.f;
+              const float at = fmaf(w[0], c, -my_ref);
+              const float mine = seen ? ex2_approx(kExact ? fminf(at, kSlack) : at) : -1.f;
 #pragma unroll
               for (int j = 0; j < kK; ++j)
 #pragma unroll

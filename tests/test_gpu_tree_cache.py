@@ -303,6 +303,71 @@ def test_quantised_attention_of_few_rows(kv, D, G, n_q, causal, window):
           causal=causal, seed=G).verify(kv)
 
 
+@pytest.mark.parametrize("D,Hk,G,n_q", [(64, 4, 2, 1), (64, 8, 1, 5), (64, 6, 4, 2), (128, 4, 8, 1), (128, 6, 3, 5), (64, 4, 5, 3), (128, 3, 4, 2)])
+@pytest.mark.parametrize("S,layout", [(16, "nhd"), (64, "hnd"), (128, "nhd"), (256, "hnd")])
+def test_quantised_attention_of_few_rows_and_many_heads(kv, D, Hk, G, n_q, S, layout):
+    """Groups of one, two and four KV heads; pages below, at and above a tile's keys of a head."""
+    Batch("e4m3", D, S, Hk, G, [(n_q, n) for n in (5, 31, 33, 64, 255, 700)] + [(0, 9), (1, 0)], layout=layout, seed=D + Hk).verify(kv)
+
+
+@pytest.mark.parametrize("G,n_q", [(2, 1), (4, 4), (4, 30), (8, 40)])
+def test_quantised_attention_of_large_keys_and_values(kv, G, n_q):
+    """Keys of 2^110 and values of 2^100 (scores far past any exponent: one key has all the weight); nothing overflows."""
+    b = Batch("e4m3", 128, 16, 2, G, [(n_q, 200)], seed=G)
+    far = b.scales != 255
+    far[:, :, 1] = False
+    b.scales[far] = 230
+    values = b.scales != 255
+    values[:, :, 0] = False
+    b.scales[values] = 220
+    b.q *= 2.0 ** -60
+    assert b.call(kv) == 0
+    assert torch.isfinite(b.out.float()).all() and torch.isfinite(b.lse).all() and int(b.status[0]) == 0
+    k, v = _pool_values(b.k[0], b.v[0], b.scales[0])
+    pages = b.table[0].tolist()
+    kk, vv = (x[pages].reshape(-1, 2, 128)[:200] for x in (k, v))
+    for t in (0, n_q - 1):
+        for h in range(2 * G):
+            s = kk[:, h // G] @ _host(b.q[t, h])
+            s[200 - n_q + t + 1:] = -np.inf
+            first, second = np.sort(s)[::-1][:2]
+            if (first - second) * ref.default_scale(128) > 30:      # the others' weights: below 1e-12
+                got, want = _host(b.out[t, h]), vv[s.argmax(), h // G]
+                assert (np.abs(got - want) <= 2.0 ** -7 * np.abs(want) + 1e-12 * np.abs(vv).max()).all()
+
+
+@pytest.mark.parametrize("G,n_q", [(2, 3), (4, 4), (4, 30), (8, 40)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_quantised_attention_of_a_query_that_is_not_finite(kv, G, n_q, what):
+    """It has no effect on other rows."""
+    lens = [(n_q, 300), (2, 50)]
+    b = Batch("e4m3", 128, 16, 2, G, lens, seed=G)
+    b.verify(kv)
+    good = b.out.clone()
+    b.q[1, 1, 5] = what
+    assert b.call(kv) == 0
+    b.out[1, 1], good[1, 1] = 0, 0
+    assert torch.equal(b.out, good) and int(b.status[0]) == 0
+
+
+@pytest.mark.parametrize("G,n_q", [(1, 4), (4, 4), (4, 40), (2, 100)])
+def test_quantised_attention_of_a_key_that_some_do_not_see(kv, G, n_q):
+    """A key of NaN (its scale says so) makes the rows that see it NaN, and no others."""
+    n = 260
+    b = Batch("e4m3", 64, 16, 1, G, [(n_q, n)], seed=n_q)
+    at = n - n_q // 2
+    page, place = int(b.table[0, at // 16]), at % 16
+    b.scales[0, page, 0, 0, place] = 255
+    assert b.call(kv) == 0
+    first = at - (n - n_q)
+    assert torch.isnan(b.out[first:].float()).all() and torch.isfinite(b.out[:first].float()).all()
+    keep, keep_lse = b.out[:first].clone(), b.lse[:first].clone()
+    b.scales[0, page, 0, 0, place] = 120
+    assert b.call(kv) == 0
+    b.out[:first], b.lse[:first] = keep, keep_lse
+    b.compare()
+
+
 @pytest.mark.parametrize("spread", [1e-4, 3.0])
 def test_quantised_attention_of_small_and_peaked_scores(kv, spread):
     Batch("e4m3", 128, 16, 2, 4, [(3, 500), (20, 300)], spread=spread, seed=5).verify(kv)
@@ -625,6 +690,50 @@ def test_update_and_compact_of_a_quantised_pool(kv, S, Hk, D, layout):
         assert q < int(used) and int(r3[q]) == int(r2[p])
         for x, y in zip((_bytes(k), _bytes(v), scales), was):
             assert torch.equal(x[:, q], y[:, p])
+
+
+def test_quantised_places_past_32_bits(kv):
+    """Pages more than 2^32 bytes into a quantised pool: written, read by few rows and by many, kept, copied on write, moved."""
+    N, S, Hk, D, G = 270000, 16, 8, 128, 2
+    g = torch.Generator(device="cuda").manual_seed(12)
+    c = kv.PagedCache(1, N, S, Hk, D, 3, 400, dtype=torch.float8_e4m3fn)
+    c.ref[:N - 60] = 1                    # somebody else's: new pages are the last ones
+    c.update(_i32([70, 300, 0]))
+    assert int(c.block_table[0, 0]) == N - 60
+    kn, vn = (torch.randn((370, Hk, D), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    c.append(0, kn, vn, _i32([0, 70, 370, 370]))
+    held = [np.ldexp(x, e[..., None]) for x, e in (ref.quantise(_host(y)) for y in (kn, vn))]
+    past = [np.stack([x[:70] for x in held]), np.stack([x[70:] for x in held]), np.stack([x[:70] for x in held])]
+
+    def check(n, pages):
+        q = torch.randn((sum(n), Hk * G, D), device="cuda", generator=g).to(torch.bfloat16)
+        start = np.concatenate([[0], np.cumsum(n)])
+        out = c.attend(0, q, _i32(start), max(n))
+        c.check_status()
+        lens = [x.shape[1] for x in past]
+        assert c.kv_len.tolist() == lens
+        kp, vp = (np.zeros((3, max(lens), Hk, D)) for _ in range(2))
+        for b in range(3):
+            kp[b, :lens[b]], vp[b, :lens[b]] = past[b]
+        want, _, tol, _ = ref.attend(_host(q), kp, vp, np.arange(3)[:, None], lens, start, lambda b: ref.causal_seen(n[b], lens[b]),
+                                     ref.default_scale(D), True)
+        assert (np.abs(_host(out) - want) <= tol).all()
+        table = c.block_table[c.block_table >= 0]
+        assert pages(int(table.min()), int(table.max()))
+
+    c.update(_i32([70, 300, 70]), parent=_i32([0, 1, 0]))
+    check([3, 1, 4], lambda lo, hi: lo >= N - 60)
+    check([3, 9, 40], lambda lo, hi: lo >= N - 60)
+    c.update(_i32([75, 300, 73]))         # both write into the shared last page: one copy
+    new = [torch.randn((8, Hk, D), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2)]
+    c.append(0, new[0], new[1], _i32([0, 5, 5, 8]))
+    x = np.stack([np.ldexp(y, e[..., None]) for y, e in (ref.quantise(_host(z)) for z in new)])
+    c.keep(_i32([[1, 2, 4], [-1, -1, -1], [0, 2, -1]]), _i32([0, 5, 5, 8]))
+    past = [np.concatenate([past[0], x[:, [1, 2, 4]]], 1), past[1], np.concatenate([past[2], x[:, [5, 7]]], 1)]
+    check([2, 1, 1], lambda lo, hi: lo >= N - 60)
+    c.ref[:N - 60] = 0
+    c.compact()
+    check([20, 1, 7], lambda lo, hi: hi < 60)
 
 
 # ---- together ------------------------------------------------------------------------------
