@@ -246,8 +246,8 @@ ds_status ds_cache_compact_scaled(const ds_compact_args* args, uint8_t* scales, 
  *   the context's tokens (window > 0: those at p - window + 1 and after,
  *                          p = kv_len - n_b + depth[i], depth 0 without `depth`),
  *   the new tokens of its mask, itself among them only if its bit is set.
- * Bits of tokens past n_b count for nothing. A negative depth counts as 0. `causal` of
- * the arguments has to be 1. A request with rows but kv_len < n_b has no context, and
+ * Bits of tokens past n_b count for nothing. A negative depth counts as 0, one past 2^29
+ * as that. `causal` of the arguments has to be 1. A request with rows but kv_len < n_b has no context, and
  * its first n_b - kv_len tokens have no place: their bits count for nothing. Table
  * entries are needed for all pages from the first that a row of depth 0 would see.
  */

@@ -370,8 +370,12 @@ ds_status ds_paged_attention_tree(const ds_attention_args* a, const uint8_t* sca
   p.group = a->n_heads / a->pool.n_kv_heads;
   p.by_group.set((uint32_t)p.group);
   p.causal = a->causal;
-  // a window as long as the table hides nothing
-  p.window = (int64_t)a->window >= (int64_t)a->max_pages * a->pool.page_size ? 0 : a->window;
+  // a window as long as the table hides nothing (but of a tree's depths, which may be larger)
+  const bool deep = tree != nullptr && tree->depth != nullptr;
+  constexpr int32_t kLongest = INT32_MAX - (1 << 24);  // past any position and depth (2^30, 2^29), without overflow
+  p.window = !deep && (int64_t)a->window >= (int64_t)a->max_pages * a->pool.page_size ? 0
+             : a->window < kLongest                                                   ? a->window
+                                                                                      : kLongest;
   p.scale = a->scale;
   p.q = static_cast<const char*>(a->q);
   p.out = static_cast<char*>(a->out);

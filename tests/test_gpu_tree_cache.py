@@ -476,6 +476,22 @@ def test_tree_attention_without_depths_and_wide_masks(kv, dtype, n, G):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("n,G", [(4, 2), (30, 4)])
+def test_tree_attention_of_depths_past_a_window_longer_than_the_table(kv, dtype, n, G):
+    """Depths are the caller's: a row far below its context sees little of it, or nothing."""
+    b = Batch(dtype, 64, 16, 2, G, [(n, n + 300), (2, 90)], window=5000, seed=n, trees=[_mixed] * 2)
+    far = [0, 4800, 4990, 6000][:n] + [0] * (n - 4) + [2**31 - 1, 4950]
+    b.depth += _i32(far)
+    depth, seen = b.depth.cpu().numpy().astype(np.int64), []
+    for at, (m, total), s in zip((0, n), [(n, n + 300), (2, 90)], b.seen):
+        first = total - m
+        low = first + depth[at:at + m, None] - 5000 + 1
+        seen.append(np.concatenate([np.arange(first) >= low, s[:, first:]], axis=1))
+    b.seen = seen
+    b.verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
 @pytest.mark.parametrize("D,G,n", [(128, 1, 9), (64, 2, 8), (64, 4, 40), (128, 4, 70)])
 @pytest.mark.parametrize("window", [0, 50])
 def test_tree_attention_of_nan_in_other_branches(kv, dtype, D, G, n, window):
