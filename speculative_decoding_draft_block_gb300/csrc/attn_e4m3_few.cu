@@ -734,6 +734,8 @@ cudaError_t launch(const AttnParams& given, cudaStream_t s) {
   p.pool.n_kv_heads /= KH;
   const cudaError_t e = launch_early(kernel, dim3(kMaxShares), dim3(32 * (kWarps + 2)), kSmem, s, p, heads, mk, mv);
   if (e != cudaSuccess) return e;
+  // (four rows a block of the join: KH heads' rows stand together. Tokens of 128 requests 104.7 us,
+  // of short ones 22.6; two a block 106 and 23.2)
   return launch_join<FormFew<NT, KH>, D, __nv_bfloat16, 4>(p, s, p.max_q * p.group, 8 * NT * KH, 8 * NT * KH);
 }
 

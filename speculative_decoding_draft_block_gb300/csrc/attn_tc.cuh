@@ -72,7 +72,11 @@
 // A code is sign, 4 bits of exponent (bias 7), 3 of fraction; moved to the
 // bfloat16's fields it is the number times 2^-120, subnormal codes included, and one
 // multiplication by 2^(scale - 127 + 120) finishes it (two for scales from 135, rows past
-// 57344). NaN as the factor is a row's NaN.
+// 57344). NaN as the factor is a row's NaN. Codes halve the bytes, but shared memory moves 1 + 2 + 2
+// of them a code (restoring reads and writes, the product reads), and prompts and trees are bound by
+// that and by the softmax beside it: 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384
+// cached 614 to 626 us (1.15 PFLOP/s), bfloat16 468; 128 trees over 500 to 6000 cached 313 to 325. Four
+// restoring warps, the softmax a row at a time: 628 and 336.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -951,40 +955,40 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
             const float2 sum = unpack2(add2(sum2[0], sum2[1]));
             l += sum.x + sum.y;
           } else {
-          uint32_t y[128];
+            uint32_t y[128];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32_issue(tS + 32 * q, y + 32 * q);
-          tmem_ld_wait(y);
-          reg_dep32(y + 32);
-          reg_dep32(y + 64);
-          reg_dep32(y + 96);
-          float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            for (int q = 0; q < 4; ++q) tmem_ld32_issue(tS + 32 * q, y + 32 * q);
+            tmem_ld_wait(y);
+            reg_dep32(y + 32);
+            reg_dep32(y + 64);
+            reg_dep32(y + 96);
+            float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-          for (int q = 0; q < 128; q += 8) {
+            for (int q = 0; q < 128; q += 8) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
-          }
-          raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
-          const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
-          const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
-          uint64_t sum2[2] = {0, 0};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int w = 0; w < 16; ++w) {
-              const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[32 * q + 2 * w]), __uint_as_float(y[32 * q + 2 * w + 1])), c2, r2);
-              float2 f = unpack2(e);
-              f.x = ex2_approx(f.x);
-              f.y = ex2_approx(f.y);
-              sum2[w & 1] = add2(sum2[w & 1], pack2(f.x, f.y));
-              pk[w] = to_bf16x2(f.x, f.y);
+              for (int w = 0; w < 4; ++w)
+                mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
             }
-            tmem_st16(tS + 16 * q, pk);
-          }
-          const float2 sum = unpack2(add2(sum2[0], sum2[1]));
-          l += sum.x + sum.y;
+            raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
+            const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
+            const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int w = 0; w < 16; ++w) {
+                const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[32 * q + 2 * w]), __uint_as_float(y[32 * q + 2 * w + 1])), c2, r2);
+                float2 f = unpack2(e);
+                f.x = ex2_approx(f.x);
+                f.y = ex2_approx(f.y);
+                sum2[w & 1] = add2(sum2[w & 1], pack2(f.x, f.y));
+                pk[w] = to_bf16x2(f.x, f.y);
+              }
+              tmem_st16(tS + 16 * q, pk);
+            }
+            const float2 sum = unpack2(add2(sum2[0], sum2[1]));
+            l += sum.x + sum.y;
           }
           tmem_st_wait();
         }
@@ -1431,18 +1435,18 @@ cudaError_t launch_form(const AttnParams& p, cudaStream_t s) {
   // 111 and 113. (The quarters' sums of 16 rows fill the staging slot.)
   const int per_tile = kTile / p.group;
   const bool pair = p.max_q > per_tile && p.T > (int64_t)p.B * per_tile;
-  const bool few = !kQuant && (int64_t)p.max_q * p.group <= kFewRows;  // (quantised: attn_e4m3_few.cu)
   if constexpr (kQuant) {
     if (p.D == 128) return pair ? launch<128, kPairs, kTree, true>(p, s) : launch<128, kSolo, kTree, true>(p, s);
     return pair ? launch<64, kPairs, kTree, true>(p, s) : launch<64, kSolo, kTree, true>(p, s);
   } else {
-  if (p.D == 128)
-    return few    ? launch<128, kFew, kTree, kQuant>(p, s)
-           : pair ? launch<128, kPairs, kTree, kQuant>(p, s)
-                  : launch<128, kSolo, kTree, kQuant>(p, s);
-  return few    ? launch<64, kFew, kTree, kQuant>(p, s)
-         : pair ? launch<64, kPairs, kTree, kQuant>(p, s)
-                : launch<64, kSolo, kTree, kQuant>(p, s);
+    const bool few = (int64_t)p.max_q * p.group <= kFewRows;
+    if (p.D == 128)
+      return few    ? launch<128, kFew, kTree, false>(p, s)
+             : pair ? launch<128, kPairs, kTree, false>(p, s)
+                    : launch<128, kSolo, kTree, false>(p, s);
+    return few    ? launch<64, kFew, kTree, false>(p, s)
+           : pair ? launch<64, kPairs, kTree, false>(p, s)
+                  : launch<64, kSolo, kTree, false>(p, s);
   }
 }
 

@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // the only one. Powers of two cost the format at most one of its 17 binades and no
 // precision, and let the attention restore a row exactly in bfloat16.
 //
-// 2 T Hk D (2 + 1) bytes are moved. A lane takes 16 values of K and of V, the
-// power of two of lanes that D / 16 asks for a row's maximum.
+// 2 T Hk D (2 + 1) bytes are moved: bound by memory (16 prompts of 8 heads of 128 values, 347 MB,
+// 60 us: 5.8 TB/s), of few rows by the launch (64: 3.5 us of their own). A lane takes 16 values
+// of K and of V, the power of two of lanes that D / 16 asks for a row's maximum.
 constexpr int kLowestScale = 27, kNoScale = 255;  // bytes: e = -100; a row that is not finite
 
 // The scale byte of a row whose largest |x| has these bits.
@@ -262,16 +263,15 @@ bool overlap(const void* a, const void* b, size_t na, size_t nb) {
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   const int pieces = p.pool.n_kv_heads * (p.pool.row_bytes >> 4);  // 16-byte pieces of a row
-  if (p.pool.scales != nullptr) {
-    const int tokens = pieces >= 32 ? 8 : 32;
-    return launch_early(tokens == 8 ? append_e4m3_kernel<8> : append_e4m3_kernel<32>, dim3((p.T + tokens - 1) / tokens),
-                        dim3(kAppendThreads), 0, s, p);
-  }
   // Eight rows of 1 KB and more keep a block's threads busy, of smaller rows it takes
   // more: 16 prompts (56 k rows) of 128 bytes 6.2 us by 32 rows a block, 12.3 by 8;
-  // of 512 bytes 22.0 and 23.1; of 1 KB 39.3 and 38.4; of 2 KB 74.4 and 71.8.
+  // of 512 bytes 22.0 and 23.1; of 1 KB 39.3 and 38.4; of 2 KB 74.4 and 71.8. Codes, whose
+  // pieces take two loads and a conversion, of 128 bytes 10.9 by 32, 21.2 by 8; of 512
+  // 31.9 and 36.6; of 1 KB 59.4 and 60.4, and 64 rows of them 8.4 and 6.7; of 2 KB 116 and 109.
   const int tokens = pieces >= 64 ? 8 : 32;
   const dim3 blocks((p.T + tokens - 1) / tokens);
+  if (p.pool.scales != nullptr)
+    return launch_early(tokens == 8 ? append_e4m3_kernel<8> : append_e4m3_kernel<32>, blocks, dim3(kAppendThreads), 0, s, p);
   return launch_early(tokens == 8 ? append_kernel<8> : append_kernel<32>, blocks, dim3(kAppendThreads), 0, s, p);
 }
 
