@@ -301,8 +301,15 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two codes, each in the upper byte of its half of p, in bfloat16 fields.
-__device__ __forceinline__ uint32_t code_fields(uint32_t p) { return (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u); }
+// Codes i and i + 1 of a word (i = 0, 2) in bfloat16 fields: each with its sign extended to 16 bits
+// (a permute of bytes does that), four bits up, without the sign's bits above the exponent's.
+// (What leaves the lower half comes to the upper one's lowest bits, which are not kept.)
+template <int i>
+__device__ __forceinline__ uint32_t code_fields(uint32_t w) {
+  uint32_t p;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(p) : "r"(w), "n"(i == 0 ? 0x9180 : 0xb3a2));
+  return (p * 16u) & 0x87f087f0u;
+}
 
 // Code d of a lane's bytes as a number, and a scale as one.
 __device__ __forceinline__ float code_value(uint32_t bytes, int d) {
@@ -606,7 +613,9 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         const uint32_t more = first ? 0u : 1u;
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_bf16_ta(tm + 256 + s * D, tm + s * kTile + k * 8, b + k * (2048 >> 4), ipv, k != 0 ? 1u : more);
+          // (quantised: the weights of the second 64 keys stand over their scores)
+          mma_bf16_ta(tm + 256 + s * D, tm + s * kTile + k * 8 + (kQuant && k >= 4 ? 32 : 0), b + k * (2048 >> 4), ipv,
+                      k != 0 ? 1u : more);
         if (free_v) mma_commit(&sh.empty[slot]);
         if (last) mma_commit(&sh.pv_done[s]);
       };
@@ -912,12 +921,14 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
             tmem_st_wait();
           }
           if constexpr (kQuant) {
-            // Half of the row at a time, read twice: the registers go to the restoring warps, and
-            // the code is half as long (the warps share one instruction cache).
+            // Half of the row at a time: the registers go to the restoring warps, and the code is
+            // half as long (the warps share one instruction cache). The second half stays in
+            // registers for its weights, the first one is read again; a half's weights stand over
+            // its own scores (see pv).
+            uint32_t y[64];
             float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll 1
             for (int h = 0; h < kTile; h += 64) {
-              uint32_t y[64];
               tmem_ld32_issue(tS + h, y);
               tmem_ld32_issue(tS + h + 32, y + 32);
               tmem_ld_wait(y);
@@ -929,28 +940,28 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
                   mx[w] = fmaxf(mx[w], fmaxf(__uint_as_float(y[q + 2 * w]), __uint_as_float(y[q + 2 * w + 1])));
             }
             raise_to(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), it);
-            const float r = m == kNegInf ? 0.f : kExact ? m : m * c;
+            const float r = m == kNegInf ? 0.f : m;
             const uint64_t c2 = pack2(c, c), r2 = pack2(-r, -r);
             uint64_t sum2[2] = {0, 0};
 #pragma unroll 1
-            for (int h = 0; h < kTile; h += 64) {
-              uint32_t y[64];
-              tmem_ld32_issue(tS + h, y);
-              tmem_ld32_issue(tS + h + 32, y + 32);
-              tmem_ld_wait(y);
-              reg_dep32(y + 32);
+            for (int h = 64; h >= 0; h -= 64) {
 #pragma unroll
               for (int w = 0; w < 32; ++w) {
-                const uint64_t e = weight_exponents<kExact>(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
+                const uint64_t e = weight_exponents<true>(pack2(__uint_as_float(y[2 * w]), __uint_as_float(y[2 * w + 1])), c2, r2);
                 float2 f = unpack2(e);
                 f.x = ex2_approx(f.x);
                 f.y = ex2_approx(f.y);
                 sum2[w & 1] = add2(sum2[w & 1], pack2(f.x, f.y));
                 y[w] = to_bf16x2(f.x, f.y);
               }
-              // (over scores that have been read)
-              tmem_st16(tS + h / 2, y);
-              tmem_st16(tS + h / 2 + 16, y + 16);
+              tmem_st16(tS + h, y);
+              tmem_st16(tS + h + 16, y + 16);
+              if (h != 0) {
+                tmem_ld32_issue(tS, y);
+                tmem_ld32_issue(tS + 32, y + 32);
+                tmem_ld_wait(y);
+                reg_dep32(y + 32);
+              }
             }
             const float2 sum = unpack2(add2(sum2[0], sum2[1]));
             l += sum.x + sum.y;
@@ -1343,10 +1354,10 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
                 const int r = (i0 + i) * kRows;
                 const uint32_t f = __shfl_sync(0xffffffffu, factor, r + r0);
                 uint32_t y[4];
-                y[0] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x1404)), f);
-                y[1] = mul_bf16x2(code_fields(__byte_perm(x[i].x, 0, 0x3424)), f);
-                y[2] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x1404)), f);
-                y[3] = mul_bf16x2(code_fields(__byte_perm(x[i].y, 0, 0x3424)), f);
+                y[0] = mul_bf16x2(code_fields<0>(x[i].x), f);
+                y[1] = mul_bf16x2(code_fields<2>(x[i].x), f);
+                y[2] = mul_bf16x2(code_fields<0>(x[i].y), f);
+                y[3] = mul_bf16x2(code_fields<2>(x[i].y), f);
                 if constexpr (decltype(twice)::value) {
                   const uint32_t f2 = __shfl_sync(0xffffffffu, factor2, r + r0);
 #pragma unroll
