@@ -75,8 +75,9 @@
 // 57344). NaN as the factor is a row's NaN. Codes halve the bytes, but shared memory moves 1 + 2 + 2
 // of them a code (restoring reads and writes, the product reads), and prompts and trees are bound by
 // that and by the softmax beside it: 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384
-// cached 614 to 626 us (1.15 PFLOP/s), bfloat16 468; 128 trees over 500 to 6000 cached 313 to 325. Four
-// restoring warps, the softmax a row at a time: 628 and 336.
+// cached 593 us (1.21 PFLOP/s), bfloat16 468; 128 trees of 8 to 60 tokens over 500 to 6000 cached
+// 292, bfloat16 247; 128 blocks of 8 tokens over 300 to 8000 cached 217. Without the restoring's arithmetic
+// 560 us of the prompts; a mask and a shift more a pair of codes cost 25 of them and 20 of the blocks'.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1445,7 +1446,12 @@ cudaError_t launch_form(const AttnParams& p, cudaStream_t s) {
   // and 197, D = 64 158 and 164; 512 of 2 rows, 1 to 300 cached 63 and 85; 64 of 16 rows
   // 111 and 113. (The quarters' sums of 16 rows fill the staging slot.)
   const int per_tile = kTile / p.group;
-  const bool pair = p.max_q > per_tile && p.T > (int64_t)p.B * per_tile;
+  // Trees, whose masks cost the softmax more: from three quarters of a row tile on average. 128
+  // trees that fill 0.81 of one, 500 to 6000 cached: pair 247 us, solo 267 (codes 292 and 307); 0.62
+  // to 0.73 of one: 238 to 244 and 237 to 254 (280 to 289 and 258 to 283). (Codes without masks, 0.72
+  // and 0.81: 303 and 307, 283 and 301.)
+  const int64_t tiles4 = p.mask != nullptr ? 3 : 4;
+  const bool pair = p.max_q > per_tile && 4 * (int64_t)p.T > tiles4 * p.B * per_tile;
   if constexpr (kQuant) {
     if (p.D == 128) return pair ? launch<128, kPairs, kTree, true>(p, s) : launch<128, kSolo, kTree, true>(p, s);
     return pair ? launch<64, kPairs, kTree, true>(p, s) : launch<64, kSolo, kTree, true>(p, s);
