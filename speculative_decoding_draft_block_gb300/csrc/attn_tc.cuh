@@ -75,9 +75,9 @@
 // 57344). NaN as the factor is a row's NaN. Codes halve the bytes, but shared memory moves 1 + 2 + 2
 // of them a code (restoring reads and writes, the product reads), and prompts and trees are bound by
 // that and by the softmax beside it: 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384
-// cached 593 us (1.21 PFLOP/s), bfloat16 468; 128 trees of 8 to 60 tokens over 500 to 6000 cached
-// 292, bfloat16 247; 128 blocks of 8 tokens over 300 to 8000 cached 217. Without the restoring's arithmetic
-// 560 us of the prompts; a mask and a shift more a pair of codes cost 25 of them and 20 of the blocks'.
+// cached 577 us (1.24 PFLOP/s), bfloat16 468; 128 trees of 8 to 60 tokens over 500 to 6000 cached
+// 292, bfloat16 247; 128 blocks of 8 tokens over 300 to 8000 cached 215. (A mask and a shift more a pair
+// of codes cost the prompts 25 us and the blocks 20.)
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -789,10 +789,9 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
       }
       // keys this row sees (of a tree's row: without its mask's); a row that is not there
       // sees all and is never stored
-      const bool tree = kTree && (!kQuant || p.mask != nullptr);
-      const uint32_t* words = tree && valid ? p.mask + t_out * p.mask_words : nullptr;
-      const int hi = !valid ? INT32_MAX : tree ? x.ctx : p.causal ? min(pos + 1, x.kv) : x.kv;
-      const int lo = !valid ? 0 : tree ? tree_low(p, x.ctx, t_out) : p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const uint32_t* words = kTree && valid ? p.mask + t_out * p.mask_words : nullptr;
+      const int hi = !valid ? INT32_MAX : kTree ? x.ctx : p.causal ? min(pos + 1, x.kv) : x.kv;
+      const int lo = !valid ? 0 : kTree ? tree_low(p, x.ctx, t_out) : p.window > 0 ? max(0, pos - p.window + 1) : 0;
       const bool work = __any_sync(0xffffffffu, valid);
       float m = kNegInf, l = 0.f;  // reference (a score, before the factor c) and sum
       bool ok = true;
@@ -826,7 +825,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         uint32_t seen4[kForm == kFew ? 1 : 4];
 #pragma unroll
         for (int q = 0; q < (kForm == kFew ? 1 : 4); ++q) seen4[q] = ~0u;
-        if (kTree && tree) {
+        if (kTree) {
           const int first = kForm == kFew ? key + 32 * quarter : key;
           if (valid && (key + kTile > hi || key < lo)) {
 #pragma unroll
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           uint32_t y[32];
           tmem_ld32_issue(tS + 32 * quarter, y);
           tmem_ld_wait(y);
-          if (kTree && tree) {
+          if (kTree) {
             if (__any_sync(0xffffffffu, seen4[0] != ~0u)) {
 #pragma unroll
               for (int w = 0; w < 32; ++w)
@@ -881,7 +880,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           l += sum.x + sum.y;
           tmem_st_wait();
         } else if (work) {
-          if (kTree && tree) {
+          if (kTree) {
             if (__any_sync(0xffffffffu, (seen4[0] & seen4[kForm == kFew ? 0 : 1] & seen4[kForm == kFew ? 0 : 2] &
                                          seen4[kForm == kFew ? 0 : 3]) != ~0u)) {
 #pragma unroll 1
@@ -1064,7 +1063,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
               my_a = ra;
               my_z = rz;
               my_ref = rr;
-              if (kTree && tree) my_words = p.mask + (int64_t)t * p.mask_words;
+              if (kTree) my_words = p.mask + (int64_t)t * p.mask_words;
             }
             if (!there) from[r] = -1;
           }
@@ -1133,7 +1132,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
                 }
               const int key = k0 + j0 + lane / kR;
               bool seen = __shfl_sync(0xffffffffu, place >= 0, j0 + lane / kR) && key >= my_a && key < my_z;
-              if (kTree && tree) seen = seen && tree_sees(my_words, key, x.ctx);
+              if (kTree) seen = seen && tree_sees(my_words, key, x.ctx);
               if (kQuant) w[0] *= __shfl_sync(0xffffffffu, k_scale, j0 + lane / kR);
               const float at = fmaf(w[0], c, -my_ref);
               const float mine = seen ? ex2_approx(kExact ? fminf(at, kSlack) : at) : -1.f;
@@ -1237,8 +1236,8 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           const float probe = fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, y.w * 0.f)));
           const uint32_t bad = __ballot_sync(0xffffffffu, there && probe != probe && r_l == r_l);
           if (bad != 0) {
-            const int r_pos = x.pos + tok, z = p.causal && !tree ? min(r_pos + 1, x.kv) : x.kv;
-            const int a = tree ? (there ? tree_low(p, x.ctx, r_t) : 0) : p.window > 0 ? max(0, r_pos - p.window + 1) : 0;
+            const int r_pos = x.pos + tok, z = p.causal && !kTree ? min(r_pos + 1, x.kv) : x.kv;
+            const int a = kTree ? (there ? tree_low(p, x.ctx, r_t) : 0) : p.window > 0 ? max(0, r_pos - p.window + 1) : 0;
             // (a bit a row: its first lane's)
             const uint32_t again = kChunks == 32 ? 1u : ((bad & 0xffffu) != 0 ? 1u : 0u) | (bad >> 16 != 0 ? 0x10000u : 0u);
             anew(again, (int)r_t, r_head, dst, max(key0, a), min(key1, z), r_ref, r_f);
@@ -1300,7 +1299,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         const float2 probes = unpack2(probe2);
         const float probe = probes.x + probes.y;
         const uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
-        if (again != 0) anew(again, (int)t_out, head, to, max(key0, lo), min(key1, tree ? x.kv : hi), ref, f);
+        if (again != 0) anew(again, (int)t_out, head, to, max(key0, lo), min(key1, kTree ? x.kv : hi), ref, f);
         if (valid) {
           if (!x.whole)
             part.stat[prow] = make_float2(ref, l);

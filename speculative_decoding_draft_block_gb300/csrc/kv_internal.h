@@ -210,6 +210,7 @@ cudaError_t launch_attention_f32(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_tc_tree(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_tc_e4m3(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attention_tc_e4m3_tree(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attention_e4m3_few(const AttnParams& p, cudaStream_t s);
 
 }  // namespace ds
