@@ -538,22 +538,25 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           if (word & kEnd) break;
           const CUtensorMap* map = kv ? &tmV : &tmK;
           uint8_t* dst = sRing + slot * L::kSlotBytes;
-#pragma unroll 1
-          for (int i = 0; i < boxes; ++i) {
-            const int pg = __shfl_sync(0xffffffffu, now, i);
-            if (kQuant) {
-              if (pg != kNoPage && elect_one()) {
-                tma_load_4d_plain(dst + L::kCodes + i * box_bytes, map, &sh.full[slot], 0, token, x.h, pg);
-                bulk_load(&sh.scale[slot][i * rows],
-                          p.pool.scales + (2 * (int64_t)pg + kv) * p.pool.scale_part() + ((int64_t)x.h << shift) + token,
-                          rows, &sh.full[slot]);
-              }
-            } else if (pg != kNoPage && elect_one()) {
-#pragma unroll
-              for (int y = 0; y < kHalves; ++y)
-                tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[slot], y * 64, token, x.h, pg);
+          if constexpr (kQuant) {
+            if (now != kNoPage) {  // (a lane a page)
+              tma_load_4d_plain(dst + L::kCodes + lane * box_bytes, map, &sh.full[slot], 0, token, x.h, now);
+              bulk_load(&sh.scale[slot][lane * rows],
+                        p.pool.scales + (2 * (int64_t)now + kv) * p.pool.scale_part() + ((int64_t)x.h << shift) + token,
+                        rows, &sh.full[slot]);
             }
             __syncwarp();
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < boxes; ++i) {
+              const int pg = __shfl_sync(0xffffffffu, now, i);
+              if (pg != kNoPage && elect_one()) {
+#pragma unroll
+                for (int y = 0; y < kHalves; ++y)
+                  tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[slot], y * 64, token, x.h, pg);
+              }
+              __syncwarp();
+            }
           }
         }
         if (!ok || (ended && (word & kEnd))) break;
