@@ -538,26 +538,21 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           if (word & kEnd) break;
           const CUtensorMap* map = kv ? &tmV : &tmK;
           uint8_t* dst = sRing + slot * L::kSlotBytes;
-          if constexpr (kQuant) {
-            if (now != kNoPage) {  // (a lane a page)
+          // A lane a page: one after the other from an elected lane they took as long as the
+          // tile's way (prompts over pages of 16 tokens 497 us, now 475; codes, blocks of 8: 284, 222).
+          if (now != kNoPage) {
+            if constexpr (kQuant) {
               tma_load_4d_plain(dst + L::kCodes + lane * box_bytes, map, &sh.full[slot], 0, token, x.h, now);
               bulk_load(&sh.scale[slot][lane * rows],
                         p.pool.scales + (2 * (int64_t)now + kv) * p.pool.scale_part() + ((int64_t)x.h << shift) + token,
                         rows, &sh.full[slot]);
-            }
-            __syncwarp();
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < boxes; ++i) {
-              const int pg = __shfl_sync(0xffffffffu, now, i);
-              if (pg != kNoPage && elect_one()) {
+            } else {
 #pragma unroll
-                for (int y = 0; y < kHalves; ++y)
-                  tma_load_4d_plain(dst + i * box_bytes + y * (kTile * 128), map, &sh.full[slot], y * 64, token, x.h, pg);
-              }
-              __syncwarp();
+              for (int y = 0; y < kHalves; ++y)
+                tma_load_4d_plain(dst + lane * box_bytes + y * (kTile * 128), map, &sh.full[slot], y * 64, token, x.h, now);
             }
           }
+          __syncwarp();
         }
         if (!ok || (ended && (word & kEnd))) break;
         ++n_tiles;
