@@ -506,9 +506,8 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         for (int kv = does_k ? 0 : 1; kv < (does_v ? 2 : 1); ++kv) {
           const uint32_t slot = kv ? vp.slot : kp.slot, parity = kv ? vp.parity : kp.parity;
           const uint32_t number = kv ? vp.number : kp.number;
-          if (number >= (uint32_t)kSlots)
-            ok = __all_sync(0xffffffffu, wait_number(&sh.entry[slot], number - kSlots + 1, watch));
-          ok = ok && wait_bar(&sh.empty[slot], parity ^ 1, watch);
+          ok = __all_sync(0xffffffffu, (number < (uint32_t)kSlots || wait_number(&sh.entry[slot], number - kSlots + 1, watch)) &&
+                                           wait_one(&sh.empty[slot], parity ^ 1, watch, kWaitPolls));
           if (!ok) break;
           if (ended) {
             // (whether the other stream has ended is read after the wait for a slot: what
