@@ -72,12 +72,12 @@
 // A code is sign, 4 bits of exponent (bias 7), 3 of fraction; moved to the
 // bfloat16's fields it is the number times 2^-120, subnormal codes included, and one
 // multiplication by 2^(scale - 127 + 120) finishes it (two for scales from 135, rows past
-// 57344). NaN as the factor is a row's NaN. Codes halve the bytes, but shared memory moves 1 + 2 + 2
-// of them a code (restoring reads and writes, the product reads), and prompts and trees are bound by
-// that and by the softmax beside it: 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384
-// cached 577 us (1.24 PFLOP/s), bfloat16 468; 128 trees of 8 to 60 tokens over 500 to 6000 cached
-// 292, bfloat16 247; 128 blocks of 8 tokens over 300 to 8000 cached 215. (A mask and a shift more a pair
-// of codes cost the prompts 25 us and the blocks 20.)
+// 57344). NaN as the factor is a row's NaN. Codes halve the bytes, but the restoring takes issue slots
+// beside the softmax (four instructions a pair of codes; with five, prompts took 20 us and blocks of 8
+// tokens 20 us more), and shared memory moves 1 + 2 + 2 bytes a code (restoring reads and writes, the product
+// reads). 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384 cached 577 to 582 us (1.24 PFLOP/s),
+// bfloat16 466; 128 trees of 8 to 60 tokens over 500 to 6000 cached 285, bfloat16 245; 128 blocks of
+// 8 tokens over 300 to 8000 cached 206, bfloat16 208.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
