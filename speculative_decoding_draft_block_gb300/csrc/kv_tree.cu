@@ -64,46 +64,36 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreePara
 // order. A thread takes 16 bytes of a head's row of K or V of one layer (or its scale) and
 // all rows of the path, kFlight at a time: no two threads share bytes. 2 * 2 * moved rows'
 // bytes; rows that stand in their place already are left there. Bound by memory, in pieces of
-// a head's row (128 trees of 8 to 60 nodes, 32 layers of 8 heads, 138 MB: 25 us, 5.4 TB/s),
+// a head's row (128 trees of 8 to 60 nodes, 32 layers of 8 heads, 138 MB: 23.7 us, 5.8 TB/s),
 // of few rows by the launch and the chain path, table, row (3.0 us of their own).
 constexpr int kKeepThreads = 256;
 constexpr int kFlight = 8;
 
 struct Step {
-  int64_t from, to;  // byte offsets in a layer
-  int2 page, token;  // from, to
+  int64_t from, to;              // byte offsets in a layer
+  int64_t scale_from, scale_to;  // the same of the scales
 };
 
-template <typename W>
+template <typename W, int64_t Step::*kFrom, int64_t Step::*kTo>
 __device__ __forceinline__ void move_rows(char* base, const Step* step, int n) {
 #pragma unroll 1
   for (int i = 0; i < n; i += kFlight) {
     W y[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (i + f < n) y[f] = __ldcg(reinterpret_cast<const W*>(base + step[i + f].from));
+      if (i + f < n) y[f] = __ldcg(reinterpret_cast<const W*>(base + step[i + f].*kFrom));
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (i + f < n) *reinterpret_cast<W*>(base + step[i + f].to) = y[f];
+      if (i + f < n) *reinterpret_cast<W*>(base + step[i + f].*kTo) = y[f];
   }
 }
 
-__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) {
+__global__ void __launch_bounds__(kKeepThreads, 4) keep_kernel(const KeepParams p) {
   __shared__ Step step[kKeepThreads];
   const int tid = threadIdx.x;
   const PoolView& v = p.pool;
   const int mask = (1 << v.page_shift) - 1, chunks = v.row_bytes >> 4;
-  // this thread's bytes: those of a chunk, head, K or V and layer, or a scale's
-  const int64_t rows = (int64_t)2 * v.n_layers * v.n_kv_heads, all = rows * chunks;
-  const int64_t x = (int64_t)blockIdx.x * kKeepThreads + tid;
-  const bool is_chunk = x < all, is_scale = !is_chunk && v.scales != nullptr && x - all < rows;
-  int64_t y = is_chunk ? x / chunks : x - all;
-  const int c = is_chunk ? (int)(x - y * chunks) : 0;
-  const int h = (int)(y % v.n_kv_heads);
-  y /= v.n_kv_heads;
-  const int kv = (int)(y & 1);
-  const int64_t layer = y >> 1;
-  char* base = (kv ? v.v : v.k) + layer * v.layer_stride + h * v.head_stride + c * 16;
+  const int64_t rows = (int64_t)2 * v.n_layers * v.n_kv_heads, all = rows * chunks, items = all + (v.scales != nullptr ? rows : 0);
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   const int b = blockIdx.y;
@@ -151,29 +141,32 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
     const int n = min(kKeepThreads, m - i0);
     if (tid < n) {
       const int src = first + __ldcg(path + i0 + tid), dst = first + i0 + tid;
+      const int from = __ldcg(table + (src >> v.page_shift)), to = __ldcg(table + (dst >> v.page_shift));
       Step s;
-      s.page = make_int2(__ldcg(table + (src >> v.page_shift)), __ldcg(table + (dst >> v.page_shift)));
-      s.token = make_int2(src & mask, dst & mask);
-      s.from = s.page.x * v.page_stride + s.token.x * v.token_stride;
-      s.to = s.page.y * v.page_stride + s.token.y * v.token_stride;
+      s.from = from * v.page_stride + (src & mask) * v.token_stride;
+      s.to = to * v.page_stride + (dst & mask) * v.token_stride;
+      s.scale_from = 2 * v.scale_part() * from + (src & mask);
+      s.scale_to = 2 * v.scale_part() * to + (dst & mask);
       step[tid] = s;
     }
     __syncthreads();
-    if (is_chunk) move_rows<uint4>(base, step, n);
-    __syncthreads();
-    if (v.scales != nullptr) {
-      if (tid < n) {
-        const Step s = step[tid];
-        step[tid].from = 2 * v.scale_part() * s.page.x + s.token.x;
-        step[tid].to = 2 * v.scale_part() * s.page.y + s.token.y;
-      }
-      __syncthreads();
-      if (is_scale)
-        move_rows<uint8_t>(reinterpret_cast<char*>(v.scales) + layer * v.scale_layer() + kv * v.scale_part() +
-                               ((int64_t)h << v.page_shift),
-                           step, n);
-      __syncthreads();
+    // a thread's bytes: those of a chunk, head, K or V and layer, or a scale's
+    for (int64_t x = (int64_t)blockIdx.x * kKeepThreads + tid; x < items; x += (int64_t)gridDim.x * kKeepThreads) {
+      const bool is_chunk = x < all;
+      int64_t y = is_chunk ? x / chunks : x - all;
+      const int c = is_chunk ? (int)(x - y * chunks) : 0;
+      const int h = (int)(y % v.n_kv_heads);
+      y /= v.n_kv_heads;
+      const int kv = (int)(y & 1);
+      const int64_t layer = y >> 1;
+      if (is_chunk)
+        move_rows<uint4, &Step::from, &Step::to>((kv ? v.v : v.k) + layer * v.layer_stride + h * v.head_stride + c * 16, step, n);
+      else
+        move_rows<uint8_t, &Step::scale_from, &Step::scale_to>(
+            reinterpret_cast<char*>(v.scales) + layer * v.scale_layer() + kv * v.scale_part() + ((int64_t)h << v.page_shift),
+            step, n);
     }
+    __syncthreads();
   }
 }
 
@@ -186,8 +179,10 @@ cudaError_t launch_tree_masks(const TreeParams& p, cudaStream_t s) {
 cudaError_t launch_keep(const KeepParams& p, cudaStream_t s) {
   const int64_t rows = (int64_t)2 * p.pool.n_layers * p.pool.n_kv_heads;
   const int64_t items = rows * (p.pool.row_bytes >> 4) + (p.pool.scales != nullptr ? rows : 0);
-  const int64_t blocks = (items + kKeepThreads - 1) / kKeepThreads;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  // Two waves of four blocks an SM at most, since a block begins with a chain of five loads: 23.7 us, one
+  // wave 25.1, a thread for each piece of a row 28.1; bfloat16 rows 43.6, 47.8 and 49.1.
+  const int64_t most = (items + kKeepThreads - 1) / kKeepThreads, waves = (8 * kMaxAttnCtas + p.B - 1) / p.B;
+  const int64_t blocks = most < waves ? most : waves;
   return launch_early(keep_kernel, dim3((unsigned)blocks, p.B), dim3(kKeepThreads), 0, s, p);
 }
 
