@@ -552,6 +552,31 @@ def test_tree_attention_same_bits_twice_in_a_graph_and_on_another_stream(kv, dty
         assert torch.equal(b.out, out) and torch.equal(b.lse, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_attention_of_trees_that_fill_most_of_a_row_tile(kv, dtype, D):
+    """Two row tiles a unit, of which some requests have one."""
+    Batch(dtype, D, 16, 2, 4, [(60, 400), (20, 700), (14, 14), (9, 130)], seed=D, trees=[_mixed] * 4).verify(kv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+def test_two_calls_at_once(kv, dtype):
+    """Calls with workspaces of their own on two streams, interleaved."""
+    a = Batch(dtype, 128, 16, 8, 4, [(1, 900), (3, 2000)], seed=4, trees=[_mixed] * 2)
+    b = Batch(dtype, 128, 16, 8, 4, [(40, 900), (13, 1500)], seed=5, trees=[_mixed] * 2)
+    a.call(kv), b.call(kv)   # (workspaces)
+    torch.cuda.synchronize()
+    a.out.fill_(7), b.out.fill_(7)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s in zip((a, b), streams):
+            assert x.call(kv, stream=s.cuda_stream) == 0
+    torch.cuda.synchronize()
+    a.compare()
+    b.compare()
+
+
 # ---- masks ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("window", [0, 1, 3])
@@ -651,6 +676,39 @@ def test_keep_against_the_plain_form(kv, dtype, D, S, Hk, L, layout):
     assert int(st[0]) == BOUNDS        # requests 7 (longer than its length), 8 (not ascending), 9 (past its rows)
     assert new_len.tolist() == lengths
     for x, y in zip([_bytes(k), _bytes(v)] + ([scales] if scales is not None else []), want):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,D", [("e4m3", 128), ("bf16", 64)])
+def test_keep_of_many_requests(kv, dtype, D):
+    """More requests than blocks of two waves: a block takes several pieces of its request's rows."""
+    B, n, S, Hk, L = 700, 6, 16, 8, 8
+    k, v, scales = _empty_pool(dtype, L, B, S, Hk, D, "nhd")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pool = [_bytes(k), _bytes(v)] + ([scales] if scales is not None else [])
+    for x in pool:
+        x.copy_(torch.randint(0, 127, x.shape, device="cuda", generator=g).to(x.dtype))
+    rng = np.random.RandomState(3)
+    kv_len, page = rng.randint(n, S + 1, B), rng.permutation(B)
+    path = np.full((B, 4), -1, dtype=np.int32)
+    want = [x.clone() for x in pool]
+    for b in range(B):
+        path[b, :b % 5] = np.sort(rng.permutation(n)[:b % 5])
+    for i in range(4):
+        b = np.nonzero(path[:, i] >= 0)[0]
+        to, src = kv_len[b] - n + i, kv_len[b] - n + path[b, i]
+        for x, y in zip(want[:2], pool[:2]):
+            x[:, page[b], to] = y[:, page[b], src]
+        if scales is not None:
+            # (the layers and K, V come behind the indexes)
+            w, t = want[2].permute(1, 4, 0, 2, 3), scales.permute(1, 4, 0, 2, 3)
+            w[page[b], to] = t[page[b], src]
+    st, new_len = _status(), torch.zeros(B, dtype=torch.int32, device="cuda")
+    kv.check(kv.ds_cache_keep(kv.KvPool(k, v, scales), _i32(path), _i32(np.arange(B + 1) * n), _i32(page[:, None]), _i32(kv_len),
+                              new_len, st))
+    assert int(st[0]) == 0
+    assert np.array_equal(new_len.cpu().numpy(), kv_len - n + (path >= 0).sum(1))
+    for x, y in zip(pool, want):
         assert torch.equal(x, y)
 
 
