@@ -339,19 +339,48 @@ struct Floats {
   }
 };
 
-template <class F, int D, typename T, int kRowsB>
+// The share whose cut unit is the n-th, -1 if there are not as many. By the whole block.
+template <int kShares>
+__device__ __forceinline__ int nth_cut(const CutUnit* cut, int n) {
+  constexpr int kWords = (kShares + 31) / 32;
+  __shared__ uint32_t valid[kWords];
+  for (int k0 = 0; k0 < kShares; k0 += kJoinThreads) {
+    const int k = k0 + threadIdx.x;
+    const uint32_t word = __ballot_sync(0xffffffffu, k < kShares && __ldcg(&cut[k].valid) != 0);
+    if ((threadIdx.x & 31) == 0 && k < kShares) valid[k >> 5] = word;
+  }
+  __syncthreads();
+  int at = -1;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const uint32_t word = valid[i];
+    if (at < 0 && n < __popc(word)) {
+      at = 32 * i;
+      bits = word;
+    }
+    if (at < 0) n -= __popc(word);
+  }
+  if (at < 0) return -1;
+  for (; n > 0; --n) bits &= bits - 1;
+  return at + __ffs(bits) - 1;
+}
+
+// kByUnit: a block a unit, else a share.
+template <class F, int D, typename T, int kRowsB, bool kByUnit = false>
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnParams p, int tile, int used) {
   constexpr int kWarps = kJoinThreads / 32, N = D / 32, kRounds = (F::kShares + 31) / 32;
   static_assert((N == 2 || N == 4) && kRowsB <= kWarps && kAlone <= 32, "a warp a row, a lane a part");
   __shared__ float factor[F::kShares][kRowsB];  // of a part in a row's sums, -1: no part
   __shared__ __align__(16) float sums[kWarps][kRowsB][D];
   const Partials part = partials<D>(p.workspace);
-  const int share = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int prow0 = blockIdx.y * kRowsB, prow = prow0 + warp;  // (warp < kRowsB: its row)
   const int in_tile = prow % tile, row = prow / tile * used + in_tile;
-  auto at = [&](int k, int r) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + r; };
   sm100::pdl_wait();
+  const int share = kByUnit ? nth_cut<F::kShares>(part.cut, blockIdx.x) : blockIdx.x;
+  if (kByUnit && share < 0) return;
+  auto at = [&](int k, int r) { return (size_t)(k * 2 + (k == share ? 1 : 0)) * F::kPartRows + r; };
   // The record, and, before it has arrived, the row's statistics in this share and
   // the ones after it (looked at only if the record says that they have parts): with
   // few rows the next 31, with many, which have few parts as a rule, the next 3,
@@ -505,13 +534,24 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const AttnPa
 // Launch of the join for units of at most `rows` rows of a slot. With few rows two a
 // block, so that the parts in flight are more: 10 rows of float32 12.7 us, with eight
 // a block 15.9; with many rows blocks of two are too many.
+//
+// Blocks of shares without a cut unit end at once, but many of them come in waves (each waits for
+// its record). With few units of many rows a block a unit, which looks for its share first: 1 tree of
+// 25 nodes (8 units of 100 rows) 18.0 us, so 16.8, of 60 nodes 18.3 and 16.3; of 12 nodes, or 8 trees, as
+// fast either way, and up to 16 rows 12.4 and 13.4.
 template <class F, int D, typename T, int kFew = 2>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s, int rows, int tile, int used) {
   if (rows <= 16)
-    return launch_early(attn_join_kernel<F, D, T, kFew>, dim3(F::kShares, (rows + kFew - 1) / kFew), dim3(kJoinThreads), 0, s,
-                        p, tile, used);
-  return launch_early(attn_join_kernel<F, D, T, 8>, dim3(F::kShares, (rows + 7) / 8), dim3(kJoinThreads), 0, s, p, tile,
-                      used);
+    return launch_early(attn_join_kernel<F, D, T, kFew>, dim3(F::kShares, (rows + kFew - 1) / kFew), dim3(kJoinThreads), 0, s, p,
+                        tile, used);
+  const unsigned y = (rows + 7) / 8;
+  if constexpr (F::kPartRows > 64) {
+    const int64_t unit_rows = (int64_t)used * (F::kPartRows / tile);
+    const int64_t units = ((int64_t)p.max_q * p.group + unit_rows - 1) / unit_rows * p.B * p.pool.n_kv_heads;
+    if (rows > 64 && 4 * units <= F::kShares)
+      return launch_early(attn_join_kernel<F, D, T, 8, true>, dim3((unsigned)units, y), dim3(kJoinThreads), 0, s, p, tile, used);
+  }
+  return launch_early(attn_join_kernel<F, D, T, 8>, dim3(F::kShares, y), dim3(kJoinThreads), 0, s, p, tile, used);
 }
 
 }  // namespace
