@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // precision, and let the attention restore a row exactly in bfloat16.
 //
 // 2 T Hk D (2 + 1) bytes are moved: bound by memory (16 prompts of 8 heads of 128 values, 347 MB,
-// 60 us: 5.8 TB/s), of few rows by the launch (64: 3.5 us of their own). A lane takes 16 values
+// 56 us: 6.2 TB/s; with the loop over lanes not unrolled, 60), of few rows by the launch (64: 3.5 us of
+// their own). A lane takes 16 values
 // of K and of V, the power of two of lanes that D / 16 asks for a row's maximum.
 constexpr int kLowestScale = 27, kNoScale = 255;  // bytes: e = -100; a row that is not finite
 
@@ -182,8 +183,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_e4m3_kernel(const Appen
       }
     }
     uint32_t top = top_of(k[0], k[1]) | top_of(v[0], v[1]) << 16;
-#pragma unroll 1
-    for (int d = 1; d < lanes; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1)
+      if (d < lanes) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
     if (!here) continue;
     const int sk = scale_of(top & 0xffffu), sv = scale_of(top >> 16);
     const int64_t o = (int64_t)place.x * p.pool.page_stride + (int64_t)place.y * p.pool.token_stride + h * p.pool.head_stride;
@@ -266,8 +268,8 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   // Eight rows of 1 KB and more keep a block's threads busy, of smaller rows it takes
   // more: 16 prompts (56 k rows) of 128 bytes 6.2 us by 32 rows a block, 12.3 by 8;
   // of 512 bytes 22.0 and 23.1; of 1 KB 39.3 and 38.4; of 2 KB 74.4 and 71.8. Codes, whose
-  // pieces take two loads and a conversion, of 128 bytes 10.9 by 32, 21.2 by 8; of 512
-  // 31.9 and 36.6; of 1 KB 59.4 and 60.4, and 64 rows of them 8.4 and 6.7; of 2 KB 116 and 109.
+  // pieces take two loads and a conversion, of 128 bytes 9.8 by 32, 18.0 by 8; of 512 29.4 and
+  // 33.1; of 1 KB 56.8 and 56.0, and 64 rows of them 7.7 and 7.1; of 2 KB 115 and 105.
   const int tokens = pieces >= 64 ? 8 : 32;
   const dim3 blocks((p.T + tokens - 1) / tokens);
   if (p.pool.scales != nullptr)
