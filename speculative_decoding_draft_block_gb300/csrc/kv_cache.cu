@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 //
 // 2 T Hk D (2 + 1) bytes are moved: bound by memory (16 prompts of 8 heads of 128 values, 347 MB,
 // 56 us: 6.2 TB/s; with the loop over lanes not unrolled, 60), of few rows by the launch (64: 3.5 us of
-// their own). A lane takes 16 values
-// of K and of V, the power of two of lanes that D / 16 asks for a row's maximum.
+// their own). A lane takes 16 values of K and of V, the power of two of lanes that D / 16 asks
+// for a row's maximum.
 constexpr int kLowestScale = 27, kNoScale = 255;  // bytes: e = -100; a row that is not finite
 
 // The scale byte of a row whose largest |x| has these bits.
