@@ -73,7 +73,7 @@ struct Shared {
   Piece piece[kAhead];
   uint64_t piece_full[kAhead], piece_empty[kAhead];
   uint64_t full[Stage<D>::kCount], empty[Stage<D>::kCount], met[KH];
-  float2 stat[2][kWarps][8 * NT];  // references and sums of a piece, and of the one before
+  float2 stat[2][kWarps][8 * NT];  // references and sums of a piece with tiles, and of the last one before it that had some
   int abort;
   ShareStart<32 * (kWarps + 2), 1> work;
   alignas(16) uint8_t scale[Stage<D>::kCount][2][kTile];
@@ -617,7 +617,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
         if (n_tiles > 0) {
           // The outputs on the warp's own reference, four rows of each eight in the places of its
           // keys and four in those of its values (16-byte pieces so that accesses do not collide).
-          float2(&stat)[kWarps][8 * NT] = sh.stat[np & 1];
+          // (By meetings, not by pieces: those that see nothing have none, and only the meeting in between
+          // orders the writes to a buffer behind what a slower warp still reads there.)
+          float2(&stat)[kWarps][8 * NT] = sh.stat[met & 1];
           constexpr int kChunks = D / 4;
           auto place = [&](int w, int n, int row) {
             return reinterpret_cast<float4*>(ring + stage * St::kBytes + (row >> 2) * St::kCodes +

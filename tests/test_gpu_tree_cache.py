@@ -310,6 +310,20 @@ def test_quantised_attention_of_few_rows_and_many_heads(kv, D, Hk, G, n_q, S, la
     Batch("e4m3", D, S, Hk, G, [(n_q, n) for n in (5, 31, 33, 64, 255, 700)] + [(0, 9), (1, 0)], layout=layout, seed=D + Hk).verify(kv)
 
 
+@pytest.mark.parametrize("D,Hk,G,n_q", [(128, 1, 4, 2), (128, 2, 4, 1), (64, 4, 1, 1), (64, 2, 3, 4), (64, 1, 2, 1)])
+def test_quantised_attention_of_requests_that_see_nothing_between_others(kv, D, Hk, G, n_q):
+    """Shares of several units, some of which have no keys and so no meeting of their warps; the same bits every time.
+    (More requests than threads, too: their shares are found in two passes.)"""
+    lens = [(n_q, 0 if i % 3 == 1 else n_q + (7 * i) % 50) for i in range(1000)]
+    b = Batch("e4m3", D, 16, Hk, G, lens, seed=D + Hk)
+    b.verify(kv)
+    out, lse = b.out.clone(), b.lse.clone()
+    for _ in range(10):
+        b.out.fill_(5)
+        assert b.call(kv) == 0
+        assert torch.equal(b.out, out) and torch.equal(b.lse, lse)
+
+
 @pytest.mark.parametrize("G,n_q", [(2, 1), (4, 4), (4, 30), (8, 40)])
 def test_quantised_attention_of_large_keys_and_values(kv, G, n_q):
     """Keys of 2^110 and values of 2^100 (scores far past any exponent: one key has all the weight); nothing overflows."""
