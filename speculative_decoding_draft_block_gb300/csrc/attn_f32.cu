@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
       // A value that is not finite, of a key that other rows of the unit see and this
       // one does not, has come in with its weight of zero: the row's sums again, from
-      // what it sees (each thread its columns).
+      // what it sees (each thread its columns; of a tree's new tokens the window hides none).
       float probe = 0.f;
 #pragma unroll
       for (int k = 0; k < kC; ++k)
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
         for (int k = 0; k < kC; ++k) o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float ref = m[i] == kNegInf ? 0.f : m[i];
 #pragma unroll 1
-        for (int key = max(key0, lo[i]); key < min(key1, kTree ? x.kv : hi[i]); ++key) {
+        for (int key = max(key0, kTree ? min(lo[i], x.ctx) : lo[i]); key < min(key1, kTree ? x.kv : hi[i]); ++key) {
           if (kTree && !sees(i, key)) continue;
           const int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) break;  // (reported above)
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_f32_few_kernel(const AttnPar
         y = make_float4(0.f, 0.f, 0.f, 0.f);
         const float ref = st.x == kNegInf ? 0.f : st.x;
 #pragma unroll 1
-        for (int key = max(key0, sh.lo[row]); key < min(key1, kTree ? x.kv : sh.hi[row]); ++key) {
+        for (int key = max(key0, kTree ? min(sh.lo[row], x.ctx) : sh.lo[row]); key < min(key1, kTree ? x.kv : sh.hi[row]); ++key) {
           if (kTree && !sees(row, key)) continue;
           const int page = __ldcg(table + (key >> shift));
           if (page < 0 || page >= p.pool.n_pages) break;

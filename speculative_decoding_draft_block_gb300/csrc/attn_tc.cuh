@@ -1029,6 +1029,8 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
       // (-1: unseen), and hands it to all. A piece may be as long as the cache, so
       // the other roles' waits do not count meanwhile.
       // 58 to 217 rows x keys a us and SM: 210 rows over 100,000 keys (D = 64) 95 ms.
+      // (A tree's keys begin at its window's beginning or, if that lies behind it, at the context's end: the
+      // window hides none of the new tokens.)
       auto anew = [&](uint32_t again, int t_row, int h_row, char* dst, int a, int z, float r_ref, float r_f) {
         constexpr int N = D / 32, kR = 4, kK = 8;  // columns, rows, keys
         static_assert(kR * kK == 32, "a lane a row and key");
@@ -1234,7 +1236,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           const uint32_t bad = __ballot_sync(0xffffffffu, there && probe != probe && r_l == r_l);
           if (bad != 0) {
             const int r_pos = x.pos + tok, z = p.causal && !kTree ? min(r_pos + 1, x.kv) : x.kv;
-            const int a = kTree ? (there ? tree_low(p, x.ctx, r_t) : 0) : p.window > 0 ? max(0, r_pos - p.window + 1) : 0;
+            const int a = kTree ? (there ? min(tree_low(p, x.ctx, r_t), x.ctx) : 0) : p.window > 0 ? max(0, r_pos - p.window + 1) : 0;
             // (a bit a row: its first lane's)
             const uint32_t again = kChunks == 32 ? 1u : ((bad & 0xffffu) != 0 ? 1u : 0u) | (bad >> 16 != 0 ? 0x10000u : 0u);
             anew(again, (int)r_t, r_head, dst, max(key0, a), min(key1, z), r_ref, r_f);
@@ -1296,7 +1298,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         const float2 probes = unpack2(probe2);
         const float probe = probes.x + probes.y;
         const uint32_t again = __ballot_sync(0xffffffffu, valid && probe != probe && l == l && (lo > key0 || hi < key1));
-        if (again != 0) anew(again, (int)t_out, head, to, max(key0, lo), min(key1, kTree ? x.kv : hi), ref, f);
+        if (again != 0) anew(again, (int)t_out, head, to, max(key0, kTree ? min(lo, x.ctx) : lo), min(key1, kTree ? x.kv : hi), ref, f);
         if (valid) {
           if (!x.whole)
             part.stat[prow] = make_float2(ref, l);

@@ -292,7 +292,7 @@ __device__ __forceinline__ uint32_t tree_seen(const uint32_t* words, int n_words
   return seen;
 }
 
-// The same for one key of [lo, kv).
+// The same for one key of the context from lo on, or of the new tokens [ctx, kv).
 __device__ __forceinline__ bool tree_sees(const uint32_t* words, int key, int ctx) {
   return key < ctx || (__ldcg(words + ((key - ctx) >> 5)) >> ((key - ctx) & 31) & 1u) != 0;
 }

@@ -532,6 +532,46 @@ def test_tree_attention_of_nan_in_other_branches(kv, dtype, D, G, n, window):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("D,G,n", [(128, 1, 4), (64, 1, 8), (64, 2, 8), (128, 2, 12), (64, 4, 30), (128, 4, 70)])
+@pytest.mark.parametrize("past", [0, 40, 300])
+def test_tree_attention_of_nan_beside_depths_past_the_window(kv, dtype, D, G, n, past):
+    """Hand-made depths that put the window's beginning behind new tokens: these are seen by the masks alone, also where a
+    value that is not finite stands beside them, of a token that only the last row sees."""
+    def masks(rng, m):
+        a = np.tril(rng.rand(m, m) < 0.5)
+        a[:, 1] = np.arange(m) == m - 1
+        a[np.arange(2, m), np.arange(2, m)] = True
+        return a
+    window = 5
+    kw = dict(window=window, seed=n + past, trees=[_mixed], masks=masks)
+    b = Batch(dtype, D, 16, 1, G, [(n, n + past)], **kw)
+    # rows with the window's beginning in the context, among the new tokens, behind them
+    b.depth = _i32([i % 3 * (window + i) if i % 4 else 10000 for i in range(n)])
+    depth = b.depth.cpu().numpy().astype(np.int64)
+    mask = b.seen[0][:, past:]
+    b.seen = [ref.tree_seen(mask, depth, n, n + past, window)]
+    page, place = int(b.table[0, (past + 1) // 16]), (past + 1) % 16
+    if dtype == "e4m3":
+        was = b.scales[0, page, :, 0, place].clone()
+        b.scales[0, page, :, 0, place] = 255
+    else:
+        was = b.k[0, page, place].clone(), b.v[0, page, place].clone()
+        b.k[0, page, place] = float("inf")
+        b.v[0, page, place] = float("nan")
+    assert b.call(kv) == 0
+    assert torch.isnan(b.out[-1].float()).all()
+    out, lse = b.out.clone(), b.lse.clone()
+    if dtype == "e4m3":
+        b.scales[0, page, :, 0, place] = was
+    else:
+        b.k[0, page, place], b.v[0, page, place] = was
+    assert b.call(kv) == 0
+    b.compare()
+    b.out[:-1], b.lse[:-1] = out[:-1], lse[:-1]
+    b.compare()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "e4m3"])
 def test_a_chain_is_causal_attention(kv, dtype):
     lens = [(1, 40), (16, 200), (40, 41), (7, 700)]
     a = Batch(dtype, 128, 16, 2, 4, lens, seed=9, trees=[_chain] * 4)
