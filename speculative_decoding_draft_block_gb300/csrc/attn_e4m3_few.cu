@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
     const int32_t* table = nullptr;
     int n = 0, tile0 = 0, lo = 0, hi = 0, head = 0, page = kNoPage, j = 0;
     uint32_t np = 0;
-    // Table entry of this lane's page of a tile, kNoPage: no row sees it.
+    // Table entry of this lane's page of a tile (any below 0 as -1), kNoPage: no row sees it.
     auto page_of = [&](int tile) {
       const int key = tile * kKeys + lane * rows;
       if (lane >= boxes || key >= hi || key + rows <= lo) return kNoPage;
-      return __ldcg(table + (key >> shift));
+      return max(__ldcg(table + (key >> shift)), -1);
     };
     // the next piece with tiles (n < 0: there is none), and its first page
     auto next_piece = [&] {

@@ -430,12 +430,12 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
       int j = 0;                                           // next tile of the piece
       const int32_t* table = nullptr;
       // Table entry of this lane's box of a key tile, kNoPage: no row of the unit sees
-      // it. (Looked at when the tile is loaded, a tile later as a rule.)
+      // it, -1 any that is below 0. (Looked at when the tile is loaded, a tile later as a rule.)
       constexpr int kNoPage = INT32_MIN;
       auto page_of = [&](int tile) {
         const int key = tile * kTile + lane * rows;
         if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return kNoPage;
-        return __ldcg(table + (key >> shift));
+        return max(__ldcg(table + (key >> shift)), -1);
       };
       int page = kNoPage;                                  // of the next tile
       volatile int* ends = sh.ended;

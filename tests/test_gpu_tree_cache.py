@@ -631,6 +631,38 @@ def test_two_calls_at_once(kv, dtype):
     b.compare()
 
 
+# ---- malformed device data, strides, many requests ----------------------------------------------
+
+@pytest.mark.parametrize("dtype,tree", [("e4m3", False), ("e4m3", True), ("bf16", True), ("f32", True), ("bf16", False), ("f32", False)])
+@pytest.mark.parametrize("n", [4, 40])
+def test_attention_reports_what_is_out_of_bounds(kv, dtype, tree, n):
+    """The status says so, nothing faults, the other requests' rows stand."""
+    def fresh():
+        return Batch(dtype, 64, 16, 2, 2, [(2, 100), (n, n + 50), (1, 70)], seed=11, trees=[_mixed] * 3 if tree else None)
+
+    good = fresh()
+    good.verify(kv)
+    for what in (good.k.shape[1], -1, 2**31 - 1, -2**31, "kv_len", "negative kv_len", "q_start", "max_q", "q_end"):
+        x = fresh()
+        if what == "kv_len":
+            x.kv_len[1] = x.table.shape[1] * 16 + 1
+        elif what == "negative kv_len":
+            x.kv_len[1] = -5
+        elif what == "q_start":
+            x.q_start[2] = 1
+        elif what == "max_q":
+            x.max_q = n - 1
+        elif what == "q_end":
+            x.q_start[3] = 1000
+        else:
+            x.table[1, 2] = what
+        assert x.call(kv) == 0
+        assert int(x.status[0]) == BOUNDS, what
+        # (the work is cut by the whole batch's, so the sums' order may be another: each within the bound of the exact ones)
+        good.out[:2], good.lse[:2] = x.out[:2], x.lse[:2]
+        good.compare()
+
+
 # ---- masks ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("window", [0, 1, 3])
