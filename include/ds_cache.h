@@ -218,10 +218,12 @@ ds_status ds_cache_compact(const ds_compact_args* args, ds_stream_t stream);
  *   ds_cache_append_scaled   a row gets the smallest 2^e, e >= -100, with
  *       max |x| <= 448 * 2^e, and its values x / 2^e rounded to the nearest (ties to
  *       even): off by at most 2^-4 |x| or 2^(e - 10), whichever is more. A row with a
- *       value that is not finite gets scale 255 and zeros for codes.
+ *       value that is not finite gets scale 255 and zeros for codes. (Scales are 27 to 247. With 247,
+ *       a row whose largest |x| is above 1.75 * 2^127, values from 248 * 2^120 on get the code of
+ *       256, which stands for 2^128: past bfloat16 and float32, and infinite where it is restored.)
  *   ds_paged_attention_tree  reads code * 2^(scale - 127). With more than 16 rows a KV head
- *       these are rounded to bfloat16, which holds them exactly for scales from 27 (what
- *       append writes) to 246, and to its smallest subnormal below that; all else is as
+ *       these are rounded to bfloat16, which holds them exactly for scales from 27 (the least that
+ *       append writes) to 246 (with 247 all but 2^128, see above), and to its smallest subnormal below 27; all else is as
  *       for bfloat16 pools. With up to 16 rows the products take codes as they are and q
  *       as float16 relative to its row's largest value (bfloat16's 8 bits down to 2^-31 of
  *       that, multiples of 2^-39 of it below), and weights are rounded to float16 (11 bits;

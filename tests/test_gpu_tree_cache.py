@@ -242,6 +242,29 @@ def test_append_quantises_values_at_the_borders(kv):
     assert (np.abs(got - want) <= np.maximum(np.abs(want) * 2.0 ** -4, np.ldexp(1.0, e[fine] - 10)[..., None])).all()
 
 
+def test_append_quantises_the_last_binade(kv):
+    """Above 1.75 * 2^127 the scale is 247. Up to 247 * 2^120 a finite row restores to finite bfloat16 values; from 248 * 2^120 on
+    (half a step below 256) the nearest code stands for 2^128, which bfloat16 does not hold."""
+    D, tops = 64, [224, 225, 232, 239, 240, 247, 248, 255]
+    x = torch.zeros((2 * len(tops), 1, D), dtype=torch.float64)
+    for i, top in enumerate(tops + [-t for t in tops]):
+        x[i, 0, :4] = torch.tensor([top, 1.0, -top / 2, 3.0], dtype=torch.float64) * 2.0 ** 120
+    new = x.to("cuda").to(torch.bfloat16)
+    assert torch.equal(new.cpu().double(), x)
+    n = len(new)
+    pool, before, places = _append_case(kv, D, 16, 1, "nhd", new, new, [(n, n)])
+    _check_append(pool, before, places, new, new)
+    k, _, scales = pool
+    at = [torch.as_tensor([p[i] for p in places], device="cuda") for i in range(2)]
+    byte = scales[1, at[0], 0, 0, at[1]].int()
+    assert byte.tolist() == [246] + [247] * 7 + [246] + [247] * 7
+    got = (k[1, at[0], at[1], 0].double() * torch.exp2(byte.double() - 127)[:, None]).to(torch.bfloat16)
+    finite = torch.isfinite(got.float()).all(1).tolist()
+    assert finite == [t <= 247 for t in tops] * 2
+    off = (got.double() - new[:, 0].double()).abs().cpu()[torch.tensor(finite)]
+    assert (off <= (2.0 ** -4 * x[:, 0].abs())[torch.tensor(finite)]).all()
+
+
 def test_append_quantises_strided_rows(kv):
     """Keys and values as slices of one wide projection."""
     D, Hk, n = 64, 2, 50
