@@ -434,6 +434,44 @@ def test_quantised_attention_of_scales_at_the_borders(kv, scale_byte):
     assert (np.abs(got - want) <= 4 * 2.0 ** -8 * np.abs(want) + 2.0 ** -133).all()
 
 
+@pytest.mark.parametrize("D,G,n_q", [(64, 4, 8), (128, 4, 8), (64, 4, 40), (128, 4, 40), (128, 24, 1)])
+@pytest.mark.parametrize("scale_byte", [3, 26, 27, 134, 135, 140, 246])
+def test_quantised_attention_of_scales_at_the_borders_with_many_rows(kv, D, G, n_q, scale_byte):
+    """As above with more than 16 rows a KV head, whose tiles are restored as bfloat16 in one product or two. Keys of zero: out is
+    the mean of what a row sees, with weights of exactly 1, so its error is the sums' (each of n terms 2^-24 of the values' mean
+    size, and the factor 1 / l twice that) and bfloat16's 2^-8 once; 2^-133 is the smallest bfloat16."""
+    n = 50
+    b = Batch("e4m3", D, 16, 1, G, [(n_q, n)], seed=1)
+    # sums below float32's range: 50 values of up to 3.75 * 2^119 with the largest scale
+    codes = torch.randint(0, 72 if scale_byte == 246 else 127, (1, b.k.shape[1], 16, 1, D), device="cuda", dtype=torch.uint8)
+    codes += 128 * torch.randint(0, 2, codes.shape, device="cuda", dtype=torch.uint8)
+    b.v = codes.view(torch.float8_e4m3fn)
+    b.k = torch.zeros_like(codes).view(torch.float8_e4m3fn)
+    b.scales[:, :, 0] = 127
+    b.scales[:, :, 1] = scale_byte
+    assert b.call(kv) == 0 and int(b.status[0]) == 0
+    v = (b.v[0].double()[b.table[0].long()].reshape(-1, D)[:n] * 2.0 ** (scale_byte - 127)).cpu().numpy()
+    got = b.out.double().cpu().numpy()
+    for t in range(n_q):
+        m = n - n_q + t + 1
+        want, size = v[:m].mean(0), np.abs(v[:m]).mean(0)
+        assert (np.abs(got[t] - want) <= 2.0 ** -8 * np.abs(want) + (m + 2) * 2.0 ** -24 * size * (1 + 2.0 ** -8) + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("D,G,n_q", [(128, 2, 1), (64, 2, 1), (128, 4, 4), (128, 4, 30), (64, 4, 30), (128, 8, 40)])
+@pytest.mark.parametrize("far", [100, -60])
+def test_quantised_attention_of_large_and_small_rows_with_ordinary_scores(kv, D, G, n_q, far):
+    """Keys times 2^far, queries and values times 2^-far: the scores, and so all weights, are those of ordinary rows."""
+    b = Batch("e4m3", D, 16, 2, G, [(n_q, 300), (1, 90)], seed=G)
+    rows = b.scales != 255
+    keys = rows.clone()
+    keys[:, :, 1] = False
+    b.scales[keys] += far % 256
+    b.scales[rows & ~keys] -= far % 256
+    b.q *= 2.0 ** -far
+    b.verify(kv)
+
+
 @pytest.mark.parametrize("D,G,n_q", [(128, 1, 4), (64, 4, 2), (128, 24, 1), (128, 4, 70), (64, 2, 90)])
 @pytest.mark.parametrize("window", [0, 30])
 def test_quantised_attention_of_rows_that_some_do_not_see(kv, D, G, n_q, window):
@@ -684,6 +722,139 @@ def test_attention_reports_what_is_out_of_bounds(kv, dtype, tree, n):
         # (the work is cut by the whole batch's, so the sums' order may be another: each within the bound of the exact ones)
         good.out[:2], good.lse[:2] = x.out[:2], x.lse[:2]
         good.compare()
+
+
+@pytest.mark.parametrize("dtype,tree", [("e4m3", False), ("e4m3", True), ("bf16", True), ("f32", True)])
+@pytest.mark.parametrize("D,G,n", [(128, 4, 3), (64, 2, 5), (128, 4, 40), (64, 4, 70)])
+def test_attention_of_strided_rows(kv, dtype, tree, D, G, n):
+    """q as a slice of a joint projection, out as one of a wider tensor, beside which nothing is written."""
+    b = Batch(dtype, D, 16, 2, G, [(n, 90), (1, 300), (n + 1, n + 2)], seed=n, trees=[_mixed] * 3 if tree else None)
+    T, H, _ = b.q.shape
+    q = torch.full((T, H + 4, 2 * D), float("nan"), dtype=b.q.dtype, device="cuda")
+    q[:, 1:H + 1, :D] = b.q
+    out = torch.zeros((T, H + 1, 2 * D), dtype=b.q.dtype, device="cuda")
+    b.q, b.out = q[:, 1:H + 1, :D], out[:, :H, D:]
+    b.verify(kv, scale=0.07)
+    assert (out[:, -1] == 0).all() and (out[:, :, :D] == 0).all()
+
+
+def _joint(kind, L, N, S, Hk, D, dtype):
+    """K and V as views of one tensor, and a tensor of truth values: what of it is theirs."""
+    dt = torch.uint8 if dtype == "e4m3" else DT[dtype]
+    if kind == "token":          # K and V of a token side by side
+        shape, cut = (L, N, S, 2, Hk, D), lambda x: (x[:, :, :, 0], x[:, :, :, 1])
+    elif kind == "head":         # of a head, with a gap behind them
+        shape, cut = (L, N, S, Hk, 2 * D + 16), lambda x: (x[..., :D], x[..., D:2 * D])
+    else:                        # layers inside pages, heads outside a page's tokens, more heads than are used
+        shape, cut = (N, 2, L, Hk + 1, S, D), lambda x: tuple(x[:, i, :, :Hk].permute(1, 0, 3, 2, 4) for i in range(2))
+    buf, mine = torch.full(shape, 7, dtype=dt, device="cuda"), torch.zeros(shape, dtype=torch.bool, device="cuda")
+    for x in cut(mine):
+        x.fill_(True)
+    views = cut(buf)
+    return buf, mine, [x.view(DT[dtype]) for x in views] if dtype == "e4m3" else list(views)
+
+
+@pytest.mark.parametrize("dtype,kind", [("e4m3", "token"), ("e4m3", "head"), ("e4m3", "layers"), ("bf16", "head"), ("f32", "layers")])
+@pytest.mark.parametrize("S,Hk,D,G,n", [(16, 2, 128, 4, 3), (64, 3, 64, 1, 2), (128, 1, 128, 5, 40), (16, 4, 64, 2, 60)])
+def test_trees_and_paths_over_interleaved_pools(kv, dtype, kind, S, Hk, D, G, n):
+    """K and V in one tensor with strides that are not dense: the same bits as over dense pools from append, attention with and
+    without masks, keep, copy on write and compaction; what lies between the rows stays as it was."""
+    L, B, N, M = 2, 3, 40, 8
+    g = torch.Generator(device="cuda").manual_seed(S + D + n)
+    rng = np.random.RandomState(n)
+    rows_dt = torch.bfloat16 if dtype == "e4m3" else DT[dtype]
+    buf, mine, joint = _joint(kind, L, N, S, Hk, D, dtype)
+
+    def scales():
+        return torch.full((L, N, 2, Hk, S), 255, dtype=torch.uint8, device="cuda") if dtype == "e4m3" else None
+
+    pools = [kv.KvPool(*joint, scales()), kv.KvPool(*(torch.full_like(x, 7).contiguous() for x in joint), scales())]
+    for x in pools[1].k, pools[1].v:
+        _bytes(x).fill_(7)
+    ws = torch.empty(max(kv.ds_cache_update_workspace_bytes(B, N), kv.ds_cache_compact_workspace_bytes(N),
+                         kv.ds_paged_attention_workspace_bytes(pools[0], G * Hk)), dtype=torch.uint8, device="cuda")
+    status = _status()
+    held = torch.zeros(N, dtype=torch.int32, device="cuda")
+    held[::3] = 1                                       # somebody else's, so that pages lie apart
+    states = [[_i32(np.full((B, M), -1)), _i32([0] * B), held.clone()] for _ in pools]
+
+    def both(call):
+        """The call over each pool with its own state; the results have to be equal."""
+        x, y = (call(pool, state) for pool, state in zip(pools, states))
+        assert all(torch.equal(a, z) for a, z in zip(x, y))
+        assert all(torch.equal(a, z) for a, z in zip(*states))
+        for a, z in ((pools[0].k, pools[1].k), (pools[0].v, pools[1].v)) + (((pools[0].scales, pools[1].scales),) if dtype == "e4m3" else ()):
+            assert torch.equal(_bytes(a), _bytes(z))
+        assert (buf[~mine] == 7).all() and int(status[0]) == 0
+        return x
+
+    def update(new, parent=None):
+        def call(pool, state):
+            out = [torch.empty_like(x) for x in state]
+            kv.check(kv.ds_cache_update(pool, *state, _i32(new), *out, ws, status, parent=None if parent is None else _i32(parent)))
+            state[:] = out
+            return []
+        both(call)
+
+    def rows(sizes, masked):
+        start = _i32(np.concatenate([[0], np.cumsum(sizes)]))
+        T = sum(sizes)
+        mask = depth = None
+        if masked:
+            pairs = [ref.ancestors(ref.random_tree(rng, m)) for m in sizes]
+            mask = torch.as_tensor(np.concatenate([ref.words(a, ceil_div(max(sizes), 32)) for a, _ in pairs]), device="cuda")
+            depth = _i32(np.concatenate([d for _, d in pairs]))
+        for layer in range(L):
+            k, v = (torch.randn((T, Hk, D), device="cuda", generator=g).to(rows_dt) for _ in range(2))
+            q = torch.randn((T, G * Hk, D), device="cuda", generator=g).to(rows_dt)
+
+            def call(pool, state):
+                out, lse = torch.empty_like(q), torch.empty((T, G * Hk), device="cuda")
+                kv.check(kv.ds_cache_append(pool, layer, k, v, start, state[0], state[1], status))
+                kv.check(kv.ds_paged_attention(pool, layer, q, start, max(sizes), state[0], state[1], out, ws, status, lse=lse, mask=mask,
+                                               depth=depth))
+                return out, lse
+            assert torch.isfinite(both(call)[0].float()).all()
+        return start
+
+    lens = [3 * S + 7, n, 5]
+    update(lens)
+    rows(lens, False)
+    update([lens[0], lens[0], 5], [0, 0, 2])             # request 1 becomes a copy of request 0
+    new = [4, n, 1]
+    update([lens[0] + 4, lens[0] + n, 6])                # both write into the shared last page
+    start = rows(new, True)
+    path = np.full((B, 3), -1)
+    path[0], path[1, :2], path[2, 0] = [0, 2, 3], [0, n - 1], 0
+
+    def keep(pool, state):
+        new_len = torch.empty(B, dtype=torch.int32, device="cuda")
+        kv.check(kv.ds_cache_keep(pool, _i32(path), start, state[0], state[1], new_len, status))
+        return [new_len]
+
+    new_len = both(keep)[0].tolist()
+    assert new_len == [lens[0] + 3, lens[0] + 2, 6]
+    update(new_len)
+
+    def compact(pool, state):
+        state[2] = state[2] - (torch.arange(N, device="cuda") % 3 == 0).int()
+        out, page_map, used = (torch.empty_like(state[0]), torch.empty_like(state[2])), torch.empty_like(state[2]), _i32([0])
+        kv.check(kv.ds_cache_compact(pool, state[0], state[2], *out, page_map, used, ws, status))
+        state[0], state[2] = out
+        return [used]
+
+    assert int(both(compact)[0]) == int((states[0][2] > 0).sum())
+    update([x + n for x in new_len])
+    rows([n] * B, True)
+
+
+@pytest.mark.parametrize("dtype,tree", [("e4m3", False), ("e4m3", True), ("bf16", True), ("f32", True)])
+@pytest.mark.parametrize("G,most", [(2, 5), (4, 12)])
+def test_attention_of_more_requests_than_threads(kv, dtype, tree, G, most):
+    """Shares are found in two passes over the requests."""
+    rng = np.random.RandomState(most)
+    lens = [(int(a), int(a + c)) for a, c in zip(rng.randint(0, most + 1, 700), rng.randint(0, 60, 700))]
+    Batch(dtype, 64, 16, 1, G, lens, seed=most, trees=[_mixed] * 700 if tree else None).verify(kv)
 
 
 # ---- masks ----------------------------------------------------------------------------------
