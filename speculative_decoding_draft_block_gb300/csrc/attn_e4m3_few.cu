@@ -92,7 +92,9 @@ constexpr uint32_t smem_bytes() {
 // (A piece's beginning and end cost a block as much as three tiles: 128 requests of 300 to 8000
 // cached 121.5 us, counted as one tile 138, as two 126, as four 121.5.)
 template <int NT, int KH>
-struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true, 3> {};
+struct FormFew : WorkForm<kTile / KH, kMaxShares, 8 * NT * KH, true, 3> {
+  static_assert(counts_in_32_bits(kMaxTableTokens, FormFew::kKeys, FormFew::kCost, kMaxKvHeads / KH), "work_fits");
+};
 
 // By all lanes of a warp; false once a wait has given up (after about a second, a minute
 // with more polls).

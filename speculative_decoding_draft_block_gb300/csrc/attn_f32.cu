@@ -23,7 +23,9 @@ constexpr int kThreads = 256;
 constexpr int kKeyTile = kAttnTileF32;
 
 template <int kBM, bool kTree>
-struct Form32 : WorkForm<kKeyTile, kMaxShares, kBM, kTree> {};
+struct Form32 : WorkForm<kKeyTile, kMaxShares, kBM, kTree> {
+  static_assert(Form32::kCost == kAttnUnitCost, "work_fits");
+};
 
 template <int D, int kBM>
 struct Tiles {

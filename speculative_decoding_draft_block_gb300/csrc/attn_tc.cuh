@@ -191,7 +191,9 @@ enum : int { kSolo, kPairs, kFew };  // forms
 // Key tiles, shares of the work list and rows of partial results of a form.
 template <int kForm, bool kTree>
 struct Form : WorkForm<kTile, kForm == kPairs ? kMaxAttnCtas : 2 * kMaxAttnCtas,
-                       kForm == kPairs ? 2 * kTile : kForm == kFew ? kFewRows : kTile, kTree> {};
+                       kForm == kPairs ? 2 * kTile : kForm == kFew ? kFewRows : kTile, kTree> {
+  static_assert(counts_in_32_bits(kMaxTableTokens, kTile, Form::kCost, kMaxKvHeads), "work_fits");
+};
 
 // Bounded waits. One that gives up sets the abort flag, which ends every role's
 // loop; the status is reported once, at the kernel's end (the waits are many and

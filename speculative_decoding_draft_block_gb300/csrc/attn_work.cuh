@@ -22,7 +22,6 @@ namespace {
 template <int kTileKeys, int kShareCount, int kPartialRows, bool kTrees = false, int kUnitCost = kAttnUnitCost>
 struct WorkForm {
   static constexpr int kCost = kUnitCost;          // of a unit's set-up, in key tiles
-  static_assert(kUnitCost <= kAttnUnitCostMost, "work_fits");
   static constexpr bool kTree = kTrees;            // whether the rows may be a tree's nodes
   static constexpr int kKeys = kTileKeys;          // keys of a tile
   static constexpr int kShares = kShareCount;

@@ -223,7 +223,7 @@ ds_status check_pool(const ds_kv_pool& a, int32_t layer, const uint8_t* scales, 
       layer >= a.n_layers)
     return DS_ERR_INVALID_ARG;
   if (a.page_size < 16 || a.page_size > 256 || (a.page_size & (a.page_size - 1)) != 0) return DS_ERR_INVALID_ARG;
-  if (a.n_kv_heads < 1 || a.n_kv_heads > 256) return DS_ERR_INVALID_ARG;
+  if (a.n_kv_heads < 1 || a.n_kv_heads > kMaxKvHeads) return DS_ERR_INVALID_ARG;
   if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % (scales != nullptr ? 16 : 8) != 0) return DS_ERR_INVALID_ARG;
   if (!aligned(a.k, 16) || !aligned(a.v, 16)) return DS_ERR_INVALID_ARG;
   if (!strides16({a.page_stride, a.token_stride, a.head_stride}, a.dtype)) return DS_ERR_INVALID_ARG;
@@ -249,7 +249,7 @@ ds_status check_pool(const ds_kv_pool& a, int32_t layer, const uint8_t* scales, 
 
 // Requests, rows and table of a call over ragged rows. Positions are 32-bit.
 bool rows_ok(int32_t B, int32_t T, int32_t max_pages, int32_t page_size) {
-  return B >= 1 && B <= 65535 && T >= 0 && T <= (1 << 23) && max_pages >= 1 && (int64_t)max_pages * page_size <= (1 << 30);
+  return B >= 1 && B <= 65535 && T >= 0 && T <= (1 << 23) && max_pages >= 1 && (int64_t)max_pages * page_size <= kMaxTableTokens;
 }
 
 // Words of a tree's masks for requests of up to max_q tokens.

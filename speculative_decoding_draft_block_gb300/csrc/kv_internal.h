@@ -182,15 +182,22 @@ struct Readiness {
 };
 
 // The attention's key tiles, and the set-up of a unit of its work in tiles (0, 2 and 3
-// are slower where units of a few tiles stand beside longer ones), the most of any form.
-constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1, kAttnUnitCostMost = 4;
+// are slower where units of a few tiles stand beside longer ones; a form may have its own).
+constexpr int kAttnTileTc = 128, kAttnTileF32 = 64, kAttnUnitCost = 1;
 
-// Whether the work of one block of rows, over all KV heads, can be counted in 32 bits: with
-// tiles of 128 keys always (2^23 + 1 tiles, 256 heads), with tiles of 64 except for 256
-// heads over 2^30 tokens.
+constexpr int64_t kMaxTableTokens = 1 << 30;  // of a request's table
+constexpr int kMaxKvHeads = 256;
+
+// Whether the work of one block of rows over all heads, in tiles of `tile` keys and `cost` tiles a head
+// for its set-up, can be counted in 32 bits.
+constexpr bool counts_in_32_bits(int64_t tokens, int tile, int cost, int heads) {
+  return ((tokens + tile - 1) / tile + cost) * heads <= (int64_t)UINT32_MAX;
+}
+
+// The same for the form that a pool's dtype leads to. Forms with tiles of 128 keys over all heads of a group
+// count any call (each says so where it is defined), float32's tiles of 64 all but 256 heads over 2^30 tokens.
 inline bool work_fits(int32_t dtype, int64_t tokens, int32_t n_kv_heads) {
-  const int64_t tile = dtype == DS_F32 ? kAttnTileF32 : kAttnTileTc;
-  return ((tokens + tile - 1) / tile + kAttnUnitCost) * n_kv_heads <= (int64_t)UINT32_MAX;
+  return dtype != DS_F32 || counts_in_32_bits(tokens, kAttnTileF32, kAttnUnitCost, n_kv_heads);
 }
 
 constexpr int kMaxTree = 4096;     // nodes of a tree whose masks are made, entries of a path

@@ -63,6 +63,15 @@ def test_quantised_calls_on_the_host(kv):
         assert getattr(lib, name.replace("_scaled", "").replace("_tree", ""))(ctypes.byref(make(kv, pool)), None) == INVALID
 
 
+@pytest.mark.parametrize("heads,group", [(256, 1), (255, 2), (254, 16), (256, 128)])
+@pytest.mark.parametrize("max_q", [1, 300])
+def test_the_longest_tables_of_many_heads_are_taken(kv, heads, group, max_q):
+    """The work over a quantised pool is counted in 32 bits for any table and number of heads."""
+    pool = _pool(kv, dtype=E4M3, n_kv_heads=heads, token_stride=heads * 128, page_stride=heads * 128 * 16)
+    args = _attend(kv, pool, T=0, n_heads=heads * group, max_q=max_q, max_pages=(1 << 30) // pool.page_size)
+    assert _call(kv, "ds_paged_attention_tree", args) == 0
+
+
 @pytest.mark.parametrize("bad,args", [(dict(mask=None), {}), (dict(mask=FAKE + 2), {}), (dict(depth=FAKE + 1), {}), (dict(mask_words=0), {}),
                                       (dict(mask_words=(1 << 18) + 1), {}), (dict(mask_words=1), dict(max_q=33, T=40)), ({}, dict(causal=0))], ids=str)
 def test_bad_trees_are_refused(kv, bad, args):
