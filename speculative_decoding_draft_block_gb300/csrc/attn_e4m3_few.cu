@@ -227,13 +227,15 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
     const int64_t scale_part = (int64_t)hd.n_kv_heads << shift;
     constexpr int kNoPage = INT32_MIN;
     const int32_t* table = nullptr;
-    int n = 0, tile0 = 0, lo = 0, hi = 0, head = 0, page = kNoPage, j = 0;
+    int n = 0, tile0 = 0, lo = 0, hi = 0, head = 0, page = 0, j = 0;
+    bool seen = false;
     uint32_t np = 0;
-    // Table entry of this lane's page of a tile (any below 0 as -1), kNoPage: no row sees it.
-    auto page_of = [&](int tile) {
+    // Whether a row sees this lane's page of a tile, and its table entry, which is looked at when
+    // the tile is loaded only.
+    auto find_page = [&](int tile) {
       const int key = tile * kKeys + lane * rows;
-      if (lane >= boxes || key >= hi || key + rows <= lo) return kNoPage;
-      return max(__ldcg(table + (key >> shift)), -1);
+      seen = lane < boxes && key < hi && key + rows > lo;
+      if (seen) page = __ldcg(table + (key >> shift));
     };
     // the next piece with tiles (n < 0: there is none), and its first page
     auto next_piece = [&] {
@@ -252,12 +254,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
         ++np;
       } while (n == 0);
       j = 0;
-      if (n > 0) page = page_of(tile0);
+      if (n > 0) find_page(tile0);
       return true;
     };
     bool ok = next_piece();
     while (ok && n > 0) {
-      int now = page;
+      int now = seen ? max(page, -1) : kNoPage;  // (an entry may be any number)
       const int token = ((tile0 + j) * kKeys) & (page_size - 1), now_head = head;
       if (now != kNoPage && (now < 0 || now >= p.pool.n_pages)) {
         report(p.status, kErrBounds);
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 2), 2)
       const uint32_t some = __ballot_sync(0xffffffffu, now != kNoPage);
       // (the next tile's page is on its way before the wait for a place for this one)
       const bool last = ++j == n;
-      if (!last) page = page_of(tile0 + j);
+      if (!last) find_page(tile0 + j);
       ok = wait_warp(&sh.empty[stage], parity ^ 1, abort);
       if (!ok) break;
       if (lane == 0) mbar_expect_tx(&sh.full[stage], __popc(some) * 2 * KH * rows * (D + 1));

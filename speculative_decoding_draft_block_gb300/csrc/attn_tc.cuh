@@ -431,15 +431,16 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
       Piece x = {};
       int j = 0;                                           // next tile of the piece
       const int32_t* table = nullptr;
-      // Table entry of this lane's box of a key tile, kNoPage: no row of the unit sees
-      // it, -1 any that is below 0. (Looked at when the tile is loaded, a tile later as a rule.)
+      // Whether a row of the unit sees this lane's box of a key tile, and its table entry.
+      // (Looked at when the tile is loaded, a tile later as a rule.)
       constexpr int kNoPage = INT32_MIN;
-      auto page_of = [&](int tile) {
+      bool seen = false;                                   // of the next tile
+      int page = 0;
+      auto find_page = [&](int tile) {
         const int key = tile * kTile + lane * rows;
-        if (lane >= boxes || key >= x.hi || key + rows <= x.lo) return kNoPage;
-        return max(__ldcg(table + (key >> shift)), -1);
+        seen = lane < boxes && key < x.hi && key + rows > x.lo;
+        if (seen) page = __ldcg(table + (key >> shift));
       };
-      int page = kNoPage;                                  // of the next tile
       volatile int* ends = sh.ended;
       while (true) {
         if (!ended && j == x.n) {  // the next piece
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
           // its first tile's page is on its way while it goes to the softmax
           if (x.n > 0) {
             table = p.block_table + (int64_t)x.b * p.max_pages;
-            page = page_of(x.tile0);
+            find_page(x.tile0);
           }
           if (does_k) {
             const uint32_t i = np % kAhead;
@@ -492,8 +493,8 @@ __global__ void __launch_bounds__(Split<kQuant>::kThreads, 1)
         int now = kNoPage;
         uint32_t word = 0;
         if (!ended) {
-          now = page;
-          if (j + 1 < x.n) page = page_of(tile + 1);
+          now = seen ? max(page, -1) : kNoPage;  // (an entry may be any number)
+          if (j + 1 < x.n) find_page(tile + 1);
           word = (x.rows > tile_rows ? kTwo : 0u) | (j == 0 ? kFirst : 0u) | (j + 1 == x.n ? kLast : 0u);
           if (F::partly_seen(tile, x.lo, x.hi))
             word |= kPart | (uint32_t)max(0, x.lo - tile * kTile) << 8 | (uint32_t)min(kTile, x.hi - tile * kTile) << 16;
