@@ -76,7 +76,7 @@
 // beside the softmax (four instructions a pair of codes; with five, prompts took 20 us and blocks of 8
 // tokens 20 us more), and shared memory moves 1 + 2 + 2 bytes a code (restoring reads and writes, the product
 // reads). 2 prompt chunks of 1777 to 2048 tokens over 9001 to 16384 cached 577 to 582 us (1.24 PFLOP/s),
-// bfloat16 466; 128 trees of 8 to 60 tokens over 500 to 6000 cached 285, bfloat16 245; 128 blocks of
+// bfloat16 466; 128 trees of 8 to 60 tokens over 500 to 6000 cached 274 to 285, bfloat16 247; 128 blocks of
 // 8 tokens over 300 to 8000 cached 206, bfloat16 208.
 #pragma once
 #include <cuda.h>
@@ -1449,8 +1449,9 @@ cudaError_t launch_form(const AttnParams& p, cudaStream_t s) {
   const int per_tile = kTile / p.group;
   // Trees, whose masks cost the softmax more: from three quarters of a row tile on average. 128
   // trees that fill 0.81 of one, 500 to 6000 cached: pair 247 us, solo 267 (codes 292 and 307); 0.62
-  // to 0.73 of one: 238 to 244 and 237 to 254 (280 to 289 and 258 to 283). (Codes without masks, 0.72
-  // and 0.81: 303 and 307, 283 and 301.)
+  // to 0.73 of one: 238 to 244 and 237 to 254 (280 to 289 and 258 to 283). Without masks, 128 requests over
+  // 500 to 6000 cached, at 0.62, 0.76, 0.81 and 0.91 of a tile: codes pair 269, 273, 283 and 279 us, solo 232, 260,
+  // 275 and 282; bfloat16 pair 229, 232, 239 and 236, solo 233, 255, 266 and 279 (the rule takes solo for both).
   const int64_t tiles4 = p.mask != nullptr ? 3 : 4;
   const bool pair = p.max_q > per_tile && 4 * (int64_t)p.T > tiles4 * p.B * per_tile;
   if constexpr (kQuant) {

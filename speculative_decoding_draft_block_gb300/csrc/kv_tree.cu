@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreePara
 // order. A thread takes 16 bytes of a head's row of K or V of one layer (or its scale) and
 // all rows of the path, kFlight at a time: no two threads share bytes. 2 * 2 * moved rows'
 // bytes; rows that stand in their place already are left there. Bound by memory, in pieces of
-// a head's row (128 trees of 8 to 60 nodes, 32 layers of 8 heads, 138 MB: 23.7 us, 5.8 TB/s),
+// a head's row (128 trees of 8 to 60 nodes, 32 layers of 8 heads, 138 MB: 23.7 to 26.3 us, 5.2 to 5.8 TB/s),
 // of few rows by the launch and the chain path, table, row (3.0 us of their own).
 constexpr int kKeepThreads = 256;
 constexpr int kFlight = 8;
@@ -180,7 +180,7 @@ cudaError_t launch_keep(const KeepParams& p, cudaStream_t s) {
   const int64_t rows = (int64_t)2 * p.pool.n_layers * p.pool.n_kv_heads;
   const int64_t items = rows * (p.pool.row_bytes >> 4) + (p.pool.scales != nullptr ? rows : 0);
   // Two waves of four blocks an SM at most, since a block begins with a chain of five loads: 23.7 us, one
-  // wave 25.1, a thread for each piece of a row 28.1; bfloat16 rows 43.6, 47.8 and 49.1.
+  // wave 25.1, a thread for each piece of a row 28.1 in one run; bfloat16 rows 43.6, 47.8 and 49.1.
   const int64_t most = (items + kKeepThreads - 1) / kKeepThreads, waves = (8 * kMaxAttnCtas + p.B - 1) / p.B;
   const int64_t blocks = most < waves ? most : waves;
   return launch_early(keep_kernel, dim3((unsigned)blocks, p.B), dim3(kKeepThreads), 0, s, p);
